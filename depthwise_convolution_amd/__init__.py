@@ -18,6 +18,10 @@ reduction).  ``fwd``, ``input_grad`` and
 ``weight_grad`` are the same calls with the outputs (and the workspace)
 allocated here; given ``pads`` or ``mult`` they use the general forms.
 
+The sequence operators (causal depthwise convolution over tokens, gated
+linear recurrence, matrix product with epilogue) are in ``sequence`` and
+exported here.
+
 Tensor shapes: NHWC tensors are ``(N, H, W, C)``, NCHW tensors
 ``(N, C, H, W)``; weights ``(mult*C, kH, kW)`` float32 or float16; bias
 ``(mult*C,)``; ``pads`` is ``(top, bottom, left, right)``.
@@ -25,6 +29,9 @@ Tensor shapes: NHWC tensors are ``(N, H, W, C)``, NCHW tensors
 import ctypes
 import functools
 import os
+
+from . import sequence
+from .sequence import *  # noqa: F401,F403  (the operators of include/dwconv_seq.h)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdwconv.so")
 
@@ -40,7 +47,7 @@ STATUS = {
     0: "OK", -1: "NULL_PTR", -2: "BAD_DIM", -3: "BAD_STRIDE", -4: "BAD_DILATION",
     -5: "EVEN_KERNEL", -6: "BAD_LAYOUT", -7: "BAD_WTYPE", -8: "ALIAS", -9: "MISALIGNED",
     -10: "LAUNCH", -11: "BAD_OP", -12: "BAD_STRATEGY", -13: "WORKSPACE", -14: "BAD_PAD",
-    -15: "BAD_EPILOGUE", -16: "SCRATCH",
+    -15: "BAD_EPILOGUE", -16: "SCRATCH", -17: "ROW_STRIDE",
 }
 SCRATCH_BYTES = 16 << 20     # DWCONV_SCRATCH_BYTES
 EXPORTS = ("dwconv2d_fwd", "dwconv2d_input_grad", "dwconv2d_launch", "dwconv2d_describe",
@@ -108,6 +115,7 @@ def lib():
     for f in EXPORTS:
         if f != "dwconv2d_strerror":
             getattr(L, f).restype = i
+    sequence.declare(L)
     _lib = L
     return L
 

@@ -10,9 +10,10 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdwconv.so")
-HOST_SOURCES = ["dwconv_api.cpp", "dwconv_plan.cpp"]
+HOST_SOURCES = ["dwconv_api.cpp", "dwconv_plan.cpp", "dwseq_api.cpp"]
 HIP_SOURCES = ["dwconv_direct.hip", "dwconv_tiled_nhwc.hip", "dwconv_tiled_nchw.hip",
-               "dwconv_wgrad.hip", "dwconv_launch.hip", "dwconv_stream.hip"]
+               "dwconv_wgrad.hip", "dwconv_launch.hip", "dwconv_stream.hip",
+               "dwseq_conv.hip", "dwseq_scan.hip", "dwseq_linear.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -83,7 +84,8 @@ def resource_usage():
     names = [n.replace("DF16_", "Dh") for n in out]
     dem = subprocess.run(["c++filt"], input="\n".join(names), capture_output=True, text=True,
                          check=True).stdout.split("\n")
-    return {d.replace("dwconv::(anonymous namespace)::", "").replace("half", "_Float16"): v
+    return {d.replace("dwconv::(anonymous namespace)::", "")
+            .replace("dwseq::(anonymous namespace)::", "").replace("half", "_Float16"): v
             for d, v in zip(dem, out.values())}
 
 

@@ -461,6 +461,7 @@ const char *dwconv2d_strerror(int status)
     case DWCONV_ERR_BAD_PAD: return "pad out of range (|pad| >= 65536) or unknown padding mode";
     case DWCONV_ERR_BAD_EPILOGUE:
         return "bad epilogue: unknown activation, partial BatchNorm, bad eps or learning rate";
+    case DWCONV_ERR_ROW_STRIDE: return "row stride smaller than the row (or not addressable)";
     case DWCONV_ERR_SCRATCH:
         return "allocation-free weight gradient: needs more than the library's 16 MiB scratch "
                "array, or the stream is not on the current device";

@@ -1,0 +1,143 @@
+// dwseq_device.h -- what the kernel files of the sequence operators share:
+// element types and vectors, activations and their slopes, the lookup of a
+// row's sequence, and the fixed-order sum of partial rows.
+#pragma once
+
+#include "dwconv_device.h"
+#include "dwseq_internal.h"
+#include "../../include/dwconv_seq.h"
+
+namespace dwseq {
+namespace {
+
+typedef _Float16 f16;
+typedef __bf16 bf16;
+
+// V elements that need only their own type's alignment: the global loads and
+// stores of gfx950 take a vector at any element's address (rows of odd width,
+// column ranges), so one kernel serves every alignment.
+template <typename T, int V> struct __attribute__((packed, aligned(sizeof(T)))) Pack { T v[V]; };
+
+// V elements as float32 (one vector load), and back (rounded to nearest even)
+template <typename T, int V>
+__device__ __forceinline__ void load(const T *p, float (&f)[V])
+{
+    const Pack<T, V> t = *reinterpret_cast<const Pack<T, V> *>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        f[i] = (float)t.v[i];
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store(T *p, const float (&f)[V])
+{
+    Pack<T, V> t;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        t.v[i] = (T)f[i];
+    *reinterpret_cast<Pack<T, V> *>(p) = t;
+}
+
+// 1 / (1 + e^-v) with the hardware's exponential and reciprocal (one unit in
+// the last place each); 0 and 1 at the infinities
+__device__ __forceinline__ float logistic(float v)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+}
+
+// log(1 + e^v), without overflow and exact for very negative v
+__device__ __forceinline__ float softplus(float v)
+{
+    return v > 20.0f ? v : log1pf(expf(v));
+}
+
+// NaN passes through every activation.
+__device__ __forceinline__ float act_of(float z, int act)
+{
+    if (act == DWCONV_ACT_SILU)
+        return z * logistic(z);
+    if (act == DWCONV_ACT_RELU)
+        return z < 0.0f ? 0.0f : z;
+    if (act == DWCONV_ACT_RELU6)
+        return z < 0.0f ? 0.0f : (z > 6.0f ? 6.0f : z);
+    return z;
+}
+
+__device__ __forceinline__ float act_slope(float z, int act)
+{
+    if (act == DWCONV_ACT_SILU) {
+        const float p = logistic(z);
+        return p * (1.0f + z * (1.0f - p));
+    }
+    if (act == DWCONV_ACT_RELU)
+        return z > 0.0f ? 1.0f : 0.0f;
+    if (act == DWCONV_ACT_RELU6)
+        return z > 0.0f && z < 6.0f ? 1.0f : 0.0f;
+    return 1.0f;
+}
+
+// First row of sequence s (s = seqs: the end).  Offsets are clamped to the
+// rows there are, and the outer two are taken as given by the batch.
+__device__ __forceinline__ int seq_start(const Batch &b, int s)
+{
+    if (s <= 0)
+        return 0;
+    if (s >= b.seqs)
+        return b.rows;
+    return b.off ? min(max(b.off[s], 0), b.rows) : s * b.tokens;
+}
+
+// The last sequence that starts at or before `row`.
+__device__ __forceinline__ int seq_of(const Batch &b, int row)
+{
+    if (!b.off)
+        return min(row / max(b.tokens, 1), b.seqs - 1);
+    int lo = 0, hi = b.seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seq_start(b, mid) <= row)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Sum of the rows of part[rows][n] per column in a fixed order: a workgroup
+// takes 64 columns, its 16 waves every 16th row each, added up in LDS.  The
+// sums go to f(column, sum).
+template <typename F>
+__device__ __forceinline__ void column_sums(const float *part, int rows, long long n, F f)
+{
+    __shared__ float lds[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long long col = (long long)blockIdx.x * 64 + lane;
+    float s = 0.0f;
+    if (col < n)
+#pragma unroll 4
+        for (int k = wave; k < rows; k += 16)
+            s += part[(long long)k * n + col];
+    lds[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < n) {
+#pragma unroll
+        for (int k = 1; k < 16; ++k)
+            s += lds[k][lane];
+        f(col, s);
+    }
+}
+
+// f(std::integral_constant<type>) with the element type of `type`
+template <typename F>
+inline int with_type(int type, F f)
+{
+    switch (type) {
+    case DWCONV_T_F32: return f((float *)nullptr);
+    case DWCONV_T_F16: return f((f16 *)nullptr);
+    case DWCONV_T_BF16: return f((bf16 *)nullptr);
+    }
+    return DWCONV_ERR_BAD_WTYPE;
+}
+
+}  // namespace
+}  // namespace dwseq

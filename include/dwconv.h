@@ -68,6 +68,7 @@ extern "C" {
 #define DWCONV_ERR_SCRATCH     -16  /* allocation-free weight gradient: the problem needs more
                                        than the library's scratch array holds, or the stream
                                        is not on the current device                   */
+#define DWCONV_ERR_ROW_STRIDE  -17  /* sequence operators: a row stride smaller than the row */
 
 /* ---- enumerations (passed as int) -------------------------------------- */
 #define DWCONV_LAYOUT_NHWC 0   /* channel innermost (the ggml page's CWHN)    */
