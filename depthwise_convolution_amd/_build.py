@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libdwconv.so")
 HOST_SOURCES = ["dwconv_api.cpp", "dwconv_plan.cpp", "dwseq_api.cpp"]
 HIP_SOURCES = ["dwconv_direct.hip", "dwconv_tiled_nhwc.hip", "dwconv_tiled_nchw.hip",
                "dwconv_wgrad.hip", "dwconv_launch.hip", "dwconv_stream.hip",
-               "dwseq_conv.hip", "dwseq_scan.hip", "dwseq_linear.hip"]
+               "dwseq_conv.hip", "dwseq_scan.hip", "dwseq_linear.hip",
+               "dwseq_gemm_f32.hip", "dwseq_gemm_f16.hip", "dwseq_gemm_bf16.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1,97 +1,65 @@
 // dwseq_linear.hip -- matrix product with bias, activation and residual, and
 // its gradients (include/dwconv_seq.h).
-#include "dwseq_device.h"
+#include "dwseq_gemm.h"
 
 namespace dwseq {
 namespace {
 
-// What happens to a sum on its way to memory.
-struct Finish {
-    const float *b;             // per column, or nullptr
-    const void *res;            // nullptr: none
-    void *z, *y;                // z nullptr: not kept
-    long long ldres, ldz, ldy;
-    int act;
+// dz = dy * act'(z), and its column sums over a strip of rows (db): a workgroup
+// takes 32 vectors of V columns, its 8 rows of threads every 8th row of the
+// strip each.  Bound by HBM.
+constexpr int kDzLanes = 32, kDzSlots = 8;
+
+struct DzPlan {
+    int strip, strips;      // rows, and how many of them: 1024 at most
 };
 
-template <typename T>
-__device__ __forceinline__ void finish(const Finish &f, long long m, int n, float s)
+DzPlan dz_plan(int M)
 {
-    if (f.b)
-        s += f.b[n];
-    if (f.z)
-        static_cast<T *>(f.z)[m * f.ldz + n] = (T)s;
-    s = act_of(s, f.act);
-    if (f.res)
-        s += (float)static_cast<const T *>(f.res)[m * f.ldres + n];
-    static_cast<T *>(f.y)[m * f.ldy + n] = (T)s;
+    int strip = 64;
+    while (cdiv(M, strip) > 1024)
+        strip *= 2;
+    return {strip, (int)cdiv(M, strip)};
 }
 
-// y[m,n] = sum_k A[m,k] B[n,k] by strides: a workgroup's 64 x 64 tile, 16 k at
-// a time through LDS, 4 x 4 sums a thread.
-template <typename T>
-__global__ __launch_bounds__(256) void k_product(const T *A, long long am, long long ak,
-                                                 const T *B, long long bn, long long bk, int M,
-                                                 int N, int K, Finish f)
+template <typename T, int V>
+__global__ __launch_bounds__(kDzLanes *kDzSlots) void k_dz(LinearArgs a, T *dz, float *part,
+                                                           int strip)
 {
-    __shared__ float sa[16][65], sb[16][65];
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    const long long tiles_n = (N + 63) / 64;
-    const int m0 = (int)(blockIdx.x / tiles_n) * 64, n0 = (int)(blockIdx.x % tiles_n) * 64;
-    float s[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        for (int e = tid; e < 1024; e += 256) {
-            const int row = ak == 1 ? e / 16 : e % 64, k = ak == 1 ? e % 16 : e / 64;
-            sa[k][row] = m0 + row < M && k0 + k < K
-                             ? (float)A[(m0 + row) * am + (long long)(k0 + k) * ak]
-                             : 0.0f;
+    __shared__ float lds[kDzSlots][kDzLanes * V];
+    const int lane = threadIdx.x % kDzLanes, slot = threadIdx.x / kDzLanes;
+    const int at = (blockIdx.x * kDzLanes + lane) * V;
+    const bool mine = at < a.N;
+    const int n = min(at, a.N - V);      // the last vector ends with the row
+    const int m0 = (int)blockIdx.y * strip, m1 = m0 + min(strip, a.M - m0);
+    float s[V] = {};
+    if (mine)
+#pragma unroll 4
+        for (int m = m0 + slot; m < m1; m += kDzSlots) {
+            float d[V], z[V];
+            load<T, V>(static_cast<const T *>(a.dy) + m * a.lddy + n, d);
+            if (a.act != DWCONV_ACT_NONE) {
+                load<T, V>(static_cast<const T *>(a.z_in) + m * a.ldz + n, z);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    d[v] *= act_slope(z[v], a.act);
+                store<T, V>(dz + (long long)m * a.N + n, d);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                s[v] += d[v];
         }
-        for (int e = tid; e < 1024; e += 256) {
-            const int row = bk == 1 ? e / 16 : e % 64, k = bk == 1 ? e % 16 : e / 64;
-            sb[k][row] = n0 + row < N && k0 + k < K
-                             ? (float)B[(n0 + row) * bn + (long long)(k0 + k) * bk]
-                             : 0.0f;
-        }
-        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], s[i][j]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < M && n < N)
-                finish<T>(f, m, n, s[i][j]);
-        }
-}
-
-// dz = dy * act'(z), and its column sums over a strip of rows (db).
-constexpr int kStrip = 64;      // rows
-
-template <typename T>
-__global__ __launch_bounds__(256) void k_dz(LinearArgs a, T *dz, float *part)
-{
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N)
+    for (int v = 0; v < V; ++v)
+        lds[slot][lane * V + v] = s[v];
+    __syncthreads();
+    if (slot != 0 || !mine)
         return;
-    const int m0 = (int)blockIdx.y * kStrip, m1 = min(m0 + kStrip, a.M);
-    float s = 0.0f;
-    for (int m = m0; m < m1; ++m) {
-        float d = (float)static_cast<const T *>(a.dy)[m * a.lddy + n];
-        if (a.act != DWCONV_ACT_NONE) {
-            d *= act_slope((float)static_cast<const T *>(a.z_in)[m * a.ldz + n], a.act);
-            dz[(long long)m * a.N + n] = (T)d;
-        }
-        s += d;
-    }
-    part[(long long)blockIdx.y * a.N + n] = s;
+    for (int k = 1; k < kDzSlots; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            s[v] += lds[k][lane * V + v];
+    store<float, V>(part + (long long)blockIdx.y * a.N + n, s);
 }
 
 __global__ __launch_bounds__(1024) void k_db(const float *part, int rows, int N, float *db)
@@ -99,36 +67,129 @@ __global__ __launch_bounds__(1024) void k_db(const float *part, int rows, int N,
     column_sums(part, rows, N, [=](long long n, float s) { db[n] = s; });
 }
 
-template <typename T>
-int product(const T *A, long long am, long long ak, const T *B, long long bn, long long bk, int M,
-            int N, int K, const Finish &f, hipStream_t st)
+struct GemmPlan {
+    GemmTile tile;
+    int splits;
+};
+
+// Which kernel, and over how many ranges of k, by the time that a product
+// should take (microseconds): rounds of the chip times (steps of k times a
+// step's time, plus a tile's beginning and end).  A step's time grows from that
+// of a workgroup alone on its CU to that of a full CU; both are measured (at K
+// of 2048 to 8192), as is the sum of the splits' results.
+//
+//   tile   workgroups a CU   16 bits: alone, full, ends   32 bits
+//   256          1             1.05    1.46  12             -
+//   128          2             0.88    1.13   6            2.3   4.1   6
+//    64          5             0.50    0.92   4            0.75  2.65  4
+//    64 deep     2             0.35    0.75   4             -
+//
+// Few rows of operands that are both read along k (`straight`) go to the kernel
+// that reads Q once: measured against
+// the 64 tile with 4 splits it is ahead while M / 16 * K is at most 4096 (at
+// 32 x 4096 x 4096: 14.8 against 13.2 us; at 16 x 4096 x 2048: 6.7 against 9.4).
+GemmPlan gemm_plan(int size, bool straight, int M, int N, int K)
 {
-    const long long blocks = cdiv(M, 64) * cdiv(N, 64);
-    if (blocks == 0)
+    if (straight && (M <= 16 || (M <= kFewRows && cdiv(M, 16) * K <= 4096)))
+        return {FEW_ROWS, 1};
+    struct Shape {
+        GemmTile tile;
+        int rows, per_cu;
+        double alone, full, ends;
+    };
+    static const Shape wide[] = {{TILE_256, 256, 1, 1.05, 1.46, 12.0},
+                                 {TILE_128, 128, 2, 0.88, 1.13, 6.0},
+                                 {TILE_64, 64, 5, 0.50, 0.92, 4.0},
+                                 {TILE_64_DEEP, 64, 2, 0.35, 0.75, 4.0}};
+    static const Shape narrow[] = {{TILE_128, 128, 2, 2.3, 4.1, 6.0},
+                                   {TILE_64, 64, 5, 0.75, 2.65, 4.0}};
+    const Shape *shapes = size == 2 ? wide : narrow;
+    const int count = size == 2 ? 4 : 2, cus = 256;
+    const long long steps = cdiv((long long)K * size, kStepBytes);
+    GemmPlan best{TILE_64, 1};
+    double least = 1e30;
+    for (int t = 0; t < count; ++t)
+        for (int splits = 1; splits <= 16; splits *= 2) {
+            const Shape &s = shapes[t];
+            const double sums = 4.0 * M * N * splits;       // bytes of partial sums
+            if (splits > 1 && (steps < 4 * splits || sums > 64e6))
+                break;
+            const double groups = (double)cdiv(M, s.rows) * cdiv(N, s.rows) * splits;
+            const double on_cu = groups / cus < s.per_cu ? groups / cus : s.per_cu;
+            const double step = on_cu <= 1.0 ? s.alone
+                                             : s.alone + (s.full - s.alone) * (on_cu - 1.0) /
+                                                             (s.per_cu > 1 ? s.per_cu - 1.0 : 1.0);
+            const double full = s.per_cu > 1 ? step : (groups > 128 ? s.full : s.alone);
+            const double rounds = (double)cdiv((long long)groups, (long long)cus * s.per_cu);
+            double time = rounds * (cdiv(steps, splits) * full + s.ends);
+            if (splits > 1)
+                time += 3.0 + sums * 2.0 / 4e6;
+            if (time < least) {
+                least = time;
+                best = {s.tile, splits};
+            }
+        }
+    return best;
+}
+
+// Bytes of a product's partial sums.
+long long gemm_workspace(int size, bool straight, int M, int N, int K)
+{
+    const GemmPlan p = gemm_plan(size, straight, M, N, K);
+    return p.splits > 1 ? 4LL * M * N * p.splits : 0;
+}
+
+template <typename T>
+int product(const T *P, long long ldp, bool p_rows_k, const T *Q, long long ldq, bool q_rows_k,
+            int M, int N, int K, Finish f, void *partials, hipStream_t st)
+{
+    if (M == 0 || N == 0)
         return DWCONV_OK;
-    if (blocks > 0x7fffffffLL)
-        return DWCONV_ERR_BAD_DIM;
-    return dwconv::launch_kernel(k_product<T>, dim3((unsigned)blocks), dim3(256), 0, st, A, am, ak,
-                                 B, bn, bk, M, N, K, f);
+    const GemmPlan plan = gemm_plan((int)sizeof(T), !p_rows_k && !q_rows_k, M, N, K);
+    f.part = static_cast<float *>(partials);
+    return launch_gemm<T>(Product{P, Q, ldp, ldq, p_rows_k, q_rows_k, M, N, K, plan.tile,
+                                  plan.splits, f},
+                          st);
 }
 
 }  // namespace
 
-long long linear_workspace(bool grad, int type, int act, int M, int N, int)
+// The parts of a gradient's workspace: dz, the partial sums of db, and those of
+// a product (dx's and dw's one after the other in the same place).
+struct GradSpace {
+    long long dz, db, sums;
+};
+
+static GradSpace grad_space(int type, int act, int M, int N, int K)
 {
-    if (!grad)
+    const int size = elem_size(type);
+    GradSpace g;
+    g.dz = act == DWCONV_ACT_NONE ? 0 : cdiv((long long)M * N * size, 16) * 16;
+    g.db = cdiv(4LL * dz_plan(M).strips * N, 16) * 16;
+    const long long dx = gemm_workspace(size, false, M, K, N),
+                    dw = gemm_workspace(size, false, N, K, M);
+    g.sums = dx > dw ? dx : dw;
+    return g;
+}
+
+long long linear_workspace(bool grad, int type, int act, int M, int N, int K)
+{
+    if (M == 0)
         return 0;
-    const long long dz = act == DWCONV_ACT_NONE ? 0 : (long long)M * N * elem_size(type);
-    return (dz + 15) / 16 * 16 + 4LL * cdiv(M, kStrip) * N;
+    if (!grad)
+        return gemm_workspace(elem_size(type), true, M, N, K);
+    const GradSpace g = grad_space(type, act, M, N, K);
+    return g.dz + g.db + g.sums;
 }
 
 int launch_linear_fwd(const LinearArgs &a, void *stream)
 {
     return with_type(a.type, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        const Finish f{a.b, a.res, a.z, a.y, a.ldres, a.ldz, a.ldy, a.act};
-        return product<T>(static_cast<const T *>(a.x), a.ldx, 1, static_cast<const T *>(a.w),
-                          a.ldw, 1, a.M, a.N, a.K, f, static_cast<hipStream_t>(stream));
+        const Finish f{a.b, a.res, a.z, a.y, a.ldres, a.ldz, a.ldy, a.act, nullptr};
+        return product<T>(static_cast<const T *>(a.x), a.ldx, false, static_cast<const T *>(a.w),
+                          a.ldw, false, a.M, a.N, a.K, f, a.workspace,
+                          static_cast<hipStream_t>(stream));
     });
 }
 
@@ -138,29 +199,37 @@ int launch_linear_grad(const LinearArgs &a, void *stream)
     return with_type(a.type, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
         const bool plain = a.act == DWCONV_ACT_NONE;
-        T *dz = static_cast<T *>(a.workspace);
-        const long long dz_bytes =
-            plain ? 0 : ((long long)a.M * a.N * (long long)sizeof(T) + 15) / 16 * 16;
-        float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + dz_bytes);
+        const GradSpace g = grad_space(a.type, a.act, a.M, a.N, a.K);
+        char *space = static_cast<char *>(a.workspace);
+        T *dz = reinterpret_cast<T *>(space);
+        float *part = reinterpret_cast<float *>(space + g.dz);
+        void *sums = space + g.dz + g.db;
         int rc = DWCONV_OK;
-        const int strips = (int)cdiv(a.M, kStrip);
-        if (strips > 0 && (!plain || a.db))
-            rc = dwconv::launch_kernel(k_dz<T>, dim3((unsigned)cdiv(a.N, 256), (unsigned)strips),
-                                       dim3(256), 0, st, a, dz, part);
+        const DzPlan dp = dz_plan(a.M);
+        auto make_dz = [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            return dwconv::launch_kernel(
+                k_dz<T, V>, dim3((unsigned)cdiv(a.N, kDzLanes * V), (unsigned)dp.strips),
+                dim3(kDzLanes * kDzSlots), 0, st, a, dz, part, dp.strip);
+        };
+        if (dp.strips > 0 && (!plain || a.db))
+            rc = a.N >= 16 / (int)sizeof(T)
+                     ? make_dz(std::integral_constant<int, 16 / (int)sizeof(T)>())
+                     : make_dz(std::integral_constant<int, 1>());
         if (rc == DWCONV_OK && a.db)
             rc = dwconv::launch_kernel(k_db, dim3((unsigned)cdiv(a.N, 64)), dim3(1024), 0, st,
-                                       (const float *)part, strips, a.N, a.db);
+                                       (const float *)part, dp.strips, a.N, a.db);
         const T *d = plain ? static_cast<const T *>(a.dy) : dz;
         const long long ldd = plain ? a.lddy : a.N;
         if (rc == DWCONV_OK && a.dx) {
-            const Finish f{nullptr, nullptr, nullptr, a.dx, 0, 0, a.lddx, DWCONV_ACT_NONE};
-            rc = product<T>(d, ldd, 1, static_cast<const T *>(a.w), 1, a.ldw, a.M, a.K, a.N, f,
-                            st);
+            const Finish f{nullptr, nullptr, nullptr, a.dx, 0, 0, a.lddx, DWCONV_ACT_NONE, nullptr};
+            rc = product<T>(d, ldd, false, static_cast<const T *>(a.w), a.ldw, true, a.M, a.K,
+                            a.N, f, sums, st);
         }
         if (rc == DWCONV_OK && a.dw) {
-            const Finish f{nullptr, nullptr, nullptr, a.dw, 0, 0, a.lddw, DWCONV_ACT_NONE};
-            rc = product<T>(d, 1, ldd, static_cast<const T *>(a.x), 1, a.ldx, a.N, a.K, a.M, f,
-                            st);
+            const Finish f{nullptr, nullptr, nullptr, a.dw, 0, 0, a.lddw, DWCONV_ACT_NONE, nullptr};
+            rc = product<T>(d, ldd, true, static_cast<const T *>(a.x), a.ldx, true, a.N, a.K, a.M,
+                            f, sums, st);
         }
         return rc;
     });
