@@ -121,6 +121,9 @@ int make_batch(int seqs, long long tokens, const int *offsets, bool packed, Batc
 // Row strides may pass 2^31 elements, not the address space.
 bool ld_ok(long long ld, long long width) { return ld >= width && ld < (1LL << 40); }
 
+// The recurrence addresses a run's rows by 32-bit offsets.
+bool scan_ld_ok(long long ld, long long width) { return ld >= width && ld < (1LL << 21); }
+
 int check_workspace(const void *ws, long long have, long long need)
 {
     if (need > 0 && (!ws || !aligned(ws, 16) || have < need))
@@ -296,7 +299,7 @@ int dwconv_scan_fwd(const void *x, long long ldx, const void *r, long long ldr, 
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!ld_ok(ldx, C) || !ld_ok(ldr, C) || !ld_ok(ldi, C) || !ld_ok(ldy, C))
+    if (!scan_ld_ok(ldx, C) || !scan_ld_ok(ldr, C) || !scan_ld_ok(ldi, C) || !scan_ld_ok(ldy, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), rows = a.batch.rows, w = C * e;
     const long long need = scan_workspace(false, a.batch, C, offsets != nullptr);
@@ -317,7 +320,7 @@ int dwconv_scan_fwd(const void *x, long long ldx, const void *r, long long ldr, 
     if (st != DWCONV_OK)
         return st;
     a.x = x; a.r = r; a.i = i; a.lam = lam; a.scale = scale; a.h0 = h0; a.y = y; a.hT = hT;
-    a.states = states; a.agg = static_cast<float *>(workspace);
+    a.states = states; a.workspace = workspace;
     a.ldx = ldx; a.ldr = ldr; a.ldi = ldi; a.ldy = ldy; a.type = type; a.C = C;
     return launch_scan_fwd(a, stream);
 }
@@ -336,7 +339,7 @@ int dwconv_scan_step(const void *x, long long ldx, const void *r, long long ldr,
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!ld_ok(ldx, C) || !ld_ok(ldr, C) || !ld_ok(ldi, C) || !ld_ok(ldy, C))
+    if (!scan_ld_ok(ldx, C) || !scan_ld_ok(ldr, C) || !scan_ld_ok(ldi, C) || !scan_ld_ok(ldy, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), w = C * e;
     Check c;
@@ -370,8 +373,8 @@ int dwconv_scan_grad(const void *dy, long long lddy, const void *x, long long ld
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!ld_ok(lddy, C) || !ld_ok(ldx, C) || !ld_ok(ldr, C) || !ld_ok(ldi, C) ||
-        !ld_ok(lddx, C) || !ld_ok(lddr, C) || !ld_ok(lddi, C))
+    if (!scan_ld_ok(lddy, C) || !scan_ld_ok(ldx, C) || !scan_ld_ok(ldr, C) || !scan_ld_ok(ldi, C) ||
+        !scan_ld_ok(lddx, C) || !scan_ld_ok(lddr, C) || !scan_ld_ok(lddi, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), rows = a.batch.rows, w = C * e;
     const long long need = scan_workspace(true, a.batch, C, offsets != nullptr);
@@ -398,7 +401,7 @@ int dwconv_scan_grad(const void *dy, long long lddy, const void *x, long long ld
         return st;
     a.dy = dy; a.x = x; a.r = r; a.i = i; a.lam = lam; a.scale = scale; a.states_in = states;
     a.dhT = dhT; a.dx = dx; a.dr = dr; a.di = di; a.dlam = dlam; a.dh0 = dh0;
-    a.agg = static_cast<float *>(workspace);
+    a.workspace = workspace;
     a.lddy = lddy; a.ldx = ldx; a.ldr = ldr; a.ldi = ldi; a.lddx = lddx; a.lddr = lddr;
     a.lddi = lddi; a.type = type; a.C = C;
     return launch_scan_grad(a, stream);

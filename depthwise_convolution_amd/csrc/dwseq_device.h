@@ -38,6 +38,80 @@ __device__ __forceinline__ void store(T *p, const float (&f)[V])
     *reinterpret_cast<Pack<T, V> *>(p) = t;
 }
 
+// V elements as they came from memory, two 16-bit ones to a register: what is
+// kept for later (the compiler gives every element of a Pack a register).
+template <typename T, int V> struct Raw {
+    static constexpr int words = V * (int)sizeof(T) < 4 ? 1 : V * (int)sizeof(T) / 4;
+    unsigned w[words];
+
+    Raw() = default;
+    __device__ __forceinline__ explicit Raw(const float (&f)[V])
+    {
+        static_assert(V == 1 || V % 2 == 0);
+#pragma unroll
+        for (int i = 0; i < words; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __builtin_bit_cast(unsigned, f[i]);
+            } else if constexpr (V == 1) {
+                w[i] = __builtin_bit_cast(unsigned short, (T)f[0]);
+            } else {
+                typedef float f32x2 __attribute__((ext_vector_type(2)));
+                typedef T t2 __attribute__((ext_vector_type(2)));
+                const f32x2 pair = {f[2 * i], f[2 * i + 1]};
+                w[i] = __builtin_bit_cast(unsigned, __builtin_convertvector(pair, t2));
+            }
+        }
+    }
+
+    // through a buffer descriptor, `lane` plus `row` bytes from its start
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, int lane, int row)
+    {
+        if constexpr (V * sizeof(T) == 2) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, lane, row, 0);
+        } else if constexpr (words == 1) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, lane, row, 0);
+        } else if constexpr (words == 2) {
+            *this = __builtin_bit_cast(Raw,
+                                       __builtin_amdgcn_raw_buffer_load_b64(rsrc, lane, row, 0));
+        } else {
+            static_assert(words == 4);
+            *this = __builtin_bit_cast(Raw,
+                                       __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, 0));
+        }
+    }
+    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t rsrc, int lane, int row) const
+    {
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+        if constexpr (V * sizeof(T) == 2) {
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)w[0], rsrc, lane, row, 0);
+        } else if constexpr (words == 1) {
+            __builtin_amdgcn_raw_buffer_store_b32(w[0], rsrc, lane, row, 0);
+        } else if constexpr (words == 2) {
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, *this), rsrc, lane, row,
+                                                  0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, *this), rsrc, lane,
+                                                   row, 0);
+        }
+    }
+    __device__ __forceinline__ float get(int v) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __builtin_bit_cast(float, w[v]);
+        else if constexpr (std::is_same_v<T, bf16>)
+            return __builtin_bit_cast(float, v & 1 ? w[v / 2] & 0xffff0000u : w[v / 2] << 16);
+        else
+            return (float)__builtin_bit_cast(f16, (unsigned short)(w[v / 2] >> (16 * (v & 1))));
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < words; ++i)
+            w[i] = 0;
+    }
+};
+
 // 1 / (1 + e^-v) with the hardware's exponential and reciprocal (one unit in
 // the last place each); 0 and 1 at the infinities
 __device__ __forceinline__ float logistic(float v)

@@ -45,22 +45,14 @@ struct ScanArgs {
     const float *lam, *h0, *dhT, *states_in;
     void *y, *dx, *dr, *di;
     float *hT, *states, *dlam, *dh0, *h;
-    float *agg, *part;
+    void *workspace;
+    float *part;                // within the workspace
     long long ldx, ldr, ldi, ldy, lddy, lddx, lddr, lddi;
     float scale;
     int type, C;
     Batch batch;
 };
 
-// A sequence is cut into segments of `seg` tokens (a multiple of the run
-// length, or at least `rows`: no sequence is cut).  Segment q of sequence s has
-// the number floor(start of s / seg) + s + q, which no other segment has and
-// which is below `segs`; the numbers between are segments of no token.
-struct ScanPlan {
-    int seg, segs;
-    int cut;            // 1: some sequence may have more than one segment
-};
-ScanPlan scan_plan(const Batch &b, int C, bool packed);
 long long scan_states(const Batch &b, int C);
 long long scan_workspace(bool grad, const Batch &b, int C, bool packed);
 

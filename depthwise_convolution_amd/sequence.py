@@ -29,7 +29,7 @@ import ctypes
 
 T_F32, T_F16, T_BF16 = 0, 1, 2
 CAUSAL_MAX_TAPS = 8          # DWCONV_CAUSAL_MAX_TAPS
-SCAN_RUN = 128               # DWCONV_SCAN_RUN
+SCAN_RUN = 8                # DWCONV_SCAN_RUN
 
 SEQ_EXPORTS = ("dwconv_causal_fwd", "dwconv_causal_step", "dwconv_causal_grad_workspace_size",
                "dwconv_causal_grad", "dwconv_scan_states_size", "dwconv_scan_workspace_size",

@@ -96,13 +96,14 @@ int dwconv_causal_grad(const void *dy, long long lddy, const void *x, long long 
  * within each sequence, h before its start being h0[s,c] (or zero where h0 is
  * NULL).  y = h in `type`, the type of x, r and i; lam is [C] float32; h0 and
  * hT, the state after the last token (h0 itself for a sequence of none; NULL
- * to skip), are [seqs][C] float32.  scale > 0 and finite.
+ * to skip), are [seqs][C] float32.  scale > 0 and finite.  Row strides are
+ * below 2^21 elements.
  *
  * states (NULL to skip): dwconv_scan_states_size floats that the gradient
  * needs, the float32 state before each run of DWCONV_SCAN_RUN tokens of a
  * sequence.  workspace: at least dwconv_scan_workspace_size(grad = 0) bytes,
  * 16-byte aligned (NULL where that is 0). */
-#define DWCONV_SCAN_RUN 128
+#define DWCONV_SCAN_RUN 8
 
 int dwconv_scan_states_size(int seqs, long long tokens, int packed, int C, long long *floats);
 int dwconv_scan_workspace_size(int grad, int seqs, long long tokens, int packed, int C,

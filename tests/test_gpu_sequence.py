@@ -231,7 +231,9 @@ SCAN_CASES = [
     ((2, 0), 8, True, False),
     ([0, 0], 8, True, False),
     ((1, 700), 1, True, True),
-    ((1, 1500), 130, False, False),         # cut into segments
+    ((1, 1500), 130, False, False),
+    ((3, 2600), 66, True, False),           # runs looked back over more than once
+    ([40] * 150 + [700], 5, True, False),   # more sequences than one search step sees
     ([1, 900, 0, 300, 2000, 5], 36, True, False),
 ]
 

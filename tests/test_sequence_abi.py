@@ -110,7 +110,7 @@ def test_scan_fwd_refuses(L):
                           (dict(states=Q), "ALIAS"), (dict(hT=Q + 2), "MISALIGNED"),
                           (dict(r=P + 1), "MISALIGNED")]:
         assert _call(L, "dwconv_scan_fwd", SCAN, changes) == code, changes
-    n = dw.dwconv_scan_workspace_size(False, 1, 100000, False, 64)     # cut into segments
+    n = dw.dwconv_scan_workspace_size(False, 1, 100000, False, 64)     # runs are linked
     assert n > 0
     long = dict(seqs=1, tokens=100000)
     for changes in (dict(ws=None), dict(wsb=n - 1), dict(ws=U + 8)):
@@ -165,11 +165,11 @@ def test_linear_refuses(L):
 
 def test_sizes(L):
     out = ctypes.c_longlong(0)
-    assert dw.dwconv_scan_states_size(3, 100, False, 8) == (300 // 128 + 3) * 8
+    assert dw.dwconv_scan_states_size(3, 100, False, 8) == (300 // dw.SCAN_RUN + 3) * 8
     assert dw.dwconv_scan_states_size(3, 0, True, 8) == 24
-    # enough workgroups without cutting: nothing to carry between passes
-    assert dw.dwconv_scan_workspace_size(False, 64, 1000, False, 1024) == 0
-    assert dw.dwconv_scan_workspace_size(False, 1, 100, False, 8) == 0
+    # sequences that one workgroup scans at once have nothing to tell each other
+    assert dw.dwconv_scan_workspace_size(False, 64, 128, False, 1024) == 0
+    assert dw.dwconv_scan_workspace_size(False, 64, 129, False, 1024) > 0
     for name, args in (("dwconv_scan_states_size", (0, 5, 0, 8)),
                        ("dwconv_scan_workspace_size", (0, 1, -1, 0, 8)),
                        ("dwconv_causal_grad_workspace_size", (1, 5, 0, 8, 9)),
