@@ -3,8 +3,8 @@
 //
 // One filter per channel and no sum over channels, so the work is a few
 // multiply-adds per element read: bound by HBM.  A thread holds V adjacent
-// channels (16 bytes of them in the forward) and walks a chunk of tokens with
-// the last K-1 rows in registers, so a row is read once per chunk, plus K-1
+// channels (4; 2 in the gradient) and walks a chunk of tokens with the last
+// K-1 rows in registers, so a row is read once per chunk, plus K-1
 // rows before it that the neighbouring chunk has read too.  Rows of other
 // sequences are never used in arithmetic (they may hold NaN): near the start
 // of a sequence each tap is taken from the carried rows or as zero.
@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;       // rows loaded before the first of them is used
+constexpr int kGradAhead = 4;   // and in the gradient, which holds the next ones too
 
 // w[c0 .. c0+V) of [C][K], as taps of a channel vector
 template <int V, int K>
@@ -234,8 +235,8 @@ __global__ __launch_bounds__(kThreads) void k_causal_step(CausalArgs a, int grou
 
 // ---------------------------------------------------------------------------
 // Gradients.  A thread walks its chunk and K-1 tokens more: dz of a token adds
-// w[j] * dz to the row K-1-j places earlier, held in K accumulators that move
-// on with the walk, so a row of dx is complete K-1 tokens later; tokens of the
+// w[j] * dz to the row K-1-j places earlier, held in accumulators that move on
+// with the walk, so a row of dx is complete K-1 tokens later; tokens of the
 // next sequence do not reach back over its start.  The sums of dw and db
 // stay in registers over the chunk, are added over the workgroup's chunks in
 // LDS and written as one row of partial sums; k_causal_grad_sum adds those.
@@ -260,60 +261,89 @@ __global__ __launch_bounds__(kThreads) void k_causal_grad(CausalArgs a, int grou
     const T *dfinal = static_cast<const T *>(a.dfinal);
     T *dx = static_cast<T *>(a.dx) + c0;
 
-    float w[K][V], b[V], win[K][V], acc[K][V], dw[K][V], db[V];
+    float w[K][V], b[V], ext[K - 1 + kGradAhead][V], acc[K - 1 + kGradAhead][V], dw[K][V], db[V];
     load_taps<V, K>(a.w, a.wtype, c0, w);
     load_bias<V>(a.b, c0, b);
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            win[j][v] = acc[j][v] = dw[j][v] = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
         db[v] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            dw[j][v] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < K - 1 + kGradAhead; ++j)
+            ext[j][v] = acc[j][v] = 0.0f;
+    }
     if (valid && t0 < t1) {
 #pragma unroll
-        for (int j = 1; j < K; ++j)
-            if (t0 - K + j >= 0)
-                load<T, V>(x + (long long)(t0 - K + j) * a.ldx, win[j]);
+        for (int j = 0; j < K - 1; ++j)
+            if (t0 - (K - 1) + j >= 0)
+                load<T, V>(x + (long long)(t0 - (K - 1) + j) * a.ldx, ext[j]);
         Walk at(a.batch, t0);
-        for (int t = t0; t < t1 + K - 1; t += kAhead) {
-            float xs[kAhead][V], ds[kAhead][V];
+        Raw<T, V> xs[kGradAhead], dys[kGradAhead];
+        auto fetch = [&](int t) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                load<T, V>(x + (long long)min(t + u, t2 - 1) * a.ldx, xs[u]);
-                load<T, V>(dy + (long long)min(t + u, t2 - 1) * a.lddy, ds[u]);
+            for (int u = 0; u < kGradAhead; ++u) {
+                xs[u].load(x + (long long)min(t + u, t2 - 1) * a.ldx);
+                dys[u].load(dy + (long long)min(t + u, t2 - 1) * a.lddy);
             }
+        };
+        fetch(t0);
+        for (int t = t0; t < t1 + K - 1; t += kGradAhead) {
+            float ds[kGradAhead][V];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int tt = t + u;
-                if (tt >= t1 + K - 1)
-                    break;
-                // the windows move on by one token
+            for (int u = 0; u < kGradAhead; ++u)
 #pragma unroll
-                for (int j = 0; j < K - 1; ++j)
+                for (int v = 0; v < V; ++v) {
+                    ext[K - 1 + u][v] = xs[u].get(v);
+                    ds[u][v] = dys[u].get(v);
+                }
+            // the next rows are on their way while these are worked on
+            fetch(t + kGradAhead);
+            at.to(a.batch, min(t, t2 - 1));
+            // away from a sequence's ends and from the chunk's
+            if (t - at.start >= K - 1 && t + kGradAhead + K - 1 <= at.end && t + kGradAhead <= t1) {
+#pragma unroll
+                for (int u = 0; u < kGradAhead; ++u) {
+                    float z[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        z[v] = b[v];
+#pragma unroll
+                    for (int j = 0; j < K; ++j)
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            z[v] = fmaf(w[j][v], ext[u + j][v], z[v]);
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        win[j][v] = win[j + 1][v];
-                        acc[j][v] = acc[j + 1][v];
+                        z[v] = ds[u][v] * act_slope(z[v], a.act);
+                        db[v] += z[v];
                     }
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    acc[K - 1][v] = 0.0f;
-                if (tt < t2) {
+                    for (int j = 0; j < K; ++j)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            dw[j][v] = fmaf(z[v], ext[u + j][v], dw[j][v]);
+                            acc[u + j][v] = fmaf(w[j][v], z[v], acc[u + j][v]);
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kGradAhead; ++u) {
+                    const int tt = t + u;
+                    if (tt >= t2)
+                        continue;
                     at.to(a.batch, tt);
                     const int pos = tt - at.start, left = at.end - 1 - tt;
                     float z[V], row[K][V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        win[K - 1][v] = xs[u][v];
+                    for (int v = 0; v < V; ++v)
                         z[v] = b[v];
-                    }
 #pragma unroll
                     for (int j = 0; j < K; ++j) {
 #pragma unroll
                         for (int v = 0; v < V; ++v)
-                            row[j][v] = win[j][v];
+                            row[j][v] = ext[u + j][v];
                         if (pos < K - 1 - j)
                             carried_row<T, V>(init, at.s, pos + j, K, a.C, c0, row[j]);
 #pragma unroll
@@ -334,19 +364,31 @@ __global__ __launch_bounds__(kThreads) void k_causal_grad(CausalArgs a, int grou
                                 dw[j][v] = fmaf(z[v], row[j][v], dw[j][v]);
                         if (dfinal && left < K - 1)
                             load<T, V>(dfinal + ((long long)at.s * (K - 1) + K - 2 - left) * a.C +
-                                           c0, acc[K - 1]);
+                                           c0, acc[u + K - 1]);
                     }
 #pragma unroll
                     for (int j = 0; j < K; ++j)
                         if (pos >= K - 1 - j)
 #pragma unroll
                             for (int v = 0; v < V; ++v)
-                                acc[j][v] = fmaf(w[j][v], z[v], acc[j][v]);
+                                acc[u + j][v] = fmaf(w[j][v], z[v], acc[u + j][v]);
                 }
-                const int done = tt - (K - 1);
-                if (done >= t0 && done < t1)
-                    store<T, V>(dx + (long long)done * a.lddx, acc[0]);
             }
+            // rows K-1 places back are complete; the windows move on
+#pragma unroll
+            for (int u = 0; u < kGradAhead; ++u) {
+                const int done = t + u - (K - 1);
+                if (done >= t0 && done < t1)
+                    store<T, V>(dx + (long long)done * a.lddx, acc[u]);
+            }
+#pragma unroll
+            for (int j = 0; j < K - 1 + kGradAhead; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    acc[j][v] = j < K - 1 ? acc[min(j, K - 2) + kGradAhead][v] : 0.0f;
+                    if (j < K - 1)
+                        ext[j][v] = ext[j + kGradAhead][v];
+                }
         }
     }
     // the partial sums of the workgroup's chunks, one row after the other
@@ -445,16 +487,14 @@ template <typename F> int with_taps(int K, F f)
     return DWCONV_ERR_BAD_DIM;
 }
 
-// f(element pointer type, channels per thread, taps): vectors of `bytes`, or
-// single channels where a row is narrower than that
-template <int BYTES, typename F> int with_variant(const CausalArgs &a, F f)
+// f(element pointer type, channels per thread, taps): vectors of W channels, or
+// single ones where a row is narrower than that
+template <int W, typename F> int with_variant(const CausalArgs &a, F f)
 {
     return with_type(a.type, [&](auto *t) {
-        using T = std::remove_pointer_t<decltype(t)>;
-        constexpr int V = BYTES / (int)sizeof(T);
         return with_taps(a.K, [&](auto k) {
-            if (a.C >= V)
-                return f(t, std::integral_constant<int, V>(), k);
+            if (a.C >= W)
+                return f(t, std::integral_constant<int, W>(), k);
             return f(t, std::integral_constant<int, 1>(), k);
         });
     });
@@ -464,11 +504,13 @@ template <int BYTES, typename F> int with_variant(const CausalArgs &a, F f)
 
 int launch_causal_fwd(const CausalArgs &a, void *stream)
 {
-    return with_variant<16>(a, [&](auto *t, auto v, auto k) {
+    return with_variant<4>(a, [&](auto *t, auto v, auto k) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(v)::value, K = decltype(k)::value;
         const int groups = (int)cdiv(a.C, V);
-        // chunks as long as leaves 16 waves for each of the 256 CUs
+        // Chunks as long as leaves 16 waves for each of the 256 CUs.  4 channels a
+        // thread against 8 of 16 bits: 54.7 and 66.4 us on 8 x 4096 x 2048 bfloat16,
+        // 4 taps, SiLU (floor 50 us): twice the waves, half the registers.
         int chunk = 32;
         while (chunk > kAhead && cdiv(a.batch.rows, chunk) * groups < 256 * 1024)
             chunk >>= 1;
@@ -491,7 +533,7 @@ int launch_causal_fwd(const CausalArgs &a, void *stream)
 
 int launch_causal_step(const CausalArgs &a, void *stream)
 {
-    return with_variant<16>(a, [&](auto *t, auto v, auto k) {
+    return with_variant<4>(a, [&](auto *t, auto v, auto k) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(v)::value, K = decltype(k)::value;
         const int groups = (int)cdiv(a.C, V);
@@ -504,12 +546,18 @@ int launch_causal_step(const CausalArgs &a, void *stream)
     });
 }
 
-// At most 256 rows of partial sums, each of 4 chunks or more.
-CausalGradPlan causal_grad_plan(int rows)
+// Chunks of 64 tokens, shorter where there would be too few workgroups, longer
+// where there would be more than 512 rows of partial sums.  Measured on 8 x 4096 x
+// 2048 bfloat16, 4 taps (floor 75 us): 64 tokens and 2 channels a thread with the
+// next rows in flight 115.7 us; 32 tokens 129.4; 4 channels 130.6; 8 rows ahead
+// 124.6; without the next rows in flight 152.
+CausalGradPlan causal_grad_plan(int rows, int C)
 {
     CausalGradPlan p;
-    p.chunk = 16;
-    while (cdiv(rows, 4LL * p.chunk) > 256)
+    p.chunk = 64;
+    while (p.chunk > 8 && cdiv(rows, 4LL * p.chunk) * cdiv(C, 128) < 512)
+        p.chunk >>= 1;
+    while (cdiv(rows, 4LL * p.chunk) > 512)
         p.chunk <<= 1;
     p.blocks = (int)cdiv(rows, 4LL * p.chunk);
     return p;
@@ -517,16 +565,16 @@ CausalGradPlan causal_grad_plan(int rows)
 
 long long causal_grad_workspace(int rows, int C, int K)
 {
-    return 4LL * causal_grad_plan(rows).blocks * C * (K + 1);
+    return 4LL * causal_grad_plan(rows, C).blocks * C * (K + 1);
 }
 
 int launch_causal_grad(const CausalArgs &a, void *stream)
 {
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const CausalGradPlan p = causal_grad_plan(a.batch.rows);
+    const CausalGradPlan p = causal_grad_plan(a.batch.rows, a.C);
     int rc = DWCONV_OK;
     if (p.blocks > 0)
-        rc = with_variant<8>(a, [&](auto *t, auto v, auto k) {
+        rc = with_variant<2>(a, [&](auto *t, auto v, auto k) {
             using T = std::remove_pointer_t<decltype(t)>;
             constexpr int V = decltype(v)::value, K = decltype(k)::value;
             const int groups = (int)cdiv(a.C, V);

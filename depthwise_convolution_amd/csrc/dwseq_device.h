@@ -63,6 +63,15 @@ template <typename T, int V> struct Raw {
         }
     }
 
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if constexpr (V * sizeof(T) == 2) {
+            w[0] = *reinterpret_cast<const unsigned short *>(p);
+        } else {
+            const Pack<T, V> t = *reinterpret_cast<const Pack<T, V> *>(p);
+            __builtin_memcpy(w, &t, sizeof(t));
+        }
+    }
     // through a buffer descriptor, `lane` plus `row` bytes from its start
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, int lane, int row)
     {

@@ -32,7 +32,7 @@ struct CausalGradPlan {
     int chunk;          // tokens that one thread walks
     int blocks;         // rows of partial sums
 };
-CausalGradPlan causal_grad_plan(int rows);
+CausalGradPlan causal_grad_plan(int rows, int C);
 long long causal_grad_workspace(int rows, int C, int K);
 
 int launch_causal_fwd(const CausalArgs &a, void *stream);
