@@ -69,6 +69,7 @@ template <typename T, int V> struct Raw {
             w[0] = *reinterpret_cast<const unsigned short *>(p);
         } else {
             const Pack<T, V> t = *reinterpret_cast<const Pack<T, V> *>(p);
+            static_assert(sizeof(w) == sizeof(t));
             __builtin_memcpy(w, &t, sizeof(t));
         }
     }
@@ -144,6 +145,22 @@ __device__ __forceinline__ float act_of(float z, int act)
     if (act == DWCONV_ACT_RELU6)
         return z < 0.0f ? 0.0f : (z > 6.0f ? 6.0f : z);
     return z;
+}
+
+// the activation is the same for all: one branch
+template <int V> __device__ __forceinline__ void act_all(float (&z)[V], int act)
+{
+    if (act == DWCONV_ACT_NONE)
+        return;
+    if (act == DWCONV_ACT_SILU) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            z[v] = act_of(z[v], DWCONV_ACT_SILU);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            z[v] = act_of(z[v], act);
+    }
 }
 
 __device__ __forceinline__ float act_slope(float z, int act)

@@ -276,25 +276,36 @@ __device__ __forceinline__ void put(E *p, int width, const float (&v)[V])
     }
 }
 
-// V adjacent sums of row m, from column n on; b: their biases
+// The residuals of V adjacent sums of row m, from column n on.
+template <typename T, int V>
+__device__ __forceinline__ void residual(const Finish &f, long long m, int n, int width,
+                                         Raw<T, V> &r)
+{
+    const T *p = static_cast<const T *>(f.res) + m * f.ldres + n;
+    if (width >= V) {
+        r.load(p);
+    } else {
+        float v[V];
+        get(p, width, v);
+        r = Raw<T, V>(v);
+    }
+}
+
+// V adjacent sums of row m, from column n on; b: their biases, r: residuals
 template <typename T, int V>
 __device__ __forceinline__ void finish(const Finish &f, long long m, int n, int width,
-                                       const float (&b)[V], float (&s)[V])
+                                       const float (&b)[V], const Raw<T, V> &r, float (&s)[V])
 {
-    float r[V];
-    if (f.res)
-        get(static_cast<const T *>(f.res) + m * f.ldres + n, width, r);
 #pragma unroll
     for (int e = 0; e < V; ++e)
         s[e] += b[e];
     if (f.z)
         put(static_cast<T *>(f.z) + m * f.ldz + n, width, s);
+    act_all(s, f.act);
+    if (f.res)
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        s[e] = act_of(s[e], f.act);
-        if (f.res)
-            s[e] += r[e];
-    }
+        for (int e = 0; e < V; ++e)
+            s[e] += r.get(e);
     put(static_cast<T *>(f.y) + m * f.ldy + n, width, s);
 }
 
@@ -458,8 +469,12 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, in
             float sum[4] = {v[0], v[1], v[2], v[3]};
             if (a.f.part)
                 put(a.f.part + ((long long)split * a.M + row) * a.N + col, width, sum);
-            else
-                finish<T>(a.f, row, col, width, b, sum);
+            else {
+                Raw<T, 4> r;
+                if (a.f.res)
+                    residual(a.f, row, col, width, r);
+                finish<T>(a.f, row, col, width, b, r, sum);
+            }
         }
     }
 }
@@ -589,8 +604,21 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
     __syncthreads();
 
     // The sums through LDS, 128 rows at a time, so that a wave's stores cover
-    // whole rows of the tile.
+    // whole rows of the tile; a thread takes 8 columns of every 16th row.  The
+    // residuals are on their way before they are needed.
+    constexpr int kRows = 128 / 16;
     const int n0 = tn * 256 + (tid & 31) * 8, width = a.N - n0;
+    const bool add = a.f.res && !a.f.part;
+    Raw<T, 8> res[kRows];
+    auto fetch = [&](int hp) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int row = tm * 256 + hp * 128 + (tid >> 5) + k * 16;
+            if (add && row < a.M && width > 0)
+                residual(a.f, row, n0, width, res[k]);
+        }
+    };
+    fetch(0);
     float b[8] = {};
     if (a.f.b && !a.f.part && width > 0)
         get(a.f.b + n0, width, b);
@@ -606,24 +634,22 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
                                                (hq * 128 + wn + n * 16 + (lane >> 4) * 4) * 4) =
                         acc[hq][hp][n][m];
         __syncthreads();
-        for (int r = tid >> 5; r < 128; r += 16) {
-            const int row = tm * 256 + hp * 128 + r;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int r = (tid >> 5) + k * 16, row = tm * 256 + hp * 128 + r;
             if (row >= a.M || width <= 0)
-                break;
-            float sum[8];
+                continue;
             const f32x4 *from =
                 reinterpret_cast<const f32x4 *>(lds + r * kPitch + (tid & 31) * 32);
             const f32x4 lo = from[0], hi = from[1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sum[e] = lo[e];
-                sum[4 + e] = hi[e];
-            }
+            float sum[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             if (a.f.part)
                 put(a.f.part + ((long long)split * a.M + row) * a.N + n0, width, sum);
             else
-                finish<T>(a.f, row, n0, width, b, sum);
+                finish<T>(a.f, row, n0, width, b, res[k], sum);
         }
+        if (hp == 0)
+            fetch(1);
         __syncthreads();
     }
 }
@@ -711,7 +737,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few_rows(Product a, int k_pe
     }
     if (a.f.b)
         get(a.f.b + col, a.N - col, b);
-    finish<T>(a.f, row, col, a.N - col, b, sum);
+    Raw<T, 4> r;
+    if (a.f.res)
+        residual(a.f, row, col, a.N - col, r);
+    finish<T>(a.f, row, col, a.N - col, b, r, sum);
 }
 
 // out = finish(the splits' partial sums, added in order): a thread per 4 columns.
@@ -734,7 +763,10 @@ __global__ __launch_bounds__(256) void k_gemm_sum(Product a, int groups)
     }
     if (a.f.b)
         get(a.f.b + n, width, b);
-    finish<T>(a.f, m, n, width, b, sum);
+    Raw<T, 4> r;
+    if (a.f.res)
+        residual(a.f, m, n, width, r);
+    finish<T>(a.f, m, n, width, b, r, sum);
 }
 
 // Whether an operand's chunks can go to LDS directly.
