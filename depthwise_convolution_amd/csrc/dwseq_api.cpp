@@ -121,8 +121,8 @@ int make_batch(int seqs, long long tokens, const int *offsets, bool packed, Batc
 // Row strides may pass 2^31 elements, not the address space.
 bool ld_ok(long long ld, long long width) { return ld >= width && ld < (1LL << 40); }
 
-// The recurrence addresses a run's rows by 32-bit offsets.
-bool scan_ld_ok(long long ld, long long width) { return ld >= width && ld < (1LL << 21); }
+// The recurrence and the products address a tile's rows by 32-bit offsets.
+bool short_ld_ok(long long ld, long long width) { return ld >= width && ld < (1LL << 21); }
 
 int check_workspace(const void *ws, long long have, long long need)
 {
@@ -299,7 +299,7 @@ int dwconv_scan_fwd(const void *x, long long ldx, const void *r, long long ldr, 
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!scan_ld_ok(ldx, C) || !scan_ld_ok(ldr, C) || !scan_ld_ok(ldi, C) || !scan_ld_ok(ldy, C))
+    if (!short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) || !short_ld_ok(ldy, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), rows = a.batch.rows, w = C * e;
     const long long need = scan_workspace(false, a.batch, C, offsets != nullptr);
@@ -339,7 +339,7 @@ int dwconv_scan_step(const void *x, long long ldx, const void *r, long long ldr,
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!scan_ld_ok(ldx, C) || !scan_ld_ok(ldr, C) || !scan_ld_ok(ldi, C) || !scan_ld_ok(ldy, C))
+    if (!short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) || !short_ld_ok(ldy, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), w = C * e;
     Check c;
@@ -373,8 +373,8 @@ int dwconv_scan_grad(const void *dy, long long lddy, const void *x, long long ld
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!scan_ld_ok(lddy, C) || !scan_ld_ok(ldx, C) || !scan_ld_ok(ldr, C) || !scan_ld_ok(ldi, C) ||
-        !scan_ld_ok(lddx, C) || !scan_ld_ok(lddr, C) || !scan_ld_ok(lddi, C))
+    if (!short_ld_ok(lddy, C) || !short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) ||
+        !short_ld_ok(lddx, C) || !short_ld_ok(lddr, C) || !short_ld_ok(lddi, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), rows = a.batch.rows, w = C * e;
     const long long need = scan_workspace(true, a.batch, C, offsets != nullptr);
@@ -431,8 +431,8 @@ int dwconv_linear_fwd(const void *x, long long ldx, const void *w, long long ldw
     const int st = dwconv_linear_workspace_size(0, type, act, M, N, K, &need);
     if (st != DWCONV_OK)
         return st;
-    if (!ld_ok(ldx, K) || !ld_ok(ldw, K) || !ld_ok(ldy, N) || (res && !ld_ok(ldres, N)) ||
-        (z && !ld_ok(ldz, N)))
+    if (!short_ld_ok(ldx, K) || !short_ld_ok(ldw, K) || !short_ld_ok(ldy, N) || (res && !short_ld_ok(ldres, N)) ||
+        (z && !short_ld_ok(ldz, N)))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type);
     Check c;
@@ -467,8 +467,8 @@ int dwconv_linear_grad(const void *dy, long long lddy, const void *x, long long 
     if (st != DWCONV_OK)
         return st;
     const bool has_z = act != DWCONV_ACT_NONE;
-    if (!ld_ok(lddy, N) || !ld_ok(ldx, K) || !ld_ok(ldw, K) || (has_z && !ld_ok(ldz, N)) ||
-        (dx && !ld_ok(lddx, K)) || (dw && !ld_ok(lddw, K)))
+    if (!short_ld_ok(lddy, N) || !short_ld_ok(ldx, K) || !short_ld_ok(ldw, K) || (has_z && !short_ld_ok(ldz, N)) ||
+        (dx && !short_ld_ok(lddx, K)) || (dw && !short_ld_ok(lddw, K)))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type);
     Check c;

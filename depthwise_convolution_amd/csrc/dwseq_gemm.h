@@ -12,7 +12,7 @@
 // chunks.  Where addresses and strides are multiples of 16 bytes the chunks go
 // from memory to LDS directly (buffer loads to LDS; what lies outside the
 // matrices reads as zero by the descriptor's bounds); elsewhere through
-// registers, element by element at the edges.  The chunks of an LDS row are
+// registers.  The chunks of an LDS row are
 // permuted (XOR by the row) so that the lanes of one LDS read fall on
 // different banks; since a direct load fills LDS in lane order, the
 // permutation is applied to the global address.
@@ -121,17 +121,33 @@ template <typename T, int ROWS, bool R, int THREADS> struct Operand {
     {
     }
 
-    // chunk number `idx` of the step at k0 is LDS row idx / per_row; its
-    // chunk of the matrix is place() of it (an involution)
+    // The step at k0 in memory: where it starts and how many bytes it has, none
+    // past the last step or in a half with no row.  (Before the last step another
+    // row of k follows an R operand's, so that its last element is in bounds by
+    // whole words.)
+    __device__ __forceinline__ const char *step_at(int k0) const
+    {
+        return base + (R ? (long long)k0 * ld : (long long)k0 * size);
+    }
+    __device__ __forceinline__ int bytes_at(int k0) const
+    {
+        const int left = K - k0;
+        if (left <= 0 || rows <= 0)
+            return 0;
+        if (R)
+            return left > step ? step * (int)ld + size : (left - 1) * (int)ld + rows * size;
+        return (rows - 1) * (int)ld + left * size;
+    }
+
+    // Chunk number `idx` of a step is LDS row idx / per_row; its chunk of the
+    // matrix is place() of it (an involution).
     __device__ __forceinline__ void stage_direct(char *lds, int k0, int wave, int lane) const
     {
         const int left = K - k0;
-        const int lines = R ? min(left, step) : rows;
-        // nothing to read past the last step, or in a half with no row
-        const int bytes_in =
-            left > 0 && rows > 0 ? (lines - 1) * (int)ld + (R ? rows : left) * size : 0;
-        const char *from = base + (R ? (long long)k0 * ld : (long long)k0 * size);
-        const auto rsrc = dwconv::make_rsrc(from, bytes_in);
+        // bounds are in whole words: round up to the word, which is aligned here,
+        // that holds the last element
+        const __amdgpu_buffer_rsrc_t rsrc =
+            dwconv::make_rsrc(step_at(k0), (bytes_at(k0) + 3) & ~3);
 #pragma unroll
         for (int j = 0; j < count; ++j) {
             const int first = (j * (THREADS / 64) + wave) * 64, idx = first + lane;
@@ -145,37 +161,51 @@ template <typename T, int ROWS, bool R, int THREADS> struct Operand {
         }
     }
 
+    // The same into registers, from any address, and with a last chunk that k
+    // does not fill: what follows in its row is cut off in keep().
     __device__ __forceinline__ void fetch(u32x4 (&regs)[count], int k0, int tid) const
     {
+        const int end = bytes_at(k0);
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(step_at(k0), end);
 #pragma unroll
         for (int j = 0; j < count; ++j) {
-            const int idx = j * THREADS + tid;
-            const int row = idx / per_row, c = place(row, idx % per_row);
-            const int line = R ? k0 + row : row, at = R ? c * elems : k0 + c * elems;
-            const int lines = R ? K : rows, width = R ? rows : K;
-            const T *p = reinterpret_cast<const T *>(base + line * ld) + at;
-            Pack<T, elems> v;
-            if (line < lines && at + elems <= width) {
-                v = *reinterpret_cast<const Pack<T, elems> *>(p);
-            } else {
+            const int idx = j * THREADS + tid, row = idx / per_row, c = place(row, idx % per_row);
+            const int off = row * (int)ld + c * 16;
+            regs[j] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+            // a word that the array's last element fills by half is out of bounds:
+            // that element by itself
+            if (size == 2 && K - k0 <= step && ((end | (int)ld) & 2)) {
+                const int last = end - 2 - off;
+                const bool here = last >= 0 && last < 16 && (last & 3) == 0;
+                const unsigned v =
+                    __builtin_amdgcn_raw_buffer_load_b16(rsrc, here ? end - 2 : kFar, 0, 0);
 #pragma unroll
-                for (int e = 0; e < elems; ++e) {
-                    v.v[e] = (T)0.0f;
-                    if (line < lines && at + e < width)
-                        v.v[e] = p[e];
-                }
+                for (int w = 0; w < 4; ++w)
+                    regs[j][w] |= here && last == w * 4 ? v & 0xffffu : 0u;
             }
-            regs[j] = __builtin_bit_cast(u32x4, v);
         }
     }
 
-    __device__ __forceinline__ void keep(char *lds, const u32x4 (&regs)[count], int tid) const
+    __device__ __forceinline__ void keep(char *lds, u32x4 (&regs)[count], int k0, int tid) const
     {
+        const int left = K - k0;
+        if (!R && left < step)
+#pragma unroll
+            for (int j = 0; j < count; ++j) {
+                const int idx = j * THREADS + tid;
+                const int in = left - place(idx / per_row, idx % per_row) * elems;  // of the chunk
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    constexpr int per_word = 4 / size;
+                    const unsigned half = per_word == 2 && in == w * 2 + 1 ? 0xffffu : 0u;
+                    regs[j][w] &= in >= (w + 1) * per_word ? ~0u : half;
+                }
+            }
 #pragma unroll
         for (int j = 0; j < count; ++j)
             *reinterpret_cast<u32x4 *>(lds + (j * THREADS + tid) * 16) = regs[j];
     }
-
 };
 
 // The fragments that a lane reads of an operand's step: N of them, each 16
@@ -341,7 +371,8 @@ __device__ __forceinline__ void bare_barrier()
 // The tiles of 128 and 64.  Direct: a ring of STAGES steps in LDS, STAGES - 1 of
 // them on their way while one is multiplied; the one barrier of a step says both
 // that every wave's share of the step has arrived and that the stage before it
-// may be refilled.  Otherwise two stages, the next step waiting in registers.
+// may be refilled.  Otherwise two stages, the steps after them
+// in registers.
 // ---------------------------------------------------------------------------
 template <typename T, bool PR, bool QR, bool DIRECT, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, int tiles_n,
@@ -430,25 +461,43 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, in
         // a wave may not end with loads to its workgroup's LDS on their way
         wait_loads<0>();
     } else if (steps > 0) {
-        u32x4 rp[P::count], rq[Q::count];
-        auto settle = [&](int slot) {
-            p.keep(lds + slot * stage_bytes, rp, tid);
-            q.keep(lds + slot * stage_bytes + P::bytes, rq, tid);
+        // the next `ahead` steps wait in registers, or are on their way there
+        constexpr int ahead = BM == 64 ? 3 : 1;
+        u32x4 rp[ahead][P::count], rq[ahead][Q::count];
+        auto fetch = [&](int step, auto d) {
+            p.fetch(rp[d.value], k_first + step * P::step, tid);
+            q.fetch(rq[d.value], k_first + step * P::step, tid);
+        };
+        auto settle = [&](int s, auto d) {
+            char *to = lds + (s & 1) * stage_bytes;
+            p.keep(to, rp[d.value], k_first + s * P::step, tid);
+            q.keep(to + P::bytes, rq[d.value], k_first + s * P::step, tid);
             __syncthreads();
         };
-        p.fetch(rp, k_first, tid);
-        q.fetch(rq, k_first, tid);
-        settle(0);
-        for (int s = 0; s < steps; ++s) {
-            if (s + 1 < steps) {
-                p.fetch(rp, k_first + (s + 1) * P::step, tid);
-                q.fetch(rq, k_first + (s + 1) * P::step, tid);
-            }
+        // step s, whose registers are number d
+        auto one = [&](int s, auto d) {
+            if (s >= steps)
+                return;
+            settle(s, d);
+            fetch(s + ahead, d);
             compute((s & 1) * stage_bytes);
             if ((s & 3) == 3)
                 to_total();
-            if (s + 1 < steps)
-                settle((s + 1) & 1);
+        };
+        constexpr std::integral_constant<int, 0> d0;
+        constexpr std::integral_constant<int, ahead == 3 ? 1 : 0> d1;
+        constexpr std::integral_constant<int, ahead == 3 ? 2 : 0> d2;
+        fetch(0, d0);
+        if constexpr (ahead == 3) {
+            fetch(1, d1);
+            fetch(2, d2);
+        }
+        for (int s = 0; s < steps; s += ahead) {
+            one(s, d0);
+            if constexpr (ahead == 3) {
+                one(s + 1, d1);
+                one(s + 2, d2);
+            }
         }
     }
     to_total();
@@ -774,7 +823,7 @@ inline bool direct_ok(const void *p, long long ld, bool rows_k, int K, int size)
 {
     const bool even = (reinterpret_cast<std::uintptr_t>(p) % 16) == 0 && (ld * size) % 16 == 0 &&
                       (rows_k || ((long long)K * size) % 16 == 0);
-    return even && ld * size < (1 << 22);      // a tile's offsets fit 31 bits
+    return even;
 }
 
 }  // namespace

@@ -11,12 +11,14 @@ namespace {
 constexpr int kDzLanes = 32, kDzSlots = 8;
 
 struct DzPlan {
-    int strip, strips;      // rows, and how many of them: 1024 at most
+    int strip, strips;      // rows, and how many of them (1024 at most)
 };
 
-DzPlan dz_plan(int M)
+DzPlan dz_plan(int M, int N)
 {
     int strip = 64;
+    while (strip > kDzSlots && cdiv(M, strip) * cdiv(N, 256) < 512)
+        strip /= 2;
     while (cdiv(M, strip) > 1024)
         strip *= 2;
     return {strip, (int)cdiv(M, strip)};
@@ -75,35 +77,32 @@ struct GemmPlan {
 // Which kernel, and over how many ranges of k, by the time that a product
 // should take (microseconds): rounds of the chip times (steps of k times a
 // step's time, plus a tile's beginning and end).  A step's time grows from that
-// of a workgroup alone on its CU to that of a full CU; both are measured (at K
-// of 2048 to 8192), as is the sum of the splits' results.
-//
-//   tile   workgroups a CU   16 bits: alone, full, ends   32 bits
-//   256          1             1.05    1.46  12             -
-//   128          2             0.88    1.13   6            2.3   4.1   6
-//    64          5             0.50    0.92   4            0.75  2.65  4
-//    64 deep     2             0.35    0.75   4             -
-//
-// Few rows of operands that are both read along k (`straight`) go to the kernel
-// that reads Q once: measured against
-// the 64 tile with 4 splits it is ahead while M / 16 * K is at most 4096 (at
-// 32 x 4096 x 4096: 14.8 against 13.2 us; at 16 x 4096 x 2048: 6.7 against 9.4).
-GemmPlan gemm_plan(int size, bool straight, int M, int N, int K)
+// of a workgroup alone on its CU to that of a full CU, and with the operands that
+// are read across k.  All from measurements at 128 to 8192 rows and columns and K
+// of 2048 to 8192, as is the time for the sum of the splits' results.
+struct Shape {
+    GemmTile tile;
+    int rows, per_cu;
+    double alone[3], full[3], ends;     // by the number of operands read across k
+};
+static const Shape kWide[] = {
+    {TILE_256, 256, 1, {1.05, 1.40, 1.63}, {1.46, 1.70, 1.92}, 12.0},
+    {TILE_128, 128, 2, {0.88, 0.95, 0.92}, {1.13, 1.18, 1.18}, 6.0},
+    {TILE_64, 64, 5, {0.50, 0.52, 0.52}, {0.92, 0.99, 1.07}, 4.0},
+    {TILE_64_DEEP, 64, 2, {0.34, 0.48, 0.50}, {0.41, 0.63, 0.71}, 4.0}};
+static const Shape kNarrow[] = {
+    {TILE_128, 128, 2, {2.30, 2.30, 2.30}, {4.10, 4.00, 4.00}, 6.0},
+    {TILE_64, 64, 5, {0.75, 0.70, 0.70}, {2.65, 2.60, 2.60}, 4.0}};
+
+// Few rows of operands that are both read along k go to the kernel that reads Q
+// once: measured against the 64 tile with 4 splits it is ahead while M / 16 * K is
+// at most 4096 (at 32 x 4096 x 4096: 14.8 against 13.2 us; at 16 x 4096 x 2048: 6.7
+// against 9.4).
+GemmPlan gemm_plan(int size, int across, int M, int N, int K)
 {
-    if (straight && (M <= 16 || (M <= kFewRows && cdiv(M, 16) * K <= 4096)))
+    if (across == 0 && (M <= 16 || (M <= kFewRows && cdiv(M, 16) * K <= 4096)))
         return {FEW_ROWS, 1};
-    struct Shape {
-        GemmTile tile;
-        int rows, per_cu;
-        double alone, full, ends;
-    };
-    static const Shape wide[] = {{TILE_256, 256, 1, 1.05, 1.46, 12.0},
-                                 {TILE_128, 128, 2, 0.88, 1.13, 6.0},
-                                 {TILE_64, 64, 5, 0.50, 0.92, 4.0},
-                                 {TILE_64_DEEP, 64, 2, 0.35, 0.75, 4.0}};
-    static const Shape narrow[] = {{TILE_128, 128, 2, 2.3, 4.1, 6.0},
-                                   {TILE_64, 64, 5, 0.75, 2.65, 4.0}};
-    const Shape *shapes = size == 2 ? wide : narrow;
+    const Shape *shapes = size == 2 ? kWide : kNarrow;
     const int count = size == 2 ? 4 : 2, cus = 256;
     const long long steps = cdiv((long long)K * size, kStepBytes);
     GemmPlan best{TILE_64, 1};
@@ -115,13 +114,14 @@ GemmPlan gemm_plan(int size, bool straight, int M, int N, int K)
             if (splits > 1 && (steps < 4 * splits || sums > 64e6))
                 break;
             const double groups = (double)cdiv(M, s.rows) * cdiv(N, s.rows) * splits;
-            const double on_cu = groups / cus < s.per_cu ? groups / cus : s.per_cu;
-            const double step = on_cu <= 1.0 ? s.alone
-                                             : s.alone + (s.full - s.alone) * (on_cu - 1.0) /
-                                                             (s.per_cu > 1 ? s.per_cu - 1.0 : 1.0);
-            const double full = s.per_cu > 1 ? step : (groups > 128 ? s.full : s.alone);
+            // how far a CU is from one workgroup to as many as it holds; where it
+            // holds one, how far the chip is from half full to full
+            const double load = s.per_cu > 1 ? (groups / cus - 1.0) / (s.per_cu - 1.0)
+                                             : 2.0 * groups / cus - 1.0;
+            const double part = load < 0.0 ? 0.0 : load > 1.0 ? 1.0 : load;
+            const double step = s.alone[across] + (s.full[across] - s.alone[across]) * part;
             const double rounds = (double)cdiv((long long)groups, (long long)cus * s.per_cu);
-            double time = rounds * (cdiv(steps, splits) * full + s.ends);
+            double time = rounds * (cdiv(steps, splits) * step + s.ends);
             if (splits > 1)
                 time += 3.0 + sums * 2.0 / 4e6;
             if (time < least) {
@@ -133,9 +133,9 @@ GemmPlan gemm_plan(int size, bool straight, int M, int N, int K)
 }
 
 // Bytes of a product's partial sums.
-long long gemm_workspace(int size, bool straight, int M, int N, int K)
+long long gemm_workspace(int size, int across, int M, int N, int K)
 {
-    const GemmPlan p = gemm_plan(size, straight, M, N, K);
+    const GemmPlan p = gemm_plan(size, across, M, N, K);
     return p.splits > 1 ? 4LL * M * N * p.splits : 0;
 }
 
@@ -145,7 +145,7 @@ int product(const T *P, long long ldp, bool p_rows_k, const T *Q, long long ldq,
 {
     if (M == 0 || N == 0)
         return DWCONV_OK;
-    const GemmPlan plan = gemm_plan((int)sizeof(T), !p_rows_k && !q_rows_k, M, N, K);
+    const GemmPlan plan = gemm_plan((int)sizeof(T), p_rows_k + q_rows_k, M, N, K);
     f.part = static_cast<float *>(partials);
     return launch_gemm<T>(Product{P, Q, ldp, ldq, p_rows_k, q_rows_k, M, N, K, plan.tile,
                                   plan.splits, f},
@@ -165,9 +165,8 @@ static GradSpace grad_space(int type, int act, int M, int N, int K)
     const int size = elem_size(type);
     GradSpace g;
     g.dz = act == DWCONV_ACT_NONE ? 0 : cdiv((long long)M * N * size, 16) * 16;
-    g.db = cdiv(4LL * dz_plan(M).strips * N, 16) * 16;
-    const long long dx = gemm_workspace(size, false, M, K, N),
-                    dw = gemm_workspace(size, false, N, K, M);
+    g.db = cdiv(4LL * dz_plan(M, N).strips * N, 16) * 16;
+    const long long dx = gemm_workspace(size, 1, M, K, N), dw = gemm_workspace(size, 2, N, K, M);
     g.sums = dx > dw ? dx : dw;
     return g;
 }
@@ -177,7 +176,7 @@ long long linear_workspace(bool grad, int type, int act, int M, int N, int K)
     if (M == 0)
         return 0;
     if (!grad)
-        return gemm_workspace(elem_size(type), true, M, N, K);
+        return gemm_workspace(elem_size(type), 0, M, N, K);
     const GradSpace g = grad_space(type, act, M, N, K);
     return g.dz + g.db + g.sums;
 }
@@ -205,7 +204,7 @@ int launch_linear_grad(const LinearArgs &a, void *stream)
         float *part = reinterpret_cast<float *>(space + g.dz);
         void *sums = space + g.dz + g.db;
         int rc = DWCONV_OK;
-        const DzPlan dp = dz_plan(a.M);
+        const DzPlan dp = dz_plan(a.M, a.N);
         auto make_dz = [&](auto v) {
             constexpr int V = decltype(v)::value;
             return dwconv::launch_kernel(

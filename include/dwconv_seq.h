@@ -149,7 +149,7 @@ int dwconv_scan_grad(const void *dy, long long lddy, const void *x, long long ld
  * elements are exact and summed in float32; float32 elements are multiplied
  * to float32 accuracy.  workspace: at least dwconv_linear_workspace_size
  * (grad = 0) bytes, 16-byte aligned (NULL where that is 0).  M = 0 is
- * allowed. */
+ * allowed.  Row strides are below 2^21 elements. */
 int dwconv_linear_workspace_size(int grad, int type, int act, long long M, int N, int K,
                                  long long *bytes);
 int dwconv_linear_fwd(const void *x, long long ldx, const void *w, long long ldw, int type,

@@ -480,6 +480,31 @@ def test_linear_into_column_ranges(torch):
         assert (rest == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_linear_odd_extents_in_aligned_rows(torch, dtype):
+    """Views whose rows start on 16 bytes but end on an odd element, in the order of
+    every product: the last element of the last row counts."""
+    rng = np.random.default_rng(6)
+    M, N, K = 67, 129, 73
+    g, r = {}, {}
+    for name, shape in (("x", (M, K)), ("w", (N, K)), ("dy", (M, N))):
+        t, r[name] = _draw(torch, rng, shape, dtype)
+        big = torch.full((shape[0], 160), float("nan"), dtype=t.dtype, device="cuda")
+        g[name] = big[:, :shape[1]]
+        g[name].copy_(t)
+    y = dw.linear(g["x"], g["w"])
+    dx, dW, db = dw.linear_grad(g["dy"], g["x"], g["w"])
+    torch.cuda.synchronize()
+    z, big = ref.linear(r["x"], r["w"], None)
+    _near(y, z, ref.store_tol(z, (2 * K + 12) * ref.EPS * big, dtype), "y")
+    want = ref.linear_grad(r["dy"], r["x"], r["w"], None, "none")
+    for name, t, n in (("dx", dx, N), ("dw", dW, M)):
+        v, b = want[name]
+        _near(t, v, ref.store_tol(v, (2 * n + 12) * ref.EPS * b, dtype), name)
+    v, b = want["db"]
+    _near(db, v, (M + 4) * ref.EPS * b + 1e-30, "db")
+
+
 def test_linear_passes_infinities_and_nan(torch):
     """A row of x with NaN or infinity reaches its own row of y only, and
     finite float32 values beyond the 16-bit types' precision stay finite."""
