@@ -89,6 +89,10 @@ template <typename T, int V> struct Raw {
                                        __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, 0));
         }
     }
+    // Four words go without a scalar offset: the compiler takes such a store to
+    // have read its registers at once and overwrites them in the next
+    // instruction, which has been seen to change the last word of some lanes.
+    // Without one it waits.
     __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t rsrc, int lane, int row) const
     {
         typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
@@ -101,8 +105,8 @@ template <typename T, int V> struct Raw {
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, *this), rsrc, lane, row,
                                                   0);
         } else {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, *this), rsrc, lane,
-                                                   row, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, *this), rsrc,
+                                                   lane + row, 0, 0);
         }
     }
     __device__ __forceinline__ float get(int v) const

@@ -186,7 +186,7 @@ template <typename T, int V> struct Rows {
     }
     __device__ __forceinline__ void fetch(Raw<T, V> (&v)[KT], int row, int rows) const
     {
-        const auto rsrc = run(row, rows);
+        const __amdgpu_buffer_rsrc_t rsrc = run(row, rows);
 #pragma unroll
         for (int k = 0; k < KT; ++k)
             v[k].load(rsrc, lane, k * (int)ld);
@@ -417,8 +417,7 @@ __device__ __forceinline__ int take(const Chain &ch)
 // Forward.
 // ---------------------------------------------------------------------------
 template <typename T, int V>
-__global__ __launch_bounds__(Layout<V>::threads, sizeof(T) == 2 ? 4 : 3) void k_scan_fwd(ScanArgs a,
-                                                                                  Chain ch)
+__global__ __launch_bounds__(Layout<V>::threads, 3) void k_scan_fwd(ScanArgs a, Chain ch)
 {
     using L = Layout<V>;
     constexpr int KT = L::KT;
@@ -487,7 +486,7 @@ __global__ __launch_bounds__(Layout<V>::threads, sizeof(T) == 2 ? 4 : 3) void k_
         hk[v] = fmaf(A[v], carry[lane * V + v], B[v]);
     if (a.states && mt < g.t1)
         store<float, V>(a.states + (long long)(g.state_row + group) * C + c0, hk);
-    const auto out = y.run(g.t0, rows);
+    const __amdgpu_buffer_rsrc_t out = y.run(g.t0, rows);
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
 #pragma unroll
@@ -602,7 +601,8 @@ __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_gra
     }
     if (g.first && a.dh0 && group == 0)
         store<float, V>(a.dh0 + (long long)g.s * C + c0, A);
-    const auto to_x = dx.run(g.t0, rows), to_r = dr.run(g.t0, rows), to_i = di.run(g.t0, rows);
+    const __amdgpu_buffer_rsrc_t to_x = dx.run(g.t0, rows), to_r = dr.run(g.t0, rows),
+                                 to_i = di.run(g.t0, rows);
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
         float ox[V], orr[V], oi[V];
