@@ -69,6 +69,7 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 typedef __attribute__((address_space(3))) char *lds_ptr;
+typedef __attribute__((address_space(3))) f32x4 *lds_f32x4;
 
 constexpr int kFar = 0x7ffffff0;    // beyond every descriptor's bounds
 
@@ -339,6 +340,100 @@ __device__ __forceinline__ void finish(const Finish &f, long long m, int n, int 
     put(static_cast<T *>(f.y) + m * f.ldy + n, width, s);
 }
 
+// The activation, and whether a tile has vectors of V columns that N cuts, as
+// constants: one branch for a tile, and the code that runs lies in one piece
+// (with the choices made row by row, the 256 tile's end was longer than the
+// instruction cache).
+template <typename F> __device__ __forceinline__ void with_act(int act, F f)
+{
+    switch (act) {
+    case DWCONV_ACT_SILU: f(std::integral_constant<int, DWCONV_ACT_SILU>()); break;
+    case DWCONV_ACT_RELU: f(std::integral_constant<int, DWCONV_ACT_RELU>()); break;
+    case DWCONV_ACT_RELU6: f(std::integral_constant<int, DWCONV_ACT_RELU6>()); break;
+    default: f(std::integral_constant<int, DWCONV_ACT_NONE>()); break;
+    }
+}
+
+template <int V, typename F> __device__ __forceinline__ void with_cut(int left, int cols, F f)
+{
+    if (left < cols && left % V != 0)
+        f(std::true_type());
+    else
+        f(std::false_type());
+}
+
+// The rows from m0 and columns from n0 on that a tile has in a matrix, of which a
+// lane moves V adjacent columns from `col` on of row `line` + `row` (`line` the
+// same in the wave).  The descriptor ends with the tile's last row, so that
+// rows beyond M are neither read (as zero) nor written; lanes beyond N are sent out
+// of bounds.  CUT: a vector that N cuts moves by element.
+template <typename E, int V, bool CUT> struct Block {
+    static constexpr int size = (int)sizeof(E);
+    const char *base;
+    int ld, bytes, left;        // bytes of a row's stride and in all; columns to N
+
+    __device__ __forceinline__ Block(const void *p, long long ld_elems, int m0, int n0, int rows,
+                                     int M, int N)
+        : base(static_cast<const char *>(p) + (m0 * ld_elems + n0) * size),
+          ld((int)ld_elems * size), bytes((min(M - m0, rows) - 1) * ld + (N - n0) * size),
+          left(N - n0)
+    {
+    }
+    __device__ __forceinline__ int at(int line, int col) const
+    {
+        return col + V <= left ? line * ld + col * size : kFar;
+    }
+    __device__ __forceinline__ int at(int line, int col, int e) const
+    {
+        return col + V > left && col + e < left ? line * ld + (col + e) * size : kFar;
+    }
+    __device__ __forceinline__ void load(Raw<E, V> &v, int line, int row, int col) const
+    {
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(base, bytes);
+        v.load(rsrc, at(line, col), row * ld);
+        if constexpr (CUT)
+#pragma unroll
+            for (int e = 0; e < V - 1; ++e) {
+                Raw<E, 1> one;
+                one.load(rsrc, at(line, col, e), row * ld);
+                v.w[e * size / 4] |= one.w[0] << (e * size % 4 * 8);
+            }
+    }
+    __device__ __forceinline__ void store(const float (&s)[V], int line, int row, int col) const
+    {
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(base, bytes);
+        Raw<E, V>(s).store(rsrc, at(line, col), row * ld);
+        if constexpr (CUT)
+#pragma unroll
+            for (int e = 0; e < V - 1; ++e) {
+                const float one[1] = {s[e]};
+                Raw<E, 1>(one).store(rsrc, at(line, col, e), row * ld);
+            }
+    }
+};
+
+// V adjacent sums of a tile on their way to memory; b: their biases, r: residuals
+template <int ACT, typename T, int V, bool CUT>
+__device__ __forceinline__ void finish(const Finish &f, const Block<T, V, CUT> &z,
+                                       const Block<T, V, CUT> &y, const float (&b)[V],
+                                       const Raw<T, V> &r, float (&s)[V], int line, int row,
+                                       int col)
+{
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        s[e] += b[e];
+    if (f.z)
+        z.store(s, line, row, col);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        s[e] = act_of(s[e], ACT);
+    if (f.res)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            s[e] += r.get(e);
+    y.store(s, line, row, col);
+}
+
 // Tile of workgroup b: each XCD (b % 8) takes a contiguous range of the tiles,
 // which are numbered in bands of 8 tile rows, down the band first, so that the
 // tiles at work in one XCD share rows of P and Q in its L2.
@@ -501,31 +596,54 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, in
         }
     }
     to_total();
+    const int m0 = tm * BM, n0 = tn * BN, line = lane & 15, first = wn + (lane >> 4) * 4;
+    auto sums_of = [&](int n, int m, float (&sum)[4]) {
+        const f32x4 v = kTotal ? total[kTotal ? n : 0][kTotal ? m : 0] : acc[n][m];
 #pragma unroll
-    for (int n = 0; n < NF; ++n) {
-        const int col = tn * BN + wn + n * 16 + (lane >> 4) * 4, width = a.N - col;
-        if (width <= 0)
-            continue;
-        float b[4] = {};
-        if (a.f.b && !a.f.part)
-            get(a.f.b + col, width, b);
+        for (int e = 0; e < 4; ++e)
+            sum[e] = v[e];
+    };
+    with_cut<4>(a.N - n0, BN, [&](auto c) {
+        constexpr bool CUT = decltype(c)::value;
+        if (a.f.part) {
+            const Block<float, 4, CUT> out(a.f.part + (long long)split * a.M * a.N, a.N, m0, n0,
+                                           BM, a.M, a.N);
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int row = tm * BM + wm + m * 16 + (lane & 15);
-            if (row >= a.M)
-                continue;
-            const f32x4 v = kTotal ? total[kTotal ? n : 0][kTotal ? m : 0] : acc[n][m];
-            float sum[4] = {v[0], v[1], v[2], v[3]};
-            if (a.f.part)
-                put(a.f.part + ((long long)split * a.M + row) * a.N + col, width, sum);
-            else {
-                Raw<T, 4> r;
-                if (a.f.res)
-                    residual(a.f, row, col, width, r);
-                finish<T>(a.f, row, col, width, b, r, sum);
-            }
+            for (int n = 0; n < NF; ++n)
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    float sum[4];
+                    sums_of(n, m, sum);
+                    out.store(sum, line, wm + m * 16, first + n * 16);
+                }
+            return;
         }
-    }
+        const Block<T, 4, CUT> res(a.f.res, a.f.ldres, m0, n0, BM, a.M, a.N),
+            z(a.f.z, a.f.ldz, m0, n0, BM, a.M, a.N), y(a.f.y, a.f.ldy, m0, n0, BM, a.M, a.N);
+        const Block<float, 4, CUT> bias(a.f.b, 0, 0, n0, 1, 1, a.N);
+        with_act(a.f.act, [&](auto act) {
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                const int col = first + n * 16;
+                Raw<T, 4> r[MF];
+                Raw<float, 4> bn;
+                bn.clear();
+                if (a.f.b)
+                    bias.load(bn, 0, 0, col);
+                const float b[4] = {bn.get(0), bn.get(1), bn.get(2), bn.get(3)};
+                if (a.f.res)
+#pragma unroll
+                    for (int m = 0; m < MF; ++m)
+                        res.load(r[m], line, wm + m * 16, col);
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    float sum[4];
+                    sums_of(n, m, sum);
+                    finish<decltype(act)::value>(a.f, z, y, b, r[m], sum, line, wm + m * 16, col);
+                }
+            }
+        });
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -656,51 +774,91 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
     // whole rows of the tile; a thread takes 8 columns of every 16th row.  The
     // residuals are on their way before they are needed.
     constexpr int kRows = 128 / 16;
-    const int n0 = tn * 256 + (tid & 31) * 8, width = a.N - n0;
-    const bool add = a.f.res && !a.f.part;
-    Raw<T, 8> res[kRows];
-    auto fetch = [&](int hp) {
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int row = tm * 256 + hp * 128 + (tid >> 5) + k * 16;
-            if (add && row < a.M && width > 0)
-                residual(a.f, row, n0, width, res[k]);
-        }
-    };
-    fetch(0);
-    float b[8] = {};
-    if (a.f.b && !a.f.part && width > 0)
-        get(a.f.b + n0, width, b);
-#pragma unroll
-    for (int hp = 0; hp < 2; ++hp) {
+    const int m0 = tm * 256, n0 = tn * 256, line = tid >> 5, col = (tid & 31) * 8;
+    auto spread = [&](int hp) {
 #pragma unroll
         for (int hq = 0; hq < 2; ++hq)
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
-                    *reinterpret_cast<f32x4 *>(lds + (wm + m * 16 + (lane & 15)) * kPitch +
-                                               (hq * 128 + wn + n * 16 + (lane >> 4) * 4) * 4) =
+                    *(lds_f32x4)((lds_ptr)lds + (wm + m * 16 + (lane & 15)) * kPitch +
+                                 (hq * 128 + wn + n * 16 + (lane >> 4) * 4) * 4) =
                         acc[hq][hp][n][m];
         __syncthreads();
+    };
+    auto row_of = [&](int k, float (&s)[8]) {
+        const lds_f32x4 from = (lds_f32x4)((lds_ptr)lds + (line + k * 16) * kPitch + col * 4);
+        const f32x4 lo = from[0], hi = from[1];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int r = (tid >> 5) + k * 16, row = tm * 256 + hp * 128 + r;
-            if (row >= a.M || width <= 0)
-                continue;
-            const f32x4 *from =
-                reinterpret_cast<const f32x4 *>(lds + r * kPitch + (tid & 31) * 32);
-            const f32x4 lo = from[0], hi = from[1];
-            float sum[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            if (a.f.part)
-                put(a.f.part + ((long long)split * a.M + row) * a.N + n0, width, sum);
-            else
-                finish<T>(a.f, row, n0, width, b, res[k], sum);
+        for (int e = 0; e < 4; ++e) {
+            s[e] = lo[e];
+            s[e + 4] = hi[e];
         }
-        if (hp == 0)
-            fetch(1);
-        __syncthreads();
+    };
+    if (a.f.part) {
+        with_cut<4>(a.N - n0, 256, [&](auto c) {
+            const Block<float, 4, decltype(c)::value> out(
+                a.f.part + (long long)split * a.M * a.N, a.N, m0, n0, 256, a.M, a.N);
+#pragma unroll
+            for (int hp = 0; hp < 2; ++hp) {
+                spread(hp);
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) {
+                    float s[8];
+                    row_of(k, s);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float half[4] = {s[h * 4], s[h * 4 + 1], s[h * 4 + 2], s[h * 4 + 3]};
+                        out.store(half, line, hp * 128 + k * 16, col + h * 4);
+                    }
+                }
+                __syncthreads();
+            }
+        });
+        return;
     }
+    with_cut<8>(a.N - n0, 256, [&](auto c) {
+        constexpr bool CUT = decltype(c)::value;
+        const Block<T, 8, CUT> from(a.f.res, a.f.ldres, m0, n0, 256, a.M, a.N),
+            z(a.f.z, a.f.ldz, m0, n0, 256, a.M, a.N), y(a.f.y, a.f.ldy, m0, n0, 256, a.M, a.N);
+        Raw<T, 8> res[kRows];
+        auto fetch = [&](int hp) {
+            if (a.f.res)
+#pragma unroll
+                for (int k = 0; k < kRows; ++k)
+                    from.load(res[k], line, hp * 128 + k * 16, col);
+        };
+        fetch(0);
+        float b[8] = {};
+        if (a.f.b) {
+            const Block<float, 4, CUT> bias(a.f.b, 0, 0, n0, 1, 1, a.N);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Raw<float, 4> v;
+                bias.load(v, 0, 0, col + h * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    b[h * 4 + e] = v.get(e);
+            }
+        }
+        with_act(a.f.act, [&](auto act) {
+#pragma unroll
+            for (int hp = 0; hp < 2; ++hp) {
+                spread(hp);
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) {
+                    float s[8];
+                    row_of(k, s);
+                    finish<decltype(act)::value>(a.f, z, y, b, res[k], s, line, hp * 128 + k * 16,
+                                                 col);
+                }
+                if (hp == 0)
+                    fetch(1);
+                __syncthreads();
+            }
+        });
+    });
 }
 
 // ---------------------------------------------------------------------------
