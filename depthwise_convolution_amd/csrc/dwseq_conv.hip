@@ -171,9 +171,7 @@ __global__ __launch_bounds__(kThreads) void k_causal_fwd(CausalArgs a, int group
                         z[v] = fmaf(w[j][v], row[v], z[v]);
                 }
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                z[v] = act_of(z[v], a.act);
+            act_all(z, a.act);
             if (t + u < t1)
                 store<T, V>(y + (long long)(t + u) * a.ldy, z);
         }
@@ -213,9 +211,7 @@ __device__ __forceinline__ void step_vector(const CausalArgs &a, int s, int c0)
         if (j > 0)
             store<T, V>(state + (long long)(j - 1) * a.C, row);
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        z[v] = act_of(z[v], a.act);
+    act_all(z, a.act);
     store<T, V>(static_cast<T *>(a.y) + s * a.ldy + c0, z);
 }
 
@@ -303,30 +299,29 @@ __global__ __launch_bounds__(kThreads) void k_causal_grad(CausalArgs a, int grou
             at.to(a.batch, min(t, t2 - 1));
             // away from a sequence's ends and from the chunk's
             if (t - at.start >= K - 1 && t + kGradAhead + K - 1 <= at.end && t + kGradAhead <= t1) {
+                float z[kGradAhead * V];
 #pragma unroll
-                for (int u = 0; u < kGradAhead; ++u) {
-                    float z[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        z[v] = b[v];
-#pragma unroll
-                    for (int j = 0; j < K; ++j)
-#pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            z[v] = fmaf(w[j][v], ext[u + j][v], z[v]);
+                for (int u = 0; u < kGradAhead; ++u)
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        z[v] = ds[u][v] * act_slope(z[v], a.act);
-                        db[v] += z[v];
+                        z[u * V + v] = b[v];
+#pragma unroll
+                        for (int j = 0; j < K; ++j)
+                            z[u * V + v] = fmaf(w[j][v], ext[u + j][v], z[u * V + v]);
                     }
+                slope_all(z, a.act);
 #pragma unroll
-                    for (int j = 0; j < K; ++j)
+                for (int u = 0; u < kGradAhead; ++u)
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            dw[j][v] = fmaf(z[v], ext[u + j][v], dw[j][v]);
-                            acc[u + j][v] = fmaf(w[j][v], z[v], acc[u + j][v]);
+                    for (int v = 0; v < V; ++v) {
+                        const float dz = ds[u][v] * z[u * V + v];
+                        db[v] += dz;
+#pragma unroll
+                        for (int j = 0; j < K; ++j) {
+                            dw[j][v] = fmaf(dz, ext[u + j][v], dw[j][v]);
+                            acc[u + j][v] = fmaf(w[j][v], dz, acc[u + j][v]);
                         }
-                }
+                    }
             } else {
 #pragma unroll
                 for (int u = 0; u < kGradAhead; ++u) {
@@ -350,9 +345,10 @@ __global__ __launch_bounds__(kThreads) void k_causal_grad(CausalArgs a, int grou
                         for (int v = 0; v < V; ++v)
                             z[v] = fmaf(w[j][v], row[j][v], z[v]);
                     }
+                    slope_all(z, a.act);
 #pragma unroll
                     for (int v = 0; v < V; ++v)
-                        z[v] = ds[u][v] * act_slope(z[v], a.act);
+                        z[v] *= ds[u][v];
                     if (tt < t1) {
 #pragma unroll
                         for (int v = 0; v < V; ++v)

@@ -180,6 +180,21 @@ __device__ __forceinline__ float act_slope(float z, int act)
     return 1.0f;
 }
 
+// z's slopes in its place, again with one branch for all: with one for each the
+// exponentials and reciprocals wait for each other instead of overlapping
+template <int V> __device__ __forceinline__ void slope_all(float (&z)[V], int act)
+{
+    if (act == DWCONV_ACT_SILU) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            z[v] = act_slope(z[v], DWCONV_ACT_SILU);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            z[v] = act == DWCONV_ACT_NONE ? 1.0f : act_slope(z[v], act);
+    }
+}
+
 // First row of sequence s (s = seqs: the end).  Offsets are clamped to the
 // rows there are, and the outer two are taken as given by the batch.
 __device__ __forceinline__ int seq_start(const Batch &b, int s)

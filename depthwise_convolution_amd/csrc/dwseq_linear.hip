@@ -42,9 +42,10 @@ __global__ __launch_bounds__(kDzLanes *kDzSlots) void k_dz(LinearArgs a, T *dz, 
             load<T, V>(static_cast<const T *>(a.dy) + m * a.lddy + n, d);
             if (a.act != DWCONV_ACT_NONE) {
                 load<T, V>(static_cast<const T *>(a.z_in) + m * a.ldz + n, z);
+                slope_all(z, a.act);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    d[v] *= act_slope(z[v], a.act);
+                    d[v] *= z[v];
                 store<T, V>(dz + (long long)m * a.N + n, d);
             }
 #pragma unroll
