@@ -232,7 +232,8 @@ int dwconv_causal_grad(const void *dy, long long lddy, const void *x, long long 
     if (!ld_ok(ldx, C) || !ld_ok(lddy, C) || !ld_ok(lddx, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), we = elem_size(wtype), rows = a.batch.rows;
-    const long long carried = e * seqs * (K - 1) * C, need = causal_grad_workspace(a.batch.rows, C, K);
+    const long long carried = e * seqs * (K - 1) * C;
+    const long long need = causal_grad_workspace(a.batch.rows, C, K);
     Check c;
     c.in(dy, region(dy, rows, lddy * e, C * e), (int)e);
     c.in(x, region(x, rows, ldx * e, C * e), (int)e);
@@ -299,7 +300,8 @@ int dwconv_scan_fwd(const void *x, long long ldx, const void *r, long long ldr, 
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) || !short_ld_ok(ldy, C))
+    if (!short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) ||
+        !short_ld_ok(ldy, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), rows = a.batch.rows, w = C * e;
     const long long need = scan_workspace(false, a.batch, C, offsets != nullptr);
@@ -339,7 +341,8 @@ int dwconv_scan_step(const void *x, long long ldx, const void *r, long long ldr,
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) || !short_ld_ok(ldy, C))
+    if (!short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) ||
+        !short_ld_ok(ldy, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), w = C * e;
     Check c;
@@ -373,7 +376,8 @@ int dwconv_scan_grad(const void *dy, long long lddy, const void *x, long long ld
         return st;
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (!short_ld_ok(lddy, C) || !short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) || !short_ld_ok(ldi, C) ||
+    if (!short_ld_ok(lddy, C) || !short_ld_ok(ldx, C) || !short_ld_ok(ldr, C) ||
+        !short_ld_ok(ldi, C) ||
         !short_ld_ok(lddx, C) || !short_ld_ok(lddr, C) || !short_ld_ok(lddi, C))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type), rows = a.batch.rows, w = C * e;
@@ -431,8 +435,8 @@ int dwconv_linear_fwd(const void *x, long long ldx, const void *w, long long ldw
     const int st = dwconv_linear_workspace_size(0, type, act, M, N, K, &need);
     if (st != DWCONV_OK)
         return st;
-    if (!short_ld_ok(ldx, K) || !short_ld_ok(ldw, K) || !short_ld_ok(ldy, N) || (res && !short_ld_ok(ldres, N)) ||
-        (z && !short_ld_ok(ldz, N)))
+    if (!short_ld_ok(ldx, K) || !short_ld_ok(ldw, K) || !short_ld_ok(ldy, N) ||
+        (res && !short_ld_ok(ldres, N)) || (z && !short_ld_ok(ldz, N)))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type);
     Check c;
@@ -467,8 +471,9 @@ int dwconv_linear_grad(const void *dy, long long lddy, const void *x, long long 
     if (st != DWCONV_OK)
         return st;
     const bool has_z = act != DWCONV_ACT_NONE;
-    if (!short_ld_ok(lddy, N) || !short_ld_ok(ldx, K) || !short_ld_ok(ldw, K) || (has_z && !short_ld_ok(ldz, N)) ||
-        (dx && !short_ld_ok(lddx, K)) || (dw && !short_ld_ok(lddw, K)))
+    if (!short_ld_ok(lddy, N) || !short_ld_ok(ldx, K) || !short_ld_ok(ldw, K) ||
+        (has_z && !short_ld_ok(ldz, N)) || (dx && !short_ld_ok(lddx, K)) ||
+        (dw && !short_ld_ok(lddw, K)))
         return DWCONV_ERR_ROW_STRIDE;
     const long long e = elem_size(type);
     Check c;

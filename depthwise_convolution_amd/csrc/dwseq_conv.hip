@@ -8,6 +8,14 @@
 // rows before it that the neighbouring chunk has read too.  Rows of other
 // sequences are never used in arithmetic (they may hold NaN): near the start
 // of a sequence each tap is taken from the carried rows or as zero.
+//
+// Measured, with inputs from HBM: forward, 8 x 4096 x 2048 bfloat16, 4 taps and
+// SiLU, 60 us (4.5 TB/s; a copy of the same bytes 50); 20011 x 1000 float32 in 37
+// sequences 37.5 us (4.3 TB/s); gradient, 16411 x 1536 float16 in 23 sequences,
+// 46 us with its sums (3.3 TB/s), bound by the vector unit's some 60 operations an element
+// as much as by HBM; single tokens, 64 x 2048, 3 us, a launch.  4
+// channels a thread in the forward take 55 us where 8 take 67 (fewer waves); in the
+// gradient 2 take 116 where 4 take 145 (8 x 4096 x 2048; registers).
 #include "dwseq_device.h"
 
 namespace dwseq {

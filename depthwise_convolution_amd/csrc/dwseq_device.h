@@ -133,12 +133,6 @@ __device__ __forceinline__ float logistic(float v)
     return __builtin_amdgcn_rcpf(1.0f + __expf(-v));
 }
 
-// log(1 + e^v), without overflow and exact for very negative v
-__device__ __forceinline__ float softplus(float v)
-{
-    return v > 20.0f ? v : log1pf(expf(v));
-}
-
 // NaN passes through every activation.
 __device__ __forceinline__ float act_of(float z, int act)
 {

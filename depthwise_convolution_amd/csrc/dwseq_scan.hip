@@ -22,6 +22,13 @@
 // timing: a state found further back is carried forward by the very operations
 // that its own workgroups use.
 //
+// What bounds it: 4 arrays of 16 bits moved an element (forward) against some 46
+// operations of the vector unit in the forward and 70 in the gradient, six and
+// more of them at a quarter of the rate.  The two overlap incompletely: at 8 x 2048 x 2048
+// bfloat16 the forward takes 73 us (3.7 TB/s; a copy of the same bytes 55) and
+// the gradient 123 us (3.8 TB/s), at 1 x 65537 x 1280 the forward 178 us (3.8
+// TB/s), of which the chain of 512 runs costs a tenth.  A run of 128 tokens is
+// what 256 threads hold in registers, 8 tokens of 4 channels each.
 #include "dwseq_device.h"
 
 namespace dwseq {
@@ -313,6 +320,9 @@ __device__ __forceinline__ unsigned long long hear(unsigned long long *word)
 
 // The state before a run, by one wave with a channel a lane.  `before`: how many
 // runs of the sequence come before it (REV: after); `mine`: this run's words.
+// Runs looked at in one go.  2, 4, 8 and 16 take 241, 184, 178 and 225 us in
+// the forward at 1 x 65537 x 1280, where the chain is longest, and 72, 74, 77 and
+// 96 at 8 x 2048 x 2048, where registers count.
 constexpr int kLookBack = 4;
 
 template <bool REV>
@@ -414,7 +424,8 @@ __device__ __forceinline__ int take(const Chain &ch)
 }
 
 // ---------------------------------------------------------------------------
-// Forward.
+// Forward.  Registers for 3 workgroups a CU: with 4 the loads of a run
+// no longer fit at once (8 x 2048 x 2048: 77 against 74 us).
 // ---------------------------------------------------------------------------
 template <typename T, int V>
 __global__ __launch_bounds__(Layout<V>::threads, 3) void k_scan_fwd(ScanArgs a, Chain ch)
@@ -502,8 +513,9 @@ __global__ __launch_bounds__(Layout<V>::threads, 3) void k_scan_fwd(ScanArgs a, 
 // Gradients, from the last run to the first.  With p[t] = a[t] g[t] the reversed
 // recurrence is p[t] = a[t] p[t+1] + a[t] dy[t], whose steps compose as the
 // forward's do.  The state before each thread's tokens has been kept, so each
-// input is read once: 7 arrays moved (dy, x, r, i; dx, dr, di) and half a
-// float16's worth of states.  Bound by instructions, some 70 an element.
+// input is read once: 7 arrays moved (dy, x, r, i; dx, dr, di) and an eighth of
+// one in float32, the states.  Bound by instructions, some 70 an element: 123 us
+// at 8 x 2048 x 2048 bfloat16, 211 us at 24593 x 2048 in 48 sequences.
 // ---------------------------------------------------------------------------
 template <typename T, int V>
 __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_grad(ScanArgs a,
