@@ -471,11 +471,11 @@ __device__ __forceinline__ void bare_barrier()
 // in registers.
 //
 // Bound by LDS and latency: a 128 tile reads each fragment for 4 others
-// (the 256 tile's hold 8).  Measured: 128 tile, weight gradient of 8192 x 4096 x 2048
-// bfloat16 155 us (885 TFLOP/s); float32 4096 x 2048 x 2048 262 us (131 TFLOP/s, the matrix
-// instructions' own 157), 25088 x 256 x 128 with bias and ReLU6 25 us, of which
-// 8 are its bytes: a tile has 4 steps, so its beginning and end are not hidden.  64 tile
-// with 4 stages: 1024^3 8.9 us.
+// (the 256 tile's hold 8).  Measured: 128 tile, weight gradient of 8192 x 4096 x
+// 2048 bfloat16 155 us (885 TFLOP/s), float32 4096 x 2048 x 2048 262 us (131
+// TFLOP/s, the matrix instructions' own 157); 64 tile, float32 25088 x 256 x 128
+// with bias and ReLU6 22.5 us, of which 8 are its bytes: a tile has 4 steps, so
+// its beginning and end are not hidden; with 4 stages, bfloat16 1024^3 8.9 us.
 // ---------------------------------------------------------------------------
 template <typename T, bool PR, bool QR, bool DIRECT, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, int tiles_n,
@@ -978,9 +978,23 @@ __global__ __launch_bounds__(256) void k_gemm_sum(Product a, int groups)
     float sum[4], b[4] = {};
     const float *part = a.f.part + (long long)m * a.N + n;
     get(part, width, sum);
-    for (int k = 1; k < a.splits; ++k) {
+    const long long next = (long long)a.M * a.N;
+    int k = 1;
+    constexpr int kAhead = 8;       // loads on their way
+    for (; k + kAhead <= a.splits; k += kAhead) {
+        float v[kAhead][4];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            get(part + (k + u) * next, width, v[u]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum[e] += v[u][e];
+    }
+    for (; k < a.splits; ++k) {
         float v[4];
-        get(part + (long long)k * a.M * a.N, width, v);
+        get(part + k * next, width, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             sum[e] += v[e];

@@ -2,6 +2,8 @@
 // its gradients (include/dwconv_seq.h).
 #include "dwseq_gemm.h"
 
+#include <cmath>
+
 namespace dwseq {
 namespace {
 
@@ -109,7 +111,9 @@ GemmPlan gemm_plan(int size, int across, int M, int N, int K)
     GemmPlan best{TILE_64, 1};
     double least = 1e30;
     for (int t = 0; t < count; ++t)
-        for (int splits = 1; splits <= 16; splits *= 2) {
+        // up to 128 for the weight gradient of a narrow layer over many rows (100000 x
+        // 48 x 64 float32: 160 us with 16, 36 with 128)
+        for (int splits = 1; splits <= 128; splits *= 2) {
             const Shape &s = shapes[t];
             const double sums = 4.0 * M * N * splits;       // bytes of partial sums
             if (splits > 1 && (steps < 4 * splits || sums > 64e6))
@@ -121,7 +125,11 @@ GemmPlan gemm_plan(int size, int across, int M, int N, int K)
                                              : 2.0 * groups / cus - 1.0;
             const double part = load < 0.0 ? 0.0 : load > 1.0 ? 1.0 : load;
             const double step = s.alone[across] + (s.full[across] - s.alone[across]) * part;
-            const double rounds = (double)cdiv((long long)groups, (long long)cus * s.per_cu);
+            // float32's small workgroups follow each other without rounds: their time is
+            // the matrix instructions' (25088 x 256 x 128: 64 tile 25.9 us, 128 tile 27.7;
+            // counted so, bfloat16 would lose: 12.3 against 11.4)
+            const double fill = groups / (cus * s.per_cu);
+            const double rounds = size == 4 && s.per_cu > 2 && fill > 1.0 ? fill : std::ceil(fill);
             double time = rounds * (cdiv(steps, splits) * step + s.ends);
             if (splits > 1)
                 time += 3.0 + sums * 2.0 / 4e6;

@@ -387,6 +387,9 @@ LINEAR_CASES = [
     (256, 512, 1024, "silu", True, True, False),
     (31, 1024, 2048, "none", True, False, False),
     (0, 8, 8, "none", True, False, False),
+    (20011, 70, 90, "silu", True, True, False),     # many ranges of rows in dw
+    (520, 300, 64, "relu6", True, True, False),     # a tile's last columns by vectors
+    (260, 515, 96, "silu", True, True, True),       # and by elements
 ]
 
 
