@@ -12,10 +12,10 @@
 // Measured, with inputs from HBM: forward, 8 x 4096 x 2048 bfloat16, 4 taps and
 // SiLU, 60 us (4.5 TB/s; a copy of the same bytes 50); 20011 x 1000 float32 in 37
 // sequences 37.5 us (4.3 TB/s); gradient, 16411 x 1536 float16 in 23 sequences,
-// 46 us with its sums (3.3 TB/s), bound by the vector unit's some 60 operations an element
-// as much as by HBM; single tokens, 64 x 2048, 3 us, a launch.  4
-// channels a thread in the forward take 55 us where 8 take 67 (fewer waves); in the
-// gradient 2 take 116 where 4 take 145 (8 x 4096 x 2048; registers).
+// 44 us with its sums (3.5 TB/s), bound by the vector unit's some 50 operations
+// an element as much as by HBM; single tokens, 64 x 2048, 3 us, a launch.  4
+// channels a thread in the forward took 55 us where 8 took 67 (fewer waves); in
+// the gradient 2 took 116 where 4 took 145 (8 x 4096 x 2048; registers; 108 since).
 #include "dwseq_device.h"
 
 namespace dwseq {
@@ -285,11 +285,27 @@ __global__ __launch_bounds__(kThreads) void k_causal_grad(CausalArgs a, int grou
                 load<T, V>(x + (long long)(t0 - (K - 1) + j) * a.ldx, ext[j]);
         Walk at(a.batch, t0);
         Raw<T, V> xs[kGradAhead], dys[kGradAhead];
+        // (a row's address is a 64-bit product, as dear as the row's arithmetic: one
+        // for all rows where none of them needs to be held back)
         auto fetch = [&](int t) {
+            const int row = min(t, t2 - 1);
+            const T *px = x + row * a.ldx, *pd = dy + row * a.lddy;
+            if (t + kGradAhead <= t2) {
 #pragma unroll
-            for (int u = 0; u < kGradAhead; ++u) {
-                xs[u].load(x + (long long)min(t + u, t2 - 1) * a.ldx);
-                dys[u].load(dy + (long long)min(t + u, t2 - 1) * a.lddy);
+                for (int u = 0; u < kGradAhead; ++u) {
+                    xs[u].load(px + u * a.ldx);
+                    dys[u].load(pd + u * a.lddy);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kGradAhead; ++u) {
+                    xs[u].load(px);
+                    dys[u].load(pd);
+                    if (t + u + 1 < t2) {
+                        px += a.ldx;
+                        pd += a.lddy;
+                    }
+                }
             }
         };
         fetch(t0);
@@ -379,11 +395,17 @@ __global__ __launch_bounds__(kThreads) void k_causal_grad(CausalArgs a, int grou
                 }
             }
             // rows K-1 places back are complete; the windows move on
+            const int done = t - (K - 1);
+            T *to = dx + done * a.lddx;
+            if (done >= t0 && done + kGradAhead <= t1) {
 #pragma unroll
-            for (int u = 0; u < kGradAhead; ++u) {
-                const int done = t + u - (K - 1);
-                if (done >= t0 && done < t1)
-                    store<T, V>(dx + (long long)done * a.lddx, acc[u]);
+                for (int u = 0; u < kGradAhead; ++u)
+                    store<T, V>(to + u * a.lddx, acc[u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kGradAhead; ++u)
+                    if (done + u >= t0 && done + u < t1)
+                        store<T, V>(to + u * a.lddx, acc[u]);
             }
 #pragma unroll
             for (int j = 0; j < K - 1 + kGradAhead; ++j)
@@ -552,7 +574,7 @@ int launch_causal_step(const CausalArgs &a, void *stream)
 
 // Chunks of 64 tokens, shorter where there would be too few workgroups, longer
 // where there would be more than 512 rows of partial sums.  Measured on 8 x 4096 x
-// 2048 bfloat16, 4 taps (floor 75 us): 64 tokens and 2 channels a thread with the
+// 2048 bfloat16, 4 taps (floor 75 us; 108 by now): 64 tokens and 2 channels a thread with the
 // next rows in flight 115.7 us; 32 tokens 129.4; 4 channels 130.6; 8 rows ahead
 // 124.6; without the next rows in flight 152.
 CausalGradPlan causal_grad_plan(int rows, int C)
