@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdio>
 
 using namespace dwseq;
 
@@ -423,6 +424,25 @@ int dwconv_linear_workspace_size(int grad, int type, int act, long long M, int N
     if (M < 0 || M > 0x7fffffffLL || N < 1 || K < 1)
         return DWCONV_ERR_BAD_DIM;
     *bytes = linear_workspace(grad != 0, type, act, (int)M, N, K);
+    return DWCONV_OK;
+}
+
+int dwconv_linear_describe(int product, int type, int aligned, long long M, int N, int K,
+                           char *name, int name_len, int *splits)
+{
+    if (product < DWCONV_LINEAR_Y || product > DWCONV_LINEAR_DW)
+        return DWCONV_ERR_BAD_OP;
+    long long bytes = 0;
+    const int st = dwconv_linear_workspace_size(1, type, DWCONV_ACT_NONE, M, N, K, &bytes);
+    if (st != DWCONV_OK)
+        return st;
+    const char *kernel = "";
+    int ranges = 0;
+    linear_describe(product, type, aligned != 0, (int)M, N, K, &kernel, &ranges);
+    if (name && name_len > 0)
+        std::snprintf(name, (size_t)name_len, "%s", kernel);
+    if (splits)
+        *splits = ranges;
     return DWCONV_OK;
 }
 

@@ -59,6 +59,34 @@ struct Product {
 
 template <typename T> int launch_gemm(const Product &p, hipStream_t st);
 
+// Whether an operand's chunks can go to LDS directly.
+inline bool direct_ok(const void *p, long long ld, bool rows_k, int K, int size)
+{
+    return (reinterpret_cast<std::uintptr_t>(p) % 16) == 0 && (ld * size) % 16 == 0 &&
+           (rows_k || ((long long)K * size) % 16 == 0);
+}
+
+// The kernel that runs for a plan's tile: the 256 tile is for 16-bit operands
+// that go to LDS directly, and so is the deep ring.
+inline GemmTile tile_taken(GemmTile tile, bool direct, int size)
+{
+    if (direct && size == 2)
+        return tile;
+    return tile == TILE_256 ? TILE_128 : tile == TILE_64_DEEP ? TILE_64 : tile;
+}
+
+// The length of k's ranges for a plan's number of them, and how many of these
+// there are: a multiple of a step's length, none of them empty.
+inline int split_length(int K, int splits, int size)
+{
+    const int step = kStepBytes / size;
+    return (int)(cdiv(cdiv(K, step), splits) * step);
+}
+inline int split_count(int K, int splits, int size)
+{
+    return K ? (int)cdiv(K, split_length(K, splits, size)) : 1;
+}
+
 #ifdef DWSEQ_GEMM_KERNELS
 namespace {
 
@@ -1007,26 +1035,17 @@ __global__ __launch_bounds__(256) void k_gemm_sum(Product a, int groups)
     finish<T>(a.f, m, n, width, b, r, sum);
 }
 
-// Whether an operand's chunks can go to LDS directly.
-inline bool direct_ok(const void *p, long long ld, bool rows_k, int K, int size)
-{
-    const bool even = (reinterpret_cast<std::uintptr_t>(p) % 16) == 0 && (ld * size) % 16 == 0 &&
-                      (rows_k || ((long long)K * size) % 16 == 0);
-    return even;
-}
-
 }  // namespace
 
 template <typename T> int launch_gemm(const Product &product, hipStream_t st)
 {
     constexpr int size = (int)sizeof(T), step = kStepBytes / size;
     Product a = product;
-    const int k_per_split = (int)(cdiv(cdiv(a.K, step), a.splits) * step);
-    a.splits = a.K ? (int)cdiv(a.K, k_per_split) : 1;      // none of them empty
+    const int k_per_split = split_length(a.K, a.splits, size);
+    a.splits = split_count(a.K, a.splits, size);
     if (a.splits == 1)
         a.f.part = nullptr;
-    const int tile = a.tile;
-    if (tile == FEW_ROWS) {
+    if (a.tile == FEW_ROWS) {
         const int k_per_wave = (int)(cdiv(a.K, kFewWaves * step) * step);
         auto few = [&](auto mf) {
             return dwconv::launch_kernel(k_few_rows<T, decltype(mf)::value>,
@@ -1041,6 +1060,7 @@ template <typename T> int launch_gemm(const Product &product, hipStream_t st)
     }
     const bool direct = direct_ok(a.p, a.ldp, a.p_rows_k, a.K, size) &&
                         direct_ok(a.q, a.ldq, a.q_rows_k, a.K, size);
+    const GemmTile tile = tile_taken(a.tile, direct, size);
     auto run = [&](auto pr, auto qr, auto dir, auto bm, auto bn, auto wm, auto wn, auto stages) {
         constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
         constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
@@ -1067,13 +1087,12 @@ template <typename T> int launch_gemm(const Product &product, hipStream_t st)
             }
         }
         switch (tile) {
-        case TILE_256:
         case TILE_128:
             return run(pr, qr, dir, integral_constant<int, 128>(), integral_constant<int, 128>(),
                        integral_constant<int, 2>(), integral_constant<int, 2>(),
                        integral_constant<int, 2>());
         case TILE_64_DEEP:
-            if constexpr (size == 2)
+            if constexpr (decltype(dir)::value && size == 2)
                 return run(pr, qr, dir, integral_constant<int, 64>(), integral_constant<int, 64>(),
                            integral_constant<int, 2>(), integral_constant<int, 2>(),
                            integral_constant<int, 4>());

@@ -72,6 +72,8 @@ struct LinearArgs {
     int M, N, K;
 };
 long long linear_workspace(bool grad, int type, int act, int M, int N, int K);
+void linear_describe(int product, int type, bool aligned, int M, int N, int K, const char **name,
+                     int *splits);
 int launch_linear_fwd(const LinearArgs &a, void *stream);
 int launch_linear_grad(const LinearArgs &a, void *stream);
 

@@ -10,6 +10,13 @@ namespace {
 // dz = dy * act'(z), and its column sums over a strip of rows (db): a workgroup
 // takes 32 vectors of V columns, its 8 rows of threads every 8th row of the
 // strip each.  Bound by HBM: 8192 x 4096 bfloat16 with SiLU 48.5 us, 4.1 TB/s.
+//
+// dz is stored in the tensors' type, since the matrix instructions of the two
+// products that read it take their operands in one type: a second part for what the
+// rounding loses would double their work.  It is the only loss beside the results' own
+// rounding: 8192 x 4096 x 2048 bfloat16 is 2.35e-3 from 64 bits (root mean
+// square), where results rounded from an exact sum are 1.66e-3, and sqrt(2) of that
+// is 2.35e-3.  db sums dz before the rounding.
 constexpr int kDzLanes = 32, kDzSlots = 8;
 
 struct DzPlan {
@@ -188,6 +195,25 @@ long long linear_workspace(bool grad, int type, int act, int M, int N, int K)
         return gemm_workspace(elem_size(type), 0, M, N, K);
     const GradSpace g = grad_space(type, act, M, N, K);
     return g.dz + g.db + g.sums;
+}
+
+void linear_describe(int product, int type, bool aligned, int M, int N, int K, const char **name,
+                     int *splits)
+{
+    // rows, columns and sum of the product, and the operands that are read across k
+    const int size = elem_size(type), across = product;
+    const int m = product == 2 ? N : M, n = product == 0 ? N : K;
+    const int k = product == 0 ? K : product == 1 ? N : M;
+    const GemmPlan plan = gemm_plan(size, across, m, n, k);
+    const bool direct = aligned && (across == 2 || direct_ok(nullptr, 0, false, k, size));
+    *splits = split_count(k, plan.splits, size);
+    switch (tile_taken(plan.tile, direct, size)) {
+    case FEW_ROWS: *name = "few_rows"; break;
+    case TILE_256: *name = "tile_256"; break;
+    case TILE_128: *name = direct ? "tile_128" : "tile_128_registers"; break;
+    case TILE_64: *name = direct ? "tile_64" : "tile_64_registers"; break;
+    case TILE_64_DEEP: *name = "tile_64_deep"; break;
+    }
 }
 
 int launch_linear_fwd(const LinearArgs &a, void *stream)

@@ -32,15 +32,18 @@ torch = None                 # imported by the first call
 T_F32, T_F16, T_BF16 = 0, 1, 2
 CAUSAL_MAX_TAPS = 8          # DWCONV_CAUSAL_MAX_TAPS
 SCAN_RUN = 8                # DWCONV_SCAN_RUN
+LINEAR_Y, LINEAR_DX, LINEAR_DW = 0, 1, 2     # DWCONV_LINEAR_*
 
 SEQ_EXPORTS = ("dwconv_causal_fwd", "dwconv_causal_step", "dwconv_causal_grad_workspace_size",
                "dwconv_causal_grad", "dwconv_scan_states_size", "dwconv_scan_workspace_size",
                "dwconv_scan_fwd", "dwconv_scan_step", "dwconv_scan_grad",
-               "dwconv_linear_workspace_size", "dwconv_linear_fwd", "dwconv_linear_grad")
+               "dwconv_linear_workspace_size", "dwconv_linear_describe", "dwconv_linear_fwd",
+               "dwconv_linear_grad")
 
 __all__ = ["causal_conv", "causal_conv_step", "causal_conv_grad", "gated_scan",
            "gated_scan_step", "gated_scan_grad", "linear", "linear_grad", "T_F32", "T_F16",
-           "T_BF16", "CAUSAL_MAX_TAPS", "SCAN_RUN", "SEQ_EXPORTS", *SEQ_EXPORTS]
+           "T_BF16", "CAUSAL_MAX_TAPS", "SCAN_RUN", "LINEAR_Y", "LINEAR_DX", "LINEAR_DW",
+           "SEQ_EXPORTS", *SEQ_EXPORTS]
 
 
 def declare(L):
@@ -61,6 +64,8 @@ def declare(L):
     L.dwconv_scan_grad.argtypes = [*row * 4, i, vp, f, vp, vp, *row * 3, vp, vp, vp, ll, *seq, i,
                                    vp]
     L.dwconv_linear_workspace_size.argtypes = [i, i, i, ll, i, i, out]
+    L.dwconv_linear_describe.argtypes = [i, i, i, ll, i, i, ctypes.c_char_p, i,
+                                         ctypes.POINTER(i)]
     L.dwconv_linear_fwd.argtypes = [*row * 2, i, vp, i, *row * 3, vp, ll, ll, i, i, vp]
     L.dwconv_linear_grad.argtypes = [*row * 3, i, i, *row * 3, vp, vp, ll, ll, i, i, vp]
     for name in SEQ_EXPORTS:
@@ -498,6 +503,18 @@ def dwconv_linear_workspace_size(grad, dtype, act, M, N, K):
         _setup()
     return _size("dwconv_linear_workspace_size", int(bool(grad)), _types.get(dtype, -1),
                  _act(act), M, N, K)
+
+
+def dwconv_linear_describe(product, dtype, M, N, K, aligned=True):
+    """(kernel, ranges of the summed index) of LINEAR_Y, LINEAR_DX or LINEAR_DW;
+    aligned: both operands' addresses and row strides are multiples of 16 bytes."""
+    if torch is None:
+        _setup()
+    name, splits = ctypes.create_string_buffer(64), ctypes.c_int(0)
+    _status(_library().dwconv_linear_describe(product, _types.get(dtype, -1), int(bool(aligned)),
+                                              M, N, K, name, 64, ctypes.byref(splits)),
+            "dwconv_linear_describe")
+    return name.value.decode(), splits.value
 
 
 def dwconv_linear_fwd(x, w, b, y, act="none", res=None, z=None, workspace=None, stream=None):

@@ -168,6 +168,17 @@ int dwconv_linear_grad(const void *dy, long long lddy, const void *x, long long 
                        float *db, void *workspace, long long workspace_bytes, long long M, int N,
                        int K, void *stream);
 
+/* Describe, without touching the GPU, the kernel of one product of these calls:
+ * y, dx or dw.  Writes its name (NUL-terminated, at most name_len bytes) and over
+ * how many ranges of the summed index it is split, each where not NULL.
+ * aligned: whether the addresses and row strides of both operands are multiples
+ * of 16 bytes (dz, where there is an activation, is dense). */
+#define DWCONV_LINEAR_Y  0
+#define DWCONV_LINEAR_DX 1
+#define DWCONV_LINEAR_DW 2
+int dwconv_linear_describe(int product, int type, int aligned, long long M, int N, int K,
+                           char *name, int name_len, int *splits);
+
 #ifdef __cplusplus
 }
 #endif
