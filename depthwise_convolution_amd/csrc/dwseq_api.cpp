@@ -105,10 +105,10 @@ bool act_ok(int act) { return act >= DWCONV_ACT_NONE && act <= DWCONV_ACT_SILU; 
 // Rows of a batch: DWCONV_OK and *b, or what is wrong.
 int make_batch(int seqs, long long tokens, const int *offsets, bool packed, Batch *b)
 {
-    if (seqs < 1 || tokens < 0)
+    if (seqs < 1 || seqs > DWCONV_SEQ_MAX_ROWS || tokens < 0 || tokens > DWCONV_SEQ_MAX_ROWS)
         return DWCONV_ERR_BAD_DIM;
-    const long long rows = packed ? tokens : (tokens > 0x7fffffffLL ? tokens : tokens * seqs);
-    if (rows > 0x7fffffffLL)
+    const long long rows = packed ? tokens : tokens * seqs;
+    if (rows > DWCONV_SEQ_MAX_ROWS)
         return DWCONV_ERR_BAD_DIM;
     if (offsets && !aligned(offsets, 4))
         return DWCONV_ERR_MISALIGNED;
@@ -421,7 +421,7 @@ int dwconv_linear_workspace_size(int grad, int type, int act, long long M, int N
         return DWCONV_ERR_BAD_WTYPE;
     if (!act_ok(act))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (M < 0 || M > 0x7fffffffLL || N < 1 || K < 1)
+    if (M < 0 || M > DWCONV_SEQ_MAX_ROWS || N < 1 || K < 1)
         return DWCONV_ERR_BAD_DIM;
     *bytes = linear_workspace(grad != 0, type, act, (int)M, N, K);
     return DWCONV_OK;

@@ -31,6 +31,7 @@ torch = None                 # imported by the first call
 
 T_F32, T_F16, T_BF16 = 0, 1, 2
 CAUSAL_MAX_TAPS = 8          # DWCONV_CAUSAL_MAX_TAPS
+SEQ_MAX_ROWS = (1 << 31) - (1 << 16)         # DWCONV_SEQ_MAX_ROWS
 SCAN_RUN = 8                # DWCONV_SCAN_RUN
 LINEAR_Y, LINEAR_DX, LINEAR_DW = 0, 1, 2     # DWCONV_LINEAR_*
 
@@ -42,7 +43,7 @@ SEQ_EXPORTS = ("dwconv_causal_fwd", "dwconv_causal_step", "dwconv_causal_grad_wo
 
 __all__ = ["causal_conv", "causal_conv_step", "causal_conv_grad", "gated_scan",
            "gated_scan_step", "gated_scan_grad", "linear", "linear_grad", "T_F32", "T_F16",
-           "T_BF16", "CAUSAL_MAX_TAPS", "SCAN_RUN", "LINEAR_Y", "LINEAR_DX", "LINEAR_DW",
+           "T_BF16", "CAUSAL_MAX_TAPS", "SEQ_MAX_ROWS", "SCAN_RUN", "LINEAR_Y", "LINEAR_DX", "LINEAR_DW",
            "SEQ_EXPORTS", *SEQ_EXPORTS]
 
 

@@ -20,8 +20,10 @@
  * clamp what they read.  tokens = 0 is allowed (pointers to arrays of no row
  * may then be NULL).
  *
- * Rows in all, outputs and inputs of a linear map: fewer than 2^31 each.
- * Addresses are computed in 64 bits.  Pointers are aligned to their element.
+ * Rows in all, and sequences: at most DWCONV_SEQ_MAX_ROWS each (the kernels
+ * count both in 32 bits and look some way ahead of the last one); outputs and
+ * inputs of a linear map: fewer than 2^31.  Addresses are computed in 64 bits.
+ * Pointers are aligned to their element.
  *
  * Arrays that are written must not overlap each other or an input, except
  * where an in-place update is named; two column ranges of one wider array
@@ -44,6 +46,8 @@ extern "C" {
 #define DWCONV_T_F32  0
 #define DWCONV_T_F16  1   /* IEEE binary16 */
 #define DWCONV_T_BF16 2   /* bfloat16      */
+
+#define DWCONV_SEQ_MAX_ROWS 2147418112   /* 2^31 - 2^16 */
 
 #define DWCONV_CAUSAL_MAX_TAPS 8   /* taps of the causal filter: 1 .. 8 */
 
