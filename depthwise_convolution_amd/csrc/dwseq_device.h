@@ -207,7 +207,7 @@ __device__ __forceinline__ int seq_of(const Batch &b, int row)
         return min(row / max(b.tokens, 1), b.seqs - 1);
     int lo = 0, hi = b.seqs - 1;
     while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
+        const int mid = lo + ((hi - lo + 1) >> 1);
         if (seq_start(b, mid) <= row)
             lo = mid;
         else

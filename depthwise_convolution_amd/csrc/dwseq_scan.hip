@@ -107,7 +107,8 @@ __device__ __forceinline__ float input_factor(float m)
 // its number among all runs (ScanPlan); `any` is false for a number that no run
 // has.  A sequence of no token has one run, of none.
 struct Run {
-    int s, q, count, t0, t1, item, state_row;
+    int s, q, count, t0, t1, item;
+    long long state_row;
     bool any, first, last;
 };
 
@@ -154,7 +155,7 @@ __device__ __forceinline__ Run run_of(const Batch &b, int items, int idx)
     g.last = g.q == g.count - 1;
     g.t0 = start + (g.any ? g.q * run : 0);
     g.t1 = g.t0 + (g.any ? min(run, len - g.q * run) : 0);
-    g.state_row = start / kKept + g.s + (g.t0 - start) / kKept;
+    g.state_row = (long long)(start / kKept) + g.s + (g.t0 - start) / kKept;
     return g;
 }
 
@@ -496,7 +497,7 @@ __global__ __launch_bounds__(Layout<V>::threads, 3) void k_scan_fwd(ScanArgs a, 
     for (int v = 0; v < V; ++v)
         hk[v] = fmaf(A[v], carry[lane * V + v], B[v]);
     if (a.states && mt < g.t1)
-        store<float, V>(a.states + (long long)(g.state_row + group) * C + c0, hk);
+        store<float, V>(a.states + (g.state_row + group) * C + c0, hk);
     const __amdgpu_buffer_rsrc_t out = y.run(g.t0, rows);
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
@@ -556,7 +557,7 @@ __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_gra
     x.fetch(px, g.t0, rows);
     float rate[V], hk[V] = {};
     if (mt < g.t1)
-        load<float, V>(a.states_in + (long long)(g.state_row + group) * C + c0, hk);
+        load<float, V>(a.states_in + (g.state_row + group) * C + c0, hk);
     load<float, V>(a.lam + c0, rate);
 #pragma unroll
     for (int v = 0; v < V; ++v)

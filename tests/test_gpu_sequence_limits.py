@@ -72,6 +72,21 @@ def test_causal_conv_of_the_most_rows(torch):
         assert abs(got - exact) <= 2.0 ** -20 * abs(exact) + 1, (got, exact)
 
 
+def test_causal_conv_of_many_sequences(torch):
+    """More than 2^30 sequences, all but the last of no token."""
+    seqs, n, C = (1 << 30) + 9, 1000, 8
+    print(f"\n[case] causal_conv {seqs} sequences", flush=True)
+    gen = _gen(torch)
+    x = _whole(torch, gen, n, C)
+    w = torch.randint(-2, 3, (C, 4), generator=gen, device="cuda").float()
+    offsets = torch.zeros(seqs + 1, dtype=torch.int32, device="cuda")
+    offsets[-1] = n
+    y = dw.dwconv_causal_fwd(x, w, None, torch.full_like(x, float("nan")), offsets=offsets)
+    want, _ = dw.causal_conv(x[None], w)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0])
+
+
 def test_linear_gradient_over_the_most_rows(torch):
     """dz, dw and db, where the rows are the summed index: a few rows that are
     not zero, the last ones among them."""
