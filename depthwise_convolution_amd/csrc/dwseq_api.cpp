@@ -138,7 +138,7 @@ int check_causal(int type, int wtype, int act, int C, int K)
         return DWCONV_ERR_BAD_WTYPE;
     if (!act_ok(act))
         return DWCONV_ERR_BAD_EPILOGUE;
-    if (C < 1 || K < 1 || K > DWCONV_CAUSAL_MAX_TAPS)
+    if (C < 1 || C > DWCONV_SEQ_MAX_ROWS || K < 1 || K > DWCONV_CAUSAL_MAX_TAPS)
         return DWCONV_ERR_BAD_DIM;
     return DWCONV_OK;
 }

@@ -106,11 +106,11 @@ __global__ __launch_bounds__(kThreads) void k_causal_fwd(CausalArgs a, int group
 {
     const T *x = static_cast<const T *>(a.x);
     const T *init = static_cast<const T *>(a.init);
-    if ((int)blockIdx.x >= main_blocks) {
-        long long id = (long long)(blockIdx.x - main_blocks) * kThreads + threadIdx.x;
+    if (block_id() >= (unsigned)main_blocks) {
+        long long id = (long long)(block_id() - main_blocks) * kThreads + threadIdx.x;
         const int c0 = first_channel<V>((int)(id % groups), a.C);
         id /= groups;
-        if (K == 1 || id >= (long long)a.batch.seqs * (K - 1))
+        if (K == 1 || !a.final_state || id >= (long long)a.batch.seqs * (K - 1))
             return;
         const int s = (int)(id / max(K - 1, 1)), j = (int)(id % max(K - 1, 1));
         const int start = seq_start(a.batch, s);
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void k_causal_fwd(CausalArgs a, int group
         store<T, V>(static_cast<T *>(a.final_state) + id * a.C + c0, f);
         return;
     }
-    const unsigned id = blockIdx.x * kThreads + threadIdx.x;
+    const unsigned id = block_id() * kThreads + threadIdx.x;
     const unsigned ck = id / (unsigned)groups;
     if (ck >= (unsigned)chunks)
         return;
@@ -226,10 +226,10 @@ __device__ __forceinline__ void step_vector(const CausalArgs &a, int s, int c0)
 template <typename T, int V, int K>
 __global__ __launch_bounds__(kThreads) void k_causal_step(CausalArgs a, int groups)
 {
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int s = (int)(id / groups), c0 = (int)(id % groups) * V;
-    if (s >= a.batch.seqs)
+    const long long id = (long long)block_id() * kThreads + threadIdx.x;
+    if (id >= (long long)a.batch.seqs * groups)
         return;
+    const int s = (int)(id / groups), c0 = (int)(id % groups) * V;
     if (c0 + V <= a.C)
         step_vector<T, V, K>(a, s, c0);
     else
@@ -458,12 +458,12 @@ __global__ __launch_bounds__(1024) void k_causal_grad_sum(const float *part, int
 template <typename T, int K>
 __global__ __launch_bounds__(kThreads) void k_causal_grad_init(CausalArgs a)
 {
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long id = (long long)block_id() * kThreads + threadIdx.x;
     const int c = (int)(id % a.C);
     const long long sq = id / a.C;
-    const int s = (int)(sq / (K - 1)), q = (int)(sq % (K - 1));
-    if (s >= a.batch.seqs)
+    if (sq >= (long long)a.batch.seqs * (K - 1))
         return;
+    const int s = (int)(sq / (K - 1)), q = (int)(sq % (K - 1));
     const int start = seq_start(a.batch, s);
     const int len = max(seq_start(a.batch, s + 1) - start, 0);
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
@@ -551,7 +551,7 @@ int launch_causal_fwd(const CausalArgs &a, void *stream)
             return DWCONV_OK;
         if (main_blocks + rest > 0x7fffffffLL)
             return DWCONV_ERR_BAD_DIM;
-        return dwconv::launch_kernel(k_causal_fwd<T, V, K>, dim3((unsigned)(main_blocks + rest)),
+        return dwconv::launch_kernel(k_causal_fwd<T, V, K>, grid_of(main_blocks + rest),
                                      dim3(kThreads), 0, static_cast<hipStream_t>(stream), a,
                                      groups, chunk, chunks, (int)main_blocks);
     });
@@ -566,9 +566,8 @@ int launch_causal_step(const CausalArgs &a, void *stream)
         const long long blocks = cdiv((long long)a.batch.seqs * groups, kThreads);
         if (blocks > 0x7fffffffLL)
             return DWCONV_ERR_BAD_DIM;
-        return dwconv::launch_kernel(k_causal_step<T, V, K>, dim3((unsigned)blocks),
-                                     dim3(kThreads), 0, static_cast<hipStream_t>(stream), a,
-                                     groups);
+        return dwconv::launch_kernel(k_causal_step<T, V, K>, grid_of(blocks), dim3(kThreads), 0,
+                                     static_cast<hipStream_t>(stream), a, groups);
     });
 }
 
@@ -610,7 +609,7 @@ int launch_causal_grad(const CausalArgs &a, void *stream)
         });
     if (rc == DWCONV_OK)
         rc = dwconv::launch_kernel(k_causal_grad_sum,
-                                   dim3((unsigned)cdiv((long long)(a.K + 1) * a.C, 64)),
+                                   grid_of(cdiv((long long)(a.K + 1) * a.C, 64)),
                                    dim3(1024), 0, st, (const float *)a.part, p.blocks, a.C, a.K,
                                    a.dw, a.db);
     if (rc == DWCONV_OK && a.dinit && a.K > 1)
@@ -625,7 +624,7 @@ int launch_causal_grad(const CausalArgs &a, void *stream)
                         cdiv((long long)a.batch.seqs * (K - 1) * a.C, kThreads);
                     if (blocks > 0x7fffffffLL)
                         return DWCONV_ERR_BAD_DIM;
-                    return dwconv::launch_kernel(k_causal_grad_init<T, K>, dim3((unsigned)blocks),
+                    return dwconv::launch_kernel(k_causal_grad_init<T, K>, grid_of(blocks),
                                                  dim3(kThreads), 0, st, a);
                 }
             });

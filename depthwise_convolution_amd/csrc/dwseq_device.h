@@ -216,6 +216,19 @@ __device__ __forceinline__ int seq_of(const Batch &b, int row)
     return lo;
 }
 
+// A dimension of a grid holds fewer than 2^32 threads: past kGridRow workgroups
+// (of 1024 threads at most) they go on in the second dimension, the last row of
+// which may have some too many.  A multiple of the XCDs.
+constexpr unsigned kGridRow = 1u << 21;
+
+inline dim3 grid_of(long long blocks)
+{
+    return blocks <= kGridRow ? dim3((unsigned)blocks)
+                              : dim3(kGridRow, (unsigned)cdiv(blocks, kGridRow));
+}
+
+__device__ __forceinline__ unsigned block_id() { return blockIdx.y * kGridRow + blockIdx.x; }
+
 // Sum of the rows of part[rows][n] per column in a fixed order: a workgroup
 // takes 64 columns, its 16 waves every 16th row each, added up in LDS.  The
 // sums go to f(column, sum).
@@ -224,7 +237,7 @@ __device__ __forceinline__ void column_sums(const float *part, int rows, long lo
 {
     __shared__ float lds[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const long long col = (long long)blockIdx.x * 64 + lane;
+    const long long col = (long long)block_id() * 64 + lane;
     float s = 0.0f;
     if (col < n)
 #pragma unroll 4

@@ -463,6 +463,15 @@ __device__ __forceinline__ void finish(const Finish &f, const Block<T, V, CUT> &
     y.store(s, line, row, col);
 }
 
+// The tiles' grid: x, and past kGridRow tiles z too; y numbers the ranges of k.
+// The number of this workgroup's tile may be one too many.
+inline dim3 tile_grid(long long tiles, int splits)
+{
+    const dim3 g = grid_of(tiles);
+    return dim3(g.x, (unsigned)splits, g.y);
+}
+__device__ __forceinline__ int tile_id() { return (int)(blockIdx.z * kGridRow + blockIdx.x); }
+
 // Tile of workgroup b: each XCD (b % 8) takes a contiguous range of the tiles,
 // which are numbered in bands of 8 tile rows, down the band first, so that the
 // tiles at work in one XCD share rows of P and Q in its L2.
@@ -519,8 +528,10 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, in
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int split = blockIdx.y, k_first = split * k_per_split;
     const int k_last = min(k_first + k_per_split, a.K);
+    if (tile_id() >= tiles_m * tiles_n)
+        return;
     int tm, tn;
-    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    tile_of(tile_id(), tiles_m, tiles_n, tm, tn);
     const P p(a.p, a.ldp, tm * BM, a.M, k_last);
     const Q q(a.q, a.ldq, tn * BN, a.N, k_last);
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
@@ -720,8 +731,10 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int split = blockIdx.y, k_first = split * k_per_split;
     const int k_last = min(k_first + k_per_split, a.K);
+    if (tile_id() >= tiles_m * tiles_n)
+        return;
     int tm, tn;
-    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    tile_of(tile_id(), tiles_m, tiles_n, tm, tn);
     const P p0(a.p, a.ldp, tm * 256, a.M, k_last), p1(a.p, a.ldp, tm * 256 + 128, a.M, k_last);
     const Q q0(a.q, a.ldq, tn * 256, a.N, k_last), q1(a.q, a.ldq, tn * 256 + 128, a.N, k_last);
     const int wm = (wave & 3) * 32, wn = (wave >> 2) * 64;
@@ -1070,8 +1083,8 @@ template <typename T> int launch_gemm(const Product &product, hipStream_t st)
         return dwconv::launch_kernel(
             k_gemm<T, decltype(pr)::value, decltype(qr)::value, decltype(dir)::value, BM, BN, WM,
                    WN, decltype(dir)::value ? decltype(stages)::value : 2>,
-            dim3((unsigned)(tiles_m * tiles_n), (unsigned)a.splits), dim3(WM * WN * 64), 0, st, a,
-            (int)tiles_m, (int)tiles_n, k_per_split);
+            tile_grid(tiles_m * tiles_n, a.splits), dim3(WM * WN * 64), 0, st, a, (int)tiles_m,
+            (int)tiles_n, k_per_split);
     };
     auto sized = [&](auto pr, auto qr, auto dir) {
         using std::integral_constant;
@@ -1082,8 +1095,8 @@ template <typename T> int launch_gemm(const Product &product, hipStream_t st)
                     return (int)DWCONV_ERR_BAD_DIM;
                 return dwconv::launch_kernel(
                     k_gemm_256<T, decltype(pr)::value, decltype(qr)::value>,
-                    dim3((unsigned)(tiles_m * tiles_n), (unsigned)a.splits), dim3(512), 0, st, a,
-                    (int)tiles_m, (int)tiles_n, k_per_split);
+                    tile_grid(tiles_m * tiles_n, a.splits), dim3(512), 0, st, a, (int)tiles_m,
+                    (int)tiles_n, k_per_split);
             }
         }
         switch (tile) {

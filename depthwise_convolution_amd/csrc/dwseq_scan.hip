@@ -296,9 +296,9 @@ struct Told {
 constexpr unsigned long long kUntold = ~0ull;
 
 __global__ __launch_bounds__(256) void k_scan_clear(unsigned long long *words, long long count,
-                                                    int *counter)
+                                                    unsigned *counter)
 {
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long id = (long long)block_id() * 256 + threadIdx.x;
     if (id < count)
         words[id] = kUntold;
     if (id == 0)
@@ -370,8 +370,9 @@ __device__ __forceinline__ float state_before(Told *mine, int slabs, int before)
 // data, and whatever they hold, a wait for a run with a smaller ticket ends.
 struct Chain {
     Told *told;         // nullptr: every sequence has one run
-    int *counter;
+    unsigned *counter;
     int slabs, items;
+    unsigned runs;              // slabs * items
 };
 
 __device__ __forceinline__ void tell_nothing(const Chain &ch, const Run &g, int slab)
@@ -412,14 +413,14 @@ __device__ __forceinline__ void link(const Chain &ch, const Run &g, int slab, in
     __syncthreads();
 }
 
-// The run that this workgroup takes.
-__device__ __forceinline__ int take(const Chain &ch)
+// The run that this workgroup takes; ch.runs or more: none is left for it.
+__device__ __forceinline__ unsigned take(const Chain &ch)
 {
-    __shared__ int ticket;
+    __shared__ unsigned ticket;
     if (!ch.told)
-        return blockIdx.x;
+        return block_id();
     if (threadIdx.x == 0)
-        ticket = __hip_atomic_fetch_add(ch.counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        ticket = __hip_atomic_fetch_add(ch.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(ticket);
 }
@@ -435,7 +436,10 @@ __global__ __launch_bounds__(Layout<V>::threads, 3) void k_scan_fwd(ScanArgs a, 
     constexpr int KT = L::KT;
     __shared__ float lds[L::waves][2][kSlab];
     __shared__ float total[2][kSlab], carry[kSlab];
-    const int idx = take(ch), slab = idx % ch.slabs;
+    const unsigned ticket = take(ch);
+    if (ticket >= ch.runs)
+        return;
+    const int idx = (int)ticket, slab = idx % ch.slabs;
     const Run g = run_of<false>(a.batch, ch.items, idx / ch.slabs);
     // Channels: a row that V does not divide ends with a vector moved back to its
     // end, and lanes past the row repeat it; equal values are written twice.
@@ -527,7 +531,10 @@ __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_gra
     __shared__ float lds[L::waves][2][kSlab];
     __shared__ float total[2][kSlab], carry[kSlab];
     __shared__ float sums[L::groups][kSlab];
-    const int idx = take(ch), slab = idx % ch.slabs;
+    const unsigned ticket = take(ch);
+    if (ticket >= ch.runs)
+        return;
+    const int idx = (int)ticket, slab = idx % ch.slabs;
     const Run g = run_of<true>(a.batch, ch.items, idx / ch.slabs);
     const int lane = threadIdx.x % L::lanes, group = threadIdx.x / L::lanes;
     const int C = a.C, c0 = min(slab * kSlab + lane * V, C - V);
@@ -687,10 +694,10 @@ __device__ __forceinline__ void step_vector(const ScanArgs &a, int s, int c0)
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a, int groups)
 {
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int s = (int)(id / groups), c0 = (int)(id % groups) * V;
-    if (s >= a.batch.seqs)
+    const long long id = (long long)block_id() * 256 + threadIdx.x;
+    if (id >= (long long)a.batch.seqs * groups)
         return;
+    const int s = (int)(id / groups), c0 = (int)(id % groups) * V;
     if (c0 + V <= a.C)
         step_vector<T, V>(a, s, c0);
     else
@@ -751,12 +758,13 @@ static int make_chain(const ScanPlan &p, void *space, hipStream_t st, Chain *ch)
     ch->counter = nullptr;
     if (p.items * p.slabs > 0x7fffffffLL)
         return DWCONV_ERR_BAD_DIM;
+    ch->runs = (unsigned)(p.items * p.slabs);
     if (!p.chained)
         return DWCONV_OK;
-    ch->counter = static_cast<int *>(space);
+    ch->counter = static_cast<unsigned *>(space);
     ch->told = reinterpret_cast<Told *>(static_cast<char *>(space) + 16);
     const long long words = p.words / 8;
-    return dwconv::launch_kernel(k_scan_clear, dim3((unsigned)cdiv(words, 256)), dim3(256), 0, st,
+    return dwconv::launch_kernel(k_scan_clear, grid_of(cdiv(words, 256)), dim3(256), 0, st,
                                  reinterpret_cast<unsigned long long *>(ch->told), words,
                                  ch->counter);
 }
@@ -772,7 +780,7 @@ int launch_scan_fwd(const ScanArgs &a, void *stream)
     return with_variant(a, [&](auto *t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(v)::value;
-        return dwconv::launch_kernel(k_scan_fwd<T, V>, dim3((unsigned)(p.items * p.slabs)),
+        return dwconv::launch_kernel(k_scan_fwd<T, V>, grid_of(p.items * p.slabs),
                                      dim3(Layout<V>::threads), 0, st, a, ch);
     });
 }
@@ -791,7 +799,7 @@ int launch_scan_grad(const ScanArgs &args, void *stream)
     rc = with_variant(a, [&](auto *t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(v)::value;
-        return dwconv::launch_kernel(k_scan_grad<T, V>, dim3((unsigned)(p.items * p.slabs)),
+        return dwconv::launch_kernel(k_scan_grad<T, V>, grid_of(p.items * p.slabs),
                                      dim3(Layout<V>::threads), 0, st, a, ch);
     });
     if (rc == DWCONV_OK)
@@ -810,7 +818,7 @@ int launch_scan_step(const ScanArgs &a, void *stream)
         const long long blocks = cdiv((long long)a.batch.seqs * groups, 256);
         if (blocks > 0x7fffffffLL)
             return DWCONV_ERR_BAD_DIM;
-        return dwconv::launch_kernel(k_scan_step<T, V>, dim3((unsigned)blocks), dim3(256), 0,
+        return dwconv::launch_kernel(k_scan_step<T, V>, grid_of(blocks), dim3(256), 0,
                                      static_cast<hipStream_t>(stream), a, groups);
     });
 }

@@ -20,8 +20,8 @@
  * clamp what they read.  tokens = 0 is allowed (pointers to arrays of no row
  * may then be NULL).
  *
- * Rows in all, and sequences: at most DWCONV_SEQ_MAX_ROWS each (the kernels
- * count both in 32 bits and look some way ahead of the last one); outputs and
+ * Rows in all, sequences, and channels: at most DWCONV_SEQ_MAX_ROWS each (the
+ * kernels count them in 32 bits and look some way ahead of the last one); outputs and
  * inputs of a linear map: fewer than 2^31.  Addresses are computed in 64 bits.
  * Pointers are aligned to their element.
  *
