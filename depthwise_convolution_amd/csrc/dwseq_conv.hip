@@ -128,7 +128,10 @@ __global__ __launch_bounds__(kThreads) void k_causal_fwd(CausalArgs a, int group
     if (ck >= (unsigned)chunks)
         return;
     const int c0 = first_channel<V>((int)(id - ck * (unsigned)groups), a.C);
-    const int t0 = (int)ck * chunk, t1 = t0 + min(chunk, a.batch.rows - t0);
+    // (rows are at most 2^31 - 2^16, and chunks of 2^16 would take 2^47 elements;
+    // t0 + min(chunk, rows - t0) took 64.4 us where this takes 60.0, 8 x 4096 x 2048
+    // bfloat16)
+    const int t0 = (int)ck * chunk, t1 = min((int)ck * chunk + chunk, a.batch.rows);
     float w[K][V], b[V], ext[K - 1 + kAhead][V];
     load_taps<V, K>(a.w, a.wtype, c0, w);
     load_bias<V>(a.b, c0, b);
