@@ -86,6 +86,30 @@ __device__ __forceinline__ void decay(float u, float &a, float &m)
     }
 }
 
+// A gate sigma(v) kept with its complement: the smaller of the two, t / (1 + t)
+// with t = e^-|v|, with a minus sign where that is 1 - sigma(v).  The gradients
+// need both; 1 - sigma(v) taken from a sigma(v) rounded near 1 would have an error
+// of 2^-24 in a value of e^-v, and be 0 from v = 17 on.
+__device__ __forceinline__ float two_sided(float v)
+{
+    const float x = v * -kLog2e;
+    const float t = __builtin_amdgcn_exp2f(-__builtin_fabsf(x));
+    return __builtin_copysignf(t * __builtin_amdgcn_rcpf(1.0f + t), x);
+}
+// sigma(v): q, or 1 + q where q is negative -- the smaller one of the two as unsigned
+// words
+__device__ __forceinline__ float gate_of(float q)
+{
+    const unsigned shut = __builtin_bit_cast(unsigned, q);
+    const unsigned open = __builtin_bit_cast(unsigned, 1.0f + q);
+    return __builtin_bit_cast(float, min(shut, open));
+}
+// sigma(v) (1 - sigma(v)), from the smaller one: at most half of it is taken off
+__device__ __forceinline__ float gate_slope(float q)
+{
+    return fmaf(-q, q, __builtin_fabsf(q));
+}
+
 // Whether decay<true> serves this lane's channels and all others of its wave
 // (every wave of a workgroup has the same channels).
 template <int V> __device__ __forceinline__ bool all_small(const float (&rate)[V])
@@ -569,17 +593,17 @@ __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_gra
 #pragma unroll
     for (int v = 0; v < V; ++v)
         rate[v] = decay_rate(rate[v], a.scale);
-    float av[KT][V], si[KT][V], bt[KT][V], sr[KT][V];
+    float av[KT][V], gi[KT][V], bt[KT][V], gr[KT][V];
     auto gates = [&](auto small) {
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float m;
-                sr[k][v] = logistic(pr[k].get(v));
-                decay<decltype(small)::value>(rate[v] * sr[k][v], av[k][v], m);
+                gr[k][v] = two_sided(pr[k].get(v));
+                decay<decltype(small)::value>(rate[v] * gate_of(gr[k][v]), av[k][v], m);
                 bt[k][v] = input_factor(m);
-                si[k][v] = logistic(pi[k].get(v));
+                gi[k][v] = two_sided(pi[k].get(v));
             }
     };
     if (all_small(rate))
@@ -594,7 +618,7 @@ __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_gra
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     av[k][v] = 1.0f;
-                    sr[k][v] = 0.0f;
+                    gr[k][v] = 0.0f;
                 }
     float A[V], B[V], gt[KT][V];
 #pragma unroll
@@ -629,17 +653,17 @@ __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_gra
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float at = av[k][v], beta = bt[k][v], xv = px[k].get(v);
-            const float gated = gt[k][v] * si[k][v], decayed = at * hk[v];
-            ox[v] = gated * beta;
-            const float pull = gated * xv;
-            oi[v] = pull * beta * (1.0f - si[k][v]);
+            const float si = gate_of(gi[k][v]), decayed = at * hk[v];
+            const float in = gt[k][v] * beta, pull = gt[k][v] * xv * si;
+            ox[v] = in * si;
+            oi[v] = in * xv * gate_slope(gi[k][v]);
             // sigma(i) x a^2 / beta, nothing where beta is 0
             const float back =
                 beta > 0.0f ? pull * at * at * __builtin_amdgcn_rcpf(beta) : 0.0f;
-            const float dgate = (back - gt[k][v] * decayed) * sr[k][v];
-            drate[v] += dgate;
-            orr[v] = dgate * rate[v] * (1.0f - sr[k][v]);
-            hk[v] = fmaf(beta * si[k][v], xv, decayed);
+            const float dgate = back - gt[k][v] * decayed;
+            drate[v] = fmaf(dgate, gate_of(gr[k][v]), drate[v]);
+            orr[v] = dgate * rate[v] * gate_slope(gr[k][v]);
+            hk[v] = fmaf(beta * si, xv, decayed);
         }
         Raw<T, V>(ox).store(to_x, dx.lane, k * (int)dx.ld);
         Raw<T, V>(orr).store(to_r, dr.lane, k * (int)dr.ld);
