@@ -127,7 +127,8 @@ template <typename T, int V> struct Raw {
 };
 
 // 1 / (1 + e^-v) with the hardware's exponential and reciprocal (one unit in
-// the last place each); 0 and 1 at the infinities
+// the last place each, beside the rounding of the exponential's argument: for
+// negative v a relative error of up to (1.25 |v| + 6) 2^-24); 0 and 1 at the infinities
 __device__ __forceinline__ float logistic(float v)
 {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-v));

@@ -39,15 +39,29 @@ constexpr int kKept = DWCONV_SCAN_RUN;          // tokens from one kept state to
 constexpr int kSlab = 64;       // channels of a workgroup
 constexpr float kLog2e = 1.44269504088896341f;
 
+// e^-|v| to 3 roundings for any v.  The hardware's exponential takes the product
+// with log2(e), whose rounding alone would cost |v| / 2 of them; what the rounding
+// and the constant lose is multiplied back.  (Past 200 the result is 0; a NaN stays.)
+__device__ __forceinline__ float exp_neg(float v)
+{
+    constexpr float kRest = 1.925962989e-8f, kLn2 = 0.693147180559945f;  // log2(e) - kLog2e
+    const float n = -__builtin_fabsf(v), x = n < -200.0f ? -200.0f : n;
+    const float y = x * kLog2e;
+    const float rest = fmaf(x, kRest, fmaf(x, kLog2e, -y));
+    const float e = __builtin_amdgcn_exp2f(y);
+    return fmaf(e, rest * kLn2, e);
+}
+
 // Decay constant of a channel: scale * softplus(lam), softplus(v) = max(v, 0) +
 // log(1 + e), e = exp(-|v|).  Every thread of a run computes it for its
 // channels, so the logarithm is short: for e up to 1/2 (very negative lam, the
 // long memories, where log(1 + e) is about e) the polynomial of degree 6 for
 // log(1 + e) / e with the least relative error (6.1e-8 with rounded
-// coefficients, fitted on 4001 points), else the hardware's of 1 + e.
+// coefficients, fitted on 4001 points), else the hardware's of 1 + e.  In all some
+// 7 roundings of 2^-24.
 __device__ __forceinline__ float decay_rate(float lam, float scale)
 {
-    const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(lam) * kLog2e);
+    const float e = exp_neg(lam);
     float q = fmaf(e, 3.867349773645401e-2f, -1.136968806385994e-1f);
     q = fmaf(e, q, 1.845046728849411e-1f);
     q = fmaf(e, q, -2.475198209285736e-1f);
@@ -689,7 +703,8 @@ __global__ __launch_bounds__(1024) void k_scan_grad_sum(const float *part, int r
                                                         float *dlam)
 {
     column_sums(part, runs, C, [=](long long c, float s) {
-        dlam[c] = s * scale * logistic(lam[c]);
+        const float e = exp_neg(lam[c]), p = 1.0f / (1.0f + e);
+        dlam[c] = s * scale * (lam[c] < 0.0f ? e * p : p);
     });
 }
 

@@ -107,3 +107,22 @@ def test_gated_scan_of_nearly_open_and_shut_gates(torch, ref, dtype):
         v = rng.uniform(6.0, 18.0, tuple(g["x"].shape)) * rng.choice([-1.0, 1.0], g["x"].shape)
         g[n] = torch.from_numpy(v).to("cuda", g["x"].dtype)
     _check_scan(torch, ref, g, offsets, dtype)
+
+
+def test_decays_of_long_memories(torch):
+    """sqrt(1 - a^2) of channels that decay by 8 e^-4 to 8 e^-85 a token, by one step
+    from zero with open gates.  In roundings of 2^-24: the exponential 3, the
+    logarithm's polynomial 3, the scale 1, u's polynomial and product 2.6, 2 m - m^2
+    1, of which the root leaves half, and its own 2."""
+    lam = torch.linspace(-85.0, -4.0, 4001, device="cuda")
+    x = torch.ones(1, 4001, device="cuda")
+    gate = torch.full_like(x, float("inf"))
+    h = torch.zeros_like(x)
+    dw.gated_scan_step(x, gate, gate, lam, h)
+    y, hT = dw.gated_scan(x[None], gate[None], gate[None], lam)
+    torch.cuda.synchronize()
+    rate = 8.0 * torch.log1p(torch.exp(lam.double()))
+    want = torch.sqrt(-torch.expm1(-2.0 * rate))
+    for t in (h[0], hT[0], y[0, 0]):
+        off = (t.double() - want).abs() / want * 2.0 ** 24
+        assert float(off.max()) <= 0.5 * (3 + 3 + 1 + 2.6 + 1) + 2, float(off.max())
