@@ -249,12 +249,13 @@ def _workspace(nbytes, x):
     return x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
-def _space(ws):
+def _space(ws, x):
     """(address, bytes) of a workspace (None: NULL)."""
     if ws is None:
         return None, 0
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
+    _gpu(ws, "workspace", x)
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -345,7 +346,7 @@ def dwconv_causal_grad(dy, x, w, b, dx, dw, db, workspace, act="none", init=None
         _dense(b, "b", x, _f32, (C,)), _act(act), _dense(init, "init", x, kind, carried),
         _dense(dfinal, "dfinal", x, kind, carried), *_rows(dx, "dx", x, x.shape),
         _dense(_needed(dw, "dw"), "dw", x, _f32, (C, K)), _dense(db, "db", x, _f32, (C,)),
-        _dense(dinit, "dinit", x, kind, carried), *_space(workspace), seqs, tokens, off, C, K,
+        _dense(dinit, "dinit", x, kind, carried), *_space(workspace, x), seqs, tokens, off, C, K,
         st), "dwconv_causal_grad")
     return dx, dw, db, dinit
 
@@ -404,7 +405,7 @@ def dwconv_scan_fwd(x, r, i, lam, y, hT=None, states=None, workspace=None, scale
         _dense(_needed(lam, "lam"), "lam", x, _f32, (C,)), scale,
         _dense(h0, "h0", x, _f32, (seqs, C)), *_rows(y, "y", x, shape),
         _dense(hT, "hT", x, _f32, (seqs, C)), _states(states, x, seqs, tokens, off is not None),
-        *_space(workspace), seqs, tokens, off, C, st), "dwconv_scan_fwd")
+        *_space(workspace, x), seqs, tokens, off, C, st), "dwconv_scan_fwd")
     return y
 
 
@@ -474,7 +475,7 @@ def dwconv_scan_grad(dy, x, r, i, lam, states, dx, dr, di, dlam, dh0=None, works
         _dense(dhT, "dhT", x, _f32, (seqs, C)), *_rows(dx, "dx", x, shape),
         *_rows(dr, "dr", x, shape), *_rows(di, "di", x, shape),
         _dense(_needed(dlam, "dlam"), "dlam", x, _f32, (C,)),
-        _dense(dh0, "dh0", x, _f32, (seqs, C)), *_space(workspace), seqs, tokens, off, C, st),
+        _dense(dh0, "dh0", x, _f32, (seqs, C)), *_space(workspace, x), seqs, tokens, off, C, st),
         "dwconv_scan_grad")
     return dx, dr, di, dlam, dh0
 
@@ -531,8 +532,8 @@ def dwconv_linear_fwd(x, w, b, y, act="none", res=None, z=None, workspace=None, 
     pz, ldz = (None, 0) if z is None else _rows(z, "z", x, shape)
     _status(_library().dwconv_linear_fwd(
         px, ldx, pw, ldw, code, _dense(b, "b", x, _f32, (N,)), _act(act), pr, ldr,
-        *_rows(y, "y", x, shape), pz, ldz, *_space(workspace), x.numel() // max(K, 1), N, K, st),
-        "dwconv_linear_fwd")
+        *_rows(y, "y", x, shape), pz, ldz, *_space(workspace, x), x.numel() // max(K, 1), N, K,
+        st), "dwconv_linear_fwd")
     return y
 
 
@@ -571,7 +572,7 @@ def dwconv_linear_grad(dy, x, w, dx, dw, db, z=None, workspace=None, act="none",
         *(none if kind == _pkg.ACT_NONE else _rows(z, "z", x, shape)),
         *(none if dx is None else _rows(dx, "dx", x, x.shape)),
         *(none if dw is None else _rows(dw, "dw", x, w.shape)), _dense(db, "db", x, _f32, (N,)),
-        *_space(workspace), x.numel() // max(K, 1), N, K, st), "dwconv_linear_grad")
+        *_space(workspace, x), x.numel() // max(K, 1), N, K, st), "dwconv_linear_grad")
     return dx, dw, db
 
 
