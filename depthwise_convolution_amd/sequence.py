@@ -133,6 +133,8 @@ def _start(x, stream, name="x"):
         return code, handle, torch.cuda.device(index) if away else None
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    elif getattr(stream, "device", x.device) != x.device:
+        raise ValueError(f"stream is on {stream.device}, {name} on {x.device}")
     return code, _Handle(stream.cuda_stream), torch.cuda.stream(stream)
 
 

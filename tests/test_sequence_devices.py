@@ -1,8 +1,12 @@
-"""The binding's checks of devices, on stand-ins for a second GPU: a workspace of
-another device than the tensors' is refused before anything is enqueued."""
+"""The binding's checks of devices, on stand-ins for a second GPU: a workspace or
+a stream of another device than the tensors' is refused before anything is
+enqueued there."""
+import types
+
 import pytest
 import torch
 
+import depthwise_convolution_amd as dw
 from depthwise_convolution_amd import sequence
 
 
@@ -40,3 +44,17 @@ def test_workspace_of_another_device():
         sequence._space(4096, x)
     with pytest.raises(ValueError, match="contiguous"):
         sequence._space(_tensor(OnGpu, 8, 8, dtype=torch.uint8)[:, :4], x)
+
+
+def test_stream_of_another_device():
+    x = _tensor(OnGpu, 2, 3, 8)
+    other = types.SimpleNamespace(cuda_stream=5, device=torch.device("cuda", 1))
+    calls = [lambda: dw.causal_conv(x, x[0], stream=other),
+             lambda: dw.causal_conv_step(x[0], x, x[0], stream=other),
+             lambda: dw.gated_scan(x, x, x, x[0, 0], stream=other),
+             lambda: dw.gated_scan_step(x[0], x[0], x[0], x[0, 0], x[0], stream=other),
+             lambda: dw.linear(x, x[0], stream=other),
+             lambda: dw.linear_grad(x, x, x[0], stream=other)]
+    for call in calls:
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
