@@ -81,12 +81,14 @@ def resource_usage():
                 m = re.search(r"remark:\s+([^:]+): (\d+) \[", line)
                 if name and m and m.group(1).strip() in keys:
                     out[name][keys[m.group(1).strip()]] = int(m.group(2))
-    # GNU c++filt does not know _Float16 (DF16_): demangle it as half, then rename
-    names = [n.replace("DF16_", "Dh") for n in out]
+    # GNU c++filt knows neither _Float16 (DF16_) nor __bf16 (DF16b): demangle them as half
+    # and __int128, then rename
+    names = [n.replace("DF16_", "Dh").replace("DF16b", "n") for n in out]
     dem = subprocess.run(["c++filt"], input="\n".join(names), capture_output=True, text=True,
                          check=True).stdout.split("\n")
     return {d.replace("dwconv::(anonymous namespace)::", "")
-            .replace("dwseq::(anonymous namespace)::", "").replace("half", "_Float16"): v
+            .replace("dwseq::(anonymous namespace)::", "").replace("half", "_Float16")
+            .replace("__int128", "__bf16"): v
             for d, v in zip(dem, out.values())}
 
 
