@@ -9,13 +9,14 @@
 // sequences are never used in arithmetic (they may hold NaN): near the start
 // of a sequence each tap is taken from the carried rows or as zero.
 //
-// Measured, with inputs from HBM: forward, 8 x 4096 x 2048 bfloat16, 4 taps and
-// SiLU, 60 us (4.5 TB/s; a copy of the same bytes 50); 20011 x 1000 float32 in 37
-// sequences 37.5 us (4.3 TB/s); gradient, 16411 x 1536 float16 in 23 sequences,
-// 44 us with its sums (3.5 TB/s), bound by the vector unit's some 50 operations
-// an element as much as by HBM; single tokens, 64 x 2048, 3 us, a launch.  4
-// channels a thread in the forward took 55 us where 8 took 67 (fewer waves); in
-// the gradient 2 took 116 where 4 took 145 (8 x 4096 x 2048; registers; 108 since).
+// Measured, with inputs from HBM (a large copy: 6.3 TB/s): forward, 8 x 4096 x 2048
+// bfloat16, 4 taps and SiLU, 60 us (4.5 TB/s); 20011 x 1000 float32 in 37 sequences
+// 38 us (4.2 TB/s); gradient, 16411 x 1536 float16 in 23 sequences, 43.5 us with its
+// sums (3.5 TB/s); 8 x 4096 x 2048 96 us and 5 for the sums in bfloat16 (4.2 TB/s, the
+// vector unit active 70% of the time), 175 in float32 (4.6 TB/s); single tokens, 64 x
+// 2048, 3 us, a launch.  With the same tensors call after call, 4 channels a thread in the
+// forward took 55 us where 8 took 67 (fewer waves); in the gradient 2 took 116 where 4
+// took 145 (8 x 4096 x 2048; registers).
 #include "dwseq_device.h"
 
 namespace dwseq {
@@ -538,8 +539,8 @@ int launch_causal_fwd(const CausalArgs &a, void *stream)
         constexpr int V = decltype(v)::value, K = decltype(k)::value;
         const int groups = (int)cdiv(a.C, V);
         // Chunks as long as leaves 16 waves for each of the 256 CUs.  4 channels a
-        // thread against 8 of 16 bits: 54.7 and 66.4 us on 8 x 4096 x 2048 bfloat16,
-        // 4 taps, SiLU (floor 50 us): twice the waves, half the registers.
+        // thread against 8 of 16 bits: 54.7 and 66.4 us on 8 x 4096 x 2048 bfloat16, 4
+        // taps, SiLU, the same tensors each time: twice the waves, half the registers.
         int chunk = 32;
         while (chunk > kAhead && cdiv(a.batch.rows, chunk) * groups < 256 * 1024)
             chunk >>= 1;
@@ -576,9 +577,9 @@ int launch_causal_step(const CausalArgs &a, void *stream)
 
 // Chunks of 64 tokens, shorter where there would be too few workgroups, longer
 // where there would be more than 512 rows of partial sums.  Measured on 8 x 4096 x
-// 2048 bfloat16, 4 taps (floor 75 us; 108 by now): 64 tokens and 2 channels a thread with the
-// next rows in flight 115.7 us; 32 tokens 129.4; 4 channels 130.6; 8 rows ahead
-// 124.6; without the next rows in flight 152.
+// 2048 bfloat16, 4 taps, before the last changes (the same tensors each time): 64 tokens
+// and 2 channels a thread with the next rows in flight 115.7 us; 32 tokens 129.4; 4
+// channels 130.6; 8 rows ahead 124.6; without the next rows in flight 152.
 CausalGradPlan causal_grad_plan(int rows, int C)
 {
     CausalGradPlan p;

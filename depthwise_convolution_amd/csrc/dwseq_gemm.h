@@ -509,10 +509,12 @@ __device__ __forceinline__ void bare_barrier()
 //
 // Bound by LDS and latency: a 128 tile reads each fragment for 4 others
 // (the 256 tile's hold 8).  Measured: 128 tile, weight gradient of 8192 x 4096 x
-// 2048 bfloat16 155 us (885 TFLOP/s), float32 4096 x 2048 x 2048 262 us (131
-// TFLOP/s, the matrix instructions' own 157); 64 tile, float32 25088 x 256 x 128
-// with bias and ReLU6 22.5 us, of which 8 are its bytes: a tile has 4 steps, so
-// its beginning and end are not hidden; with 4 stages, bfloat16 1024^3 8.9 us.
+// 2048 bfloat16 155 us (887 TFLOP/s, matrix instructions busy 36% of the time), float32
+// 4096 x 2048 x 2048 261 us (132 TFLOP/s, the matrix instructions' own 157); 64 tile,
+// float32 25088 x 256 x 128 with bias and ReLU6 22.5 us among other calls (24.7 in a
+// trace, from its own beginning to its end), of which 6 are its bytes: a tile has 4
+// steps, so its beginning and end are not hidden; with 4 stages, bfloat16 1024^3 8.9
+// us; through registers, 4001 x 4003 x 4005 204 us (628 TFLOP/s: one step in flight).
 // ---------------------------------------------------------------------------
 template <typename T, bool PR, bool QR, bool DIRECT, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, int tiles_n,
@@ -709,11 +711,11 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, in
 // their way, which covers what the next phase reads.  Past the last step the
 // loads' descriptors are empty, so the count stays the same.
 //
-// Measured: 8192^3 bfloat16 1343 to 1368 TFLOP/s with both operands along k,
-// some 1200 with one and 1120 with both across it (two LDS reads a
-// fragment); the matrix instructions are busy 70% of the time at the clock that the card's
-// power allows.  16384 x 8192 x 2048 with bias, SiLU and residual 480 to 520 us:
-// the product 440, and the residuals' 268 MB, which wait for the product's
+// Measured: 8192^3 bfloat16 1505 TFLOP/s with both operands along k (1343 to 1368 on
+// another card), 1220 with one and 1100 with both across it (two LDS reads a
+// fragment); the matrix instructions are busy 76% of the time at the clock that the card's
+// power allows.  16384 x 8192 x 2048 with bias, SiLU and residual 486 to 510 us:
+// the product 418, and the residuals' 268 MB, which wait for the product's
 // registers (touching their lines some steps earlier gained nothing).
 // ---------------------------------------------------------------------------
 constexpr int kPitch = 256 * 4 + 16;      // bytes of a row of sums in LDS
@@ -922,8 +924,8 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
 // Few rows m (single tokens of many sequences): bound by reading Q once.  A
 // workgroup takes 16 columns n; its 8 waves each take a range of k straight from
 // memory into fragments, and their sums are added in LDS in order.  P is read
-// by every workgroup, from the caches.  8 x 8192 x 2048 bfloat16: 9.0 us, 3.8 TB/s
-// (the weights alone at the rate of a large copy: 6.8).
+// by every workgroup, from the caches.  8 x 8192 x 2048 bfloat16: 9 to 10 us, 3.5 TB/s
+// (the weights alone at the rate of a large copy: 5.4); float32 18 us.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 

@@ -9,7 +9,7 @@ namespace {
 
 // dz = dy * act'(z), and its column sums over a strip of rows (db): a workgroup
 // takes 32 vectors of V columns, its 8 rows of threads every 8th row of the
-// strip each.  Bound by HBM: 8192 x 4096 bfloat16 with SiLU 48.5 us, 4.1 TB/s.
+// strip each.  Bound by HBM: 8192 x 4096 bfloat16 with SiLU 42.6 us, 4.7 TB/s.
 //
 // dz is stored in the tensors' type, since the matrix instructions of the two
 // products that read it take their operands in one type: a second part for what the
@@ -133,8 +133,8 @@ GemmPlan gemm_plan(int size, int across, int M, int N, int K)
             const double part = load < 0.0 ? 0.0 : load > 1.0 ? 1.0 : load;
             const double step = s.alone[across] + (s.full[across] - s.alone[across]) * part;
             // float32's small workgroups follow each other without rounds: their time is
-            // the matrix instructions' (25088 x 256 x 128: 64 tile 25.9 us, 128 tile 27.7;
-            // counted so, bfloat16 would lose: 12.3 against 11.4)
+            // the matrix instructions' (25088 x 256 x 128, kernels alone: 64 tile 25.9 us,
+            // 128 tile 27.7; counted so, bfloat16 would lose: 12.3 against 11.4)
             const double fill = groups / (cus * s.per_cu);
             const double rounds = size == 4 && s.per_cu > 2 && fill > 1.0 ? fill : std::ceil(fill);
             double time = rounds * (cdiv(steps, splits) * step + s.ends);

@@ -22,13 +22,18 @@
 // timing: a state found further back is carried forward by the very operations
 // that its own workgroups use.
 //
-// What bounds it: 4 arrays of 16 bits moved an element (forward) against some 46
-// operations of the vector unit in the forward and 70 in the gradient, six and
-// more of them at a quarter of the rate.  The two overlap incompletely: at 8 x 2048 x 2048
-// bfloat16 the forward takes 73 us (3.7 TB/s; a copy of the same bytes 55) and
-// the gradient 123 us (3.8 TB/s), at 1 x 65537 x 1280 the forward 178 us (3.8
-// TB/s), of which the chain of 512 runs costs a tenth.  A run of 128 tokens is
-// what 256 threads hold in registers, 8 tokens of 4 channels each.
+// What bounds it: 4 arrays of 16 bits moved an element (forward) against 35
+// instructions of the vector unit in the forward and 66 in the gradient, six and
+// more of them at a quarter of the rate.  Neither is at its limit, as a run's loads, scan
+// and stores follow one another in a workgroup and registers leave 3 (2) of them a
+// CU: at 8 x 2048 x 2048 bfloat16 the forward takes 72 us (3.7 TB/s; a large copy
+// 6.3) and the gradient 121 us (4.0 TB/s), at 1 x 65537 x 1280 the forward 176 us (3.8
+// TB/s), of which the chain of 512 runs costs a tenth; the vector unit is active half
+// of the time.  float32 takes 130 and 213 us, and 261: its rows of 4 words do not fit
+// beside the gates (40 and 92 bytes of scratch a lane).  A run of 128 tokens is what 256
+// threads hold in registers, 8 tokens of 4 channels each; a sequence's last run
+// computes the gates of all 128, so that 64 sequences of 8 tokens, 2048 channels, take
+// 20 us.
 #include "dwseq_device.h"
 
 namespace dwseq {
@@ -557,8 +562,8 @@ __global__ __launch_bounds__(Layout<V>::threads, 3) void k_scan_fwd(ScanArgs a, 
 // recurrence is p[t] = a[t] p[t+1] + a[t] dy[t], whose steps compose as the
 // forward's do.  The state before each thread's tokens has been kept, so each
 // input is read once: 7 arrays moved (dy, x, r, i; dx, dr, di) and an eighth of
-// one in float32, the states.  Bound by instructions, some 70 an element: 123 us
-// at 8 x 2048 x 2048 bfloat16, 211 us at 24593 x 2048 in 48 sequences.
+// one in float32, the states.  66 instructions of the vector unit an element: 121 us
+// at 8 x 2048 x 2048 bfloat16, 9 of which is what the gates' complements cost.
 // ---------------------------------------------------------------------------
 template <typename T, int V>
 __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_grad(ScanArgs a,
