@@ -563,7 +563,7 @@ __global__ __launch_bounds__(Layout<V>::threads, 3) void k_scan_fwd(ScanArgs a, 
 // forward's do.  The state before each thread's tokens has been kept, so each
 // input is read once: 7 arrays moved (dy, x, r, i; dx, dr, di) and an eighth of
 // one in float32, the states.  66 instructions of the vector unit an element: 121 us
-// at 8 x 2048 x 2048 bfloat16, 9 of which is what the gates' complements cost.
+// at 8 x 2048 x 2048 bfloat16, 6 of which are what the gates' complements cost.
 // ---------------------------------------------------------------------------
 template <typename T, int V>
 __global__ __launch_bounds__(Layout<V>::threads, V == 1 ? 4 : 2) void k_scan_grad(ScanArgs a,

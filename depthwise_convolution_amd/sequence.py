@@ -43,8 +43,8 @@ SEQ_EXPORTS = ("dwconv_causal_fwd", "dwconv_causal_step", "dwconv_causal_grad_wo
 
 __all__ = ["causal_conv", "causal_conv_step", "causal_conv_grad", "gated_scan",
            "gated_scan_step", "gated_scan_grad", "linear", "linear_grad", "T_F32", "T_F16",
-           "T_BF16", "CAUSAL_MAX_TAPS", "SEQ_MAX_ROWS", "SCAN_RUN", "LINEAR_Y", "LINEAR_DX", "LINEAR_DW",
-           "SEQ_EXPORTS", *SEQ_EXPORTS]
+           "T_BF16", "CAUSAL_MAX_TAPS", "SEQ_MAX_ROWS", "SCAN_RUN", "LINEAR_Y", "LINEAR_DX",
+           "LINEAR_DW", "SEQ_EXPORTS", *SEQ_EXPORTS]
 
 
 def declare(L):
