@@ -19,7 +19,8 @@ reduction).  ``fwd``, ``input_grad`` and
 allocated here; given ``pads`` or ``mult`` they use the general forms.
 
 The sequence operators (causal depthwise convolution over tokens, gated
-linear recurrence, matrix product with epilogue) are in ``sequence`` and
+linear recurrence, matrix product with epilogue) are in ``sequence``, the
+mixing operators (matrix product in 8-bit integers) in ``mixing``; both are
 exported here.
 
 Tensor shapes: NHWC tensors are ``(N, H, W, C)``, NCHW tensors
@@ -30,7 +31,8 @@ import ctypes
 import functools
 import os
 
-from . import sequence
+from . import mixing, sequence
+from .mixing import *  # noqa: F401,F403  (the operators of include/dwconv_mix.h)
 from .sequence import *  # noqa: F401,F403  (the operators of include/dwconv_seq.h)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdwconv.so")
@@ -116,6 +118,7 @@ def lib():
         if f != "dwconv2d_strerror":
             getattr(L, f).restype = i
     sequence.declare(L)
+    mixing.declare(L)
     _lib = L
     return L
 

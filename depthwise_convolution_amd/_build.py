@@ -10,11 +10,12 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdwconv.so")
-HOST_SOURCES = ["dwconv_api.cpp", "dwconv_plan.cpp", "dwseq_api.cpp"]
+HOST_SOURCES = ["dwconv_api.cpp", "dwconv_plan.cpp", "dwseq_api.cpp", "dwmix_api.cpp"]
 HIP_SOURCES = ["dwconv_direct.hip", "dwconv_tiled_nhwc.hip", "dwconv_tiled_nchw.hip",
                "dwconv_wgrad.hip", "dwconv_launch.hip", "dwconv_stream.hip",
                "dwseq_conv.hip", "dwseq_scan.hip", "dwseq_linear.hip",
-               "dwseq_gemm_f32.hip", "dwseq_gemm_f16.hip", "dwseq_gemm_bf16.hip"]
+               "dwseq_gemm_f32.hip", "dwseq_gemm_f16.hip", "dwseq_gemm_bf16.hip",
+               "dwseq_gemm_i8.hip", "dwmix_quant.hip", "dwmix_norm.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -83,10 +83,15 @@ template <typename T, int V> struct Raw {
         } else if constexpr (words == 2) {
             *this = __builtin_bit_cast(Raw,
                                        __builtin_amdgcn_raw_buffer_load_b64(rsrc, lane, row, 0));
-        } else {
-            static_assert(words == 4);
+        } else if constexpr (words == 4) {
             *this = __builtin_bit_cast(Raw,
                                        __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, 0));
+        } else {
+            static_assert(words == 8);
+            const auto lo = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, 0);
+            const auto hi = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane + 16, row, 0);
+            __builtin_memcpy(w, &lo, 16);
+            __builtin_memcpy(w + 4, &hi, 16);
         }
     }
     // Four words go without a scalar offset: the compiler takes such a store to
@@ -104,9 +109,15 @@ template <typename T, int V> struct Raw {
         } else if constexpr (words == 2) {
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, *this), rsrc, lane, row,
                                                   0);
-        } else {
+        } else if constexpr (words == 4) {
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, *this), rsrc,
                                                    lane + row, 0, 0);
+        } else {
+            static_assert(words == 8);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, rsrc, lane + row,
+                                                   0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[4], w[5], w[6], w[7]}, rsrc,
+                                                   lane + row + 16, 0, 0);
         }
     }
     __device__ __forceinline__ float get(int v) const

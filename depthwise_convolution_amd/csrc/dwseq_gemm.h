@@ -1,5 +1,6 @@
 // dwseq_gemm.h -- the tiled matrix product behind dwconv_linear_*, one
-// translation unit per element type (dwseq_gemm_*.hip).
+// translation unit per element type (dwseq_gemm_*.hip; dwseq_gemm_i8.hip for
+// dwconv_linear_i8).
 //
 //   out[m, n] = finish(sum_k P[m, k] * Q[n, k])
 //
@@ -24,6 +25,12 @@
 // 16-bit fragments come through the LDS transpose read, its float32 ones as
 // four single reads (the float32 instructions are 16 times slower, so LDS has
 // the time).
+//
+// 8-bit integers (I8<O>, with results of type O): 16x16x64, which reads the same
+// 16 bytes of a row from a lane as 16x16x32 does, in the same time, so that a step
+// of 128 bytes is twice the k at the 16-bit kernels' cost.  Sums are 32-bit
+// integers, held in the same registers, exact, and scaled by their row and column
+// on their way out.  Both operands are read along k.
 #pragma once
 
 #include "dwseq_device.h"
@@ -32,6 +39,12 @@ namespace dwseq {
 
 constexpr int kStepBytes = 128;     // of k that a step multiplies
 
+// An 8-bit integer of a product whose results are of type O.
+template <typename O> struct I8 { signed char v; };
+template <typename T> struct Result { typedef T type; };
+template <typename O> struct Result<I8<O>> { typedef O type; };
+template <typename T> using result_t = typename Result<T>::type;
+
 // What happens to a sum on its way to memory.
 struct Finish {
     const float *b;             // per column, or nullptr
@@ -39,7 +52,8 @@ struct Finish {
     void *z, *y;                // z nullptr: not kept
     long long ldres, ldz, ldy;
     int act;
-    float *part;                // not nullptr: float32 partial sums [split][M][N] instead
+    float *part;                // not nullptr: 32-bit partial sums [split][M][N] instead
+    const float *rows, *cols;   // 8-bit integers: the factors of each row and column
 };
 
 // Which kernel a product runs with: tiles of that many rows and columns (the
@@ -59,6 +73,16 @@ struct Product {
 
 template <typename T> int launch_gemm(const Product &p, hipStream_t st);
 
+// The tile and the number of ranges of k for a product of elements of `size` bytes
+// with that many operands read across k, and the bytes of its partial sums
+// (dwseq_linear.hip).
+struct GemmPlan {
+    GemmTile tile;
+    int splits;
+};
+GemmPlan gemm_plan(int size, int across, int M, int N, int K);
+long long gemm_workspace(int size, int across, int M, int N, int K);
+
 // Whether an operand's chunks can go to LDS directly.
 inline bool direct_ok(const void *p, long long ld, bool rows_k, int K, int size)
 {
@@ -66,13 +90,24 @@ inline bool direct_ok(const void *p, long long ld, bool rows_k, int K, int size)
            (rows_k || ((long long)K * size) % 16 == 0);
 }
 
-// The kernel that runs for a plan's tile: the 256 tile is for 16-bit operands
-// that go to LDS directly, and so is the deep ring.
+// The kernel that runs for a plan's tile: the 256 tile is for 16-bit and 8-bit
+// operands that go to LDS directly, and so is the deep ring.
 inline GemmTile tile_taken(GemmTile tile, bool direct, int size)
 {
-    if (direct && size == 2)
+    if (direct && size != 4)
         return tile;
     return tile == TILE_256 ? TILE_128 : tile == TILE_64_DEEP ? TILE_64 : tile;
+}
+
+inline const char *tile_name(GemmTile tile, bool direct)
+{
+    switch (tile) {
+    case FEW_ROWS: return "few_rows";
+    case TILE_256: return "tile_256";
+    case TILE_128: return direct ? "tile_128" : "tile_128_registers";
+    case TILE_64_DEEP: return "tile_64_deep";
+    default: return direct ? "tile_64" : "tile_64_registers";
+    }
 }
 
 // The length of k's ranges for a plan's number of them, and how many of these
@@ -95,6 +130,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 typedef __attribute__((address_space(3))) char *lds_ptr;
 typedef __attribute__((address_space(3))) f32x4 *lds_f32x4;
@@ -110,6 +146,11 @@ __device__ __forceinline__ void mma(const u32x4 &a, const u32x4 &b, f32x4 &c)
     } else if constexpr (std::is_same_v<T, f16>) {
         c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                    __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    } else if constexpr (sizeof(T) == 1) {
+        c = __builtin_bit_cast(
+            f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                       __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                       __builtin_bit_cast(i32x4, c), 0, 0, 0));
     } else {
         const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
 #pragma unroll
@@ -194,6 +235,26 @@ template <typename T, int ROWS, bool R, int THREADS> struct Operand {
     // does not fill: what follows in its row is cut off in keep().
     __device__ __forceinline__ void fetch(u32x4 (&regs)[count], int k0, int tid) const
     {
+        if constexpr (size == 1) {      // rows from any byte on
+            const int left = K - k0;
+#pragma unroll
+            for (int j = 0; j < count; ++j) {
+                const int idx = j * THREADS + tid, row = idx / per_row;
+                const int at = place(row, idx % per_row) * 16;
+                const char *from = step_at(k0) + row * ld + at;
+                regs[j] = u32x4{0, 0, 0, 0};
+                if (row < rows && at + 16 <= left) {
+                    regs[j] = __builtin_bit_cast(
+                        u32x4, *reinterpret_cast<const Pack<T, 16> *>(from));
+                } else if (row < rows) {
+#pragma unroll
+                    for (int e = 0; e < 15; ++e)
+                        if (at + e < left)
+                            regs[j][e / 4] |= (unsigned)(unsigned char)from[e] << (e % 4 * 8);
+                }
+            }
+            return;
+        }
         const int end = bytes_at(k0);
         const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(step_at(k0), end);
 #pragma unroll
@@ -219,7 +280,7 @@ template <typename T, int ROWS, bool R, int THREADS> struct Operand {
     __device__ __forceinline__ void keep(char *lds, u32x4 (&regs)[count], int k0, int tid) const
     {
         const int left = K - k0;
-        if (!R && left < step)
+        if (size != 1 && !R && left < step)
 #pragma unroll
             for (int j = 0; j < count; ++j) {
                 const int idx = j * THREADS + tid;
@@ -334,6 +395,26 @@ __device__ __forceinline__ void put(E *p, int width, const float (&v)[V])
             if (e < width)
                 p[e] = (E)v[e];
     }
+}
+
+// V sums as the kernels hold them, as float32: those of 8-bit integers are 32-bit
+// integers, scaled by the factors of their row and columns.
+template <typename T, int V>
+__device__ __forceinline__ void widen(float (&s)[V], float row, const float (&cols)[V])
+{
+    if constexpr (sizeof(T) == 1)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            s[e] = (float)__builtin_bit_cast(int, s[e]) * (row * cols[e]);
+}
+
+// a + b of two sums as the kernels hold them
+template <typename T> __device__ __forceinline__ float add(float a, float b)
+{
+    if constexpr (sizeof(T) == 1)
+        return __builtin_bit_cast(float, __builtin_bit_cast(int, a) + __builtin_bit_cast(int, b));
+    else
+        return a + b;
 }
 
 // The residuals of V adjacent sums of row m, from column n on.
@@ -667,19 +748,34 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, in
                 }
             return;
         }
-        const Block<T, 4, CUT> res(a.f.res, a.f.ldres, m0, n0, BM, a.M, a.N),
+        using O = result_t<T>;
+        const Block<O, 4, CUT> res(a.f.res, a.f.ldres, m0, n0, BM, a.M, a.N),
             z(a.f.z, a.f.ldz, m0, n0, BM, a.M, a.N), y(a.f.y, a.f.ldy, m0, n0, BM, a.M, a.N);
         const Block<float, 4, CUT> bias(a.f.b, 0, 0, n0, 1, 1, a.N);
+        float row_factor[MF] = {};
+        if constexpr (sizeof(T) == 1)
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+                row_factor[m] = a.f.rows[min(m0 + wm + m * 16 + line, a.M - 1)];
         with_act(a.f.act, [&](auto act) {
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 const int col = first + n * 16;
-                Raw<T, 4> r[MF];
+                Raw<O, 4> r[MF];
                 Raw<float, 4> bn;
                 bn.clear();
                 if (a.f.b)
                     bias.load(bn, 0, 0, col);
                 const float b[4] = {bn.get(0), bn.get(1), bn.get(2), bn.get(3)};
+                float cols[4] = {};
+                if constexpr (sizeof(T) == 1) {
+                    const Block<float, 4, CUT> factors(a.f.cols, 0, 0, n0, 1, 1, a.N);
+                    Raw<float, 4> v;
+                    factors.load(v, 0, 0, col);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        cols[e] = v.get(e);
+                }
                 if (a.f.res)
 #pragma unroll
                     for (int m = 0; m < MF; ++m)
@@ -688,6 +784,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(Product a, int tiles_m, in
                 for (int m = 0; m < MF; ++m) {
                     float sum[4];
                     sums_of(n, m, sum);
+                    widen<T>(sum, row_factor[m], cols);
                     finish<decltype(act)::value>(a.f, z, y, b, r[m], sum, line, wm + m * 16, col);
                 }
             }
@@ -879,9 +976,10 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
     }
     with_cut<8>(a.N - n0, 256, [&](auto c) {
         constexpr bool CUT = decltype(c)::value;
-        const Block<T, 8, CUT> from(a.f.res, a.f.ldres, m0, n0, 256, a.M, a.N),
+        using O = result_t<T>;
+        const Block<O, 8, CUT> from(a.f.res, a.f.ldres, m0, n0, 256, a.M, a.N),
             z(a.f.z, a.f.ldz, m0, n0, 256, a.M, a.N), y(a.f.y, a.f.ldy, m0, n0, 256, a.M, a.N);
-        Raw<T, 8> res[kRows];
+        Raw<O, 8> res[kRows];
         auto fetch = [&](int hp) {
             if (a.f.res)
 #pragma unroll
@@ -901,14 +999,32 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
                     b[h * 4 + e] = v.get(e);
             }
         }
+        float cols[8] = {};
+        if constexpr (sizeof(T) == 1) {
+            const Block<float, 4, CUT> factors(a.f.cols, 0, 0, n0, 1, 1, a.N);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Raw<float, 4> v;
+                factors.load(v, 0, 0, col + h * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    cols[h * 4 + e] = v.get(e);
+            }
+        }
         with_act(a.f.act, [&](auto act) {
 #pragma unroll
             for (int hp = 0; hp < 2; ++hp) {
+                float row_factor[kRows] = {};
+                if constexpr (sizeof(T) == 1)
+#pragma unroll
+                    for (int k = 0; k < kRows; ++k)
+                        row_factor[k] = a.f.rows[min(m0 + hp * 128 + k * 16 + line, a.M - 1)];
                 spread(hp);
 #pragma unroll
                 for (int k = 0; k < kRows; ++k) {
                     float s[8];
                     row_of(k, s);
+                    widen<T>(s, row_factor[k], cols);
                     finish<decltype(act)::value>(a.f, z, y, b, res[k], s, line, hp * 128 + k * 16,
                                                  col);
                 }
@@ -939,7 +1055,7 @@ __device__ __forceinline__ u32x4 chunk_of(const T *row, int k, int K)
     } else {
 #pragma unroll
         for (int e = 0; e < elems; ++e) {
-            v.v[e] = (T)0.0f;
+            v.v[e] = T{};
             if (k + e < K)
                 v.v[e] = row[k + e];
         }
@@ -1000,14 +1116,20 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few_rows(Product a, int k_pe
         const f32x4 v = lds[w][wave][lane];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            sum[e] += v[e];
+            sum[e] = add<T>(sum[e], v[e]);
+    }
+    if constexpr (sizeof(T) == 1) {
+        float cols[4];
+        get(a.f.cols + col, a.N - col, cols);
+        widen<T>(sum, a.f.rows[row], cols);
     }
     if (a.f.b)
         get(a.f.b + col, a.N - col, b);
-    Raw<T, 4> r;
+    using O = result_t<T>;
+    Raw<O, 4> r;
     if (a.f.res)
         residual(a.f, row, col, a.N - col, r);
-    finish<T>(a.f, row, col, a.N - col, b, r, sum);
+    finish<O>(a.f, row, col, a.N - col, b, r, sum);
 }
 
 // out = finish(the splits' partial sums, added in order): a thread per 4 columns.
@@ -1033,21 +1155,27 @@ __global__ __launch_bounds__(256) void k_gemm_sum(Product a, int groups)
         for (int u = 0; u < kAhead; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                sum[e] += v[u][e];
+                sum[e] = add<T>(sum[e], v[u][e]);
     }
     for (; k < a.splits; ++k) {
         float v[4];
         get(part + k * next, width, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            sum[e] += v[e];
+            sum[e] = add<T>(sum[e], v[e]);
+    }
+    if constexpr (sizeof(T) == 1) {
+        float cols[4];
+        get(a.f.cols + n, width, cols);
+        widen<T>(sum, a.f.rows[m], cols);
     }
     if (a.f.b)
         get(a.f.b + n, width, b);
-    Raw<T, 4> r;
+    using O = result_t<T>;
+    Raw<O, 4> r;
     if (a.f.res)
         residual(a.f, m, n, width, r);
-    finish<T>(a.f, m, n, width, b, r, sum);
+    finish<O>(a.f, m, n, width, b, r, sum);
 }
 
 }  // namespace
@@ -1090,7 +1218,7 @@ template <typename T> int launch_gemm(const Product &product, hipStream_t st)
     };
     auto sized = [&](auto pr, auto qr, auto dir) {
         using std::integral_constant;
-        if constexpr (decltype(dir)::value && size == 2) {
+        if constexpr (decltype(dir)::value && size != 4) {
             if (tile == TILE_256) {
                 const long long tiles_m = cdiv(a.M, 256), tiles_n = cdiv(a.N, 256);
                 if (tiles_m * tiles_n > 0x3fffffffLL)
@@ -1107,7 +1235,7 @@ template <typename T> int launch_gemm(const Product &product, hipStream_t st)
                        integral_constant<int, 2>(), integral_constant<int, 2>(),
                        integral_constant<int, 2>());
         case TILE_64_DEEP:
-            if constexpr (decltype(dir)::value && size == 2)
+            if constexpr (decltype(dir)::value && size != 4)
                 return run(pr, qr, dir, integral_constant<int, 64>(), integral_constant<int, 64>(),
                            integral_constant<int, 2>(), integral_constant<int, 2>(),
                            integral_constant<int, 4>());
@@ -1120,9 +1248,12 @@ template <typename T> int launch_gemm(const Product &product, hipStream_t st)
     auto ways = [&](auto dir) {
         if (!a.p_rows_k && !a.q_rows_k)
             return sized(std::false_type(), std::false_type(), dir);
-        if (!a.p_rows_k)
+        if constexpr (size == 1)
+            return (int)DWCONV_ERR_BAD_OP;
+        else if (!a.p_rows_k)
             return sized(std::false_type(), std::true_type(), dir);
-        return sized(std::true_type(), std::true_type(), dir);
+        else
+            return sized(std::true_type(), std::true_type(), dir);
     };
     const int rc = direct ? ways(std::true_type()) : ways(std::false_type());
     if (rc != DWCONV_OK || !a.f.part)

@@ -79,11 +79,6 @@ __global__ __launch_bounds__(1024) void k_db(const float *part, int rows, int N,
     column_sums(part, rows, N, [=](long long n, float s) { db[n] = s; });
 }
 
-struct GemmPlan {
-    GemmTile tile;
-    int splits;
-};
-
 // Which kernel, and over how many ranges of k, by the time that a product
 // should take (microseconds): rounds of the chip times (steps of k times a
 // step's time, plus a tile's beginning and end).  A step's time grows from that
@@ -104,16 +99,19 @@ static const Shape kNarrow[] = {
     {TILE_128, 128, 2, {2.30, 2.30, 2.30}, {4.10, 4.00, 4.00}, 6.0},
     {TILE_64, 64, 5, {0.75, 0.70, 0.70}, {2.65, 2.60, 2.60}, 4.0}};
 
+}  // namespace
+
 // Few rows of operands that are both read along k go to the kernel that reads Q
 // once: measured against the 64 tile with 4 splits it is ahead while M / 16 * K is
 // at most 4096 (at 32 x 4096 x 4096: 14.8 against 13.2 us; at 16 x 4096 x 2048: 6.7
-// against 9.4).
+// against 9.4); 8-bit operands are counted as half as many 16-bit ones.
 GemmPlan gemm_plan(int size, int across, int M, int N, int K)
 {
-    if (across == 0 && (M <= 16 || (M <= kFewRows && cdiv(M, 16) * K <= 4096)))
+    if (across == 0 &&
+        (M <= 16 || (M <= kFewRows && cdiv(M, 16) * K <= (size == 1 ? 8192 : 4096))))
         return {FEW_ROWS, 1};
-    const Shape *shapes = size == 2 ? kWide : kNarrow;
-    const int count = size == 2 ? 4 : 2, cus = 256;
+    const Shape *shapes = size != 4 ? kWide : kNarrow;
+    const int count = size != 4 ? 4 : 2, cus = 256;
     const long long steps = cdiv((long long)K * size, kStepBytes);
     GemmPlan best{TILE_64, 1};
     double least = 1e30;
@@ -148,12 +146,13 @@ GemmPlan gemm_plan(int size, int across, int M, int N, int K)
     return best;
 }
 
-// Bytes of a product's partial sums.
 long long gemm_workspace(int size, int across, int M, int N, int K)
 {
     const GemmPlan p = gemm_plan(size, across, M, N, K);
     return p.splits > 1 ? 4LL * M * N * p.splits : 0;
 }
+
+namespace {
 
 template <typename T>
 int product(const T *P, long long ldp, bool p_rows_k, const T *Q, long long ldq, bool q_rows_k,
@@ -207,13 +206,7 @@ void linear_describe(int product, int type, bool aligned, int M, int N, int K, c
     const GemmPlan plan = gemm_plan(size, across, m, n, k);
     const bool direct = aligned && (across == 2 || direct_ok(nullptr, 0, false, k, size));
     *splits = split_count(k, plan.splits, size);
-    switch (tile_taken(plan.tile, direct, size)) {
-    case FEW_ROWS: *name = "few_rows"; break;
-    case TILE_256: *name = "tile_256"; break;
-    case TILE_128: *name = direct ? "tile_128" : "tile_128_registers"; break;
-    case TILE_64: *name = direct ? "tile_64" : "tile_64_registers"; break;
-    case TILE_64_DEEP: *name = "tile_64_deep"; break;
-    }
+    *name = tile_name(tile_taken(plan.tile, direct, size), direct);
 }
 
 int launch_linear_fwd(const LinearArgs &a, void *stream)
