@@ -13,6 +13,31 @@ using namespace dwseq;
 
 namespace {
 
+int check_attention(int type, int H, int KV, int Dk, int Dv)
+{
+    if (!type_ok(type))
+        return DWCONV_ERR_BAD_WTYPE;
+    if (H < 1 || H > (1 << 16) || KV < 1 || H % KV != 0 || Dk < 1 ||
+        Dk > DWCONV_ATTENTION_MAX_DIM || Dv < 1 || Dv > DWCONV_ATTENTION_MAX_DIM)
+        return DWCONV_ERR_BAD_DIM;
+    return DWCONV_OK;
+}
+
+// The arrays of q, k and v, and what of them the record holds.
+void take_qkv(Check &c, AttentionArgs &a, const void *q, long long ldq, const void *k,
+              long long ldk, const void *v, long long ldv, long long rows)
+{
+    const long long e = elem_size(a.type);
+    c.in(q, region(q, rows, ldq * e, e * a.H * a.Dk), (int)e);
+    c.in(k, region(k, rows, ldk * e, e * a.KV * a.Dk), (int)e);
+    c.in(v, region(v, rows, ldv * e, e * a.KV * a.Dv), (int)e);
+    c.in(a.log_decay, dense(a.log_decay, 4LL * a.H), 4);
+    if (!short_ld_ok(ldq, (long long)a.H * a.Dk) || !short_ld_ok(ldk, (long long)a.KV * a.Dk) ||
+        !short_ld_ok(ldv, (long long)a.KV * a.Dv))
+        c.fail(DWCONV_ERR_ROW_STRIDE);
+    a.q = q; a.k = k; a.v = v; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
+}
+
 int check_norm(int type, long long N, long long P, int C, int groups)
 {
     if (!type_ok(type))
@@ -27,6 +52,131 @@ int check_norm(int type, long long N, long long P, int C, int groups)
 }  // namespace
 
 extern "C" {
+
+int dwconv_attention_workspace_size(int grad, int type, int seqs, long long tokens, int packed,
+                                    int H, int KV, int Dk, int Dv, long long *bytes)
+{
+    if (!bytes)
+        return DWCONV_ERR_NULL_PTR;
+    Batch b;
+    int st = check_attention(type, H, KV, Dk, Dv);
+    if (st == DWCONV_OK)
+        st = make_batch(seqs, tokens, nullptr, packed != 0, &b);
+    if (st != DWCONV_OK)
+        return st;
+    *bytes = attention_workspace(grad != 0, b, packed != 0, H, KV, Dk, Dv);
+    return DWCONV_OK;
+}
+
+int dwconv_attention_fwd(const void *q, long long ldq, const void *k, long long ldk,
+                         const void *v, long long ldv, int type, const float *log_decay,
+                         float scale, const float *h0, void *y, long long ldy, float *hT,
+                         void *workspace, long long workspace_bytes, int seqs, long long tokens,
+                         const int *offsets, int H, int KV, int Dk, int Dv, void *stream)
+{
+    AttentionArgs a{};
+    int st = check_attention(type, H, KV, Dk, Dv);
+    if (st == DWCONV_OK)
+        st = make_batch(seqs, tokens, offsets, offsets != nullptr, &a.batch);
+    if (st != DWCONV_OK)
+        return st;
+    if (!std::isfinite(scale))
+        return DWCONV_ERR_BAD_EPILOGUE;
+    a.log_decay = log_decay; a.scale = scale; a.type = type; a.H = H; a.KV = KV; a.Dk = Dk;
+    a.Dv = Dv;
+    const long long e = elem_size(type), rows = a.batch.rows, states = 4LL * seqs * H * Dk * Dv;
+    const long long need = attention_workspace(false, a.batch, offsets != nullptr, H, KV, Dk, Dv);
+    if (!short_ld_ok(ldy, (long long)H * Dv))
+        return DWCONV_ERR_ROW_STRIDE;
+    Check c;
+    take_qkv(c, a, q, ldq, k, ldk, v, ldv, rows);
+    c.in(h0, dense(h0, states), 4, false);
+    c.in(offsets, dense(offsets, 4LL * (seqs + 1LL)), 4, false);
+    c.out(y, region(y, rows, ldy * e, e * H * Dv), (int)e);
+    c.out(hT, dense(hT, states), 4, false);
+    c.out(workspace, dense(workspace, need), 1, false);
+    if (c.done() != DWCONV_OK)
+        return c.status;
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != DWCONV_OK)
+        return st;
+    a.h0 = h0; a.y = y; a.ldy = ldy; a.hT = hT; a.workspace = workspace;
+    return launch_attention_fwd(a, stream);
+}
+
+int dwconv_attention_step(const void *q, long long ldq, const void *k, long long ldk,
+                          const void *v, long long ldv, int type, const float *log_decay,
+                          float scale, float *h, void *y, long long ldy, int seqs, int H, int KV,
+                          int Dk, int Dv, void *stream)
+{
+    AttentionArgs a{};
+    int st = check_attention(type, H, KV, Dk, Dv);
+    if (st == DWCONV_OK)
+        st = make_batch(seqs, 1, nullptr, false, &a.batch);
+    if (st != DWCONV_OK)
+        return st;
+    if (!std::isfinite(scale))
+        return DWCONV_ERR_BAD_EPILOGUE;
+    a.log_decay = log_decay; a.scale = scale; a.type = type; a.H = H; a.KV = KV; a.Dk = Dk;
+    a.Dv = Dv;
+    const long long e = elem_size(type);
+    if (!short_ld_ok(ldy, (long long)H * Dv))
+        return DWCONV_ERR_ROW_STRIDE;
+    Check c;
+    take_qkv(c, a, q, ldq, k, ldk, v, ldv, seqs);
+    c.out(y, region(y, seqs, ldy * e, e * H * Dv), (int)e);
+    c.out(h, dense(h, 4LL * seqs * H * Dk * Dv), 4);
+    if (c.done() != DWCONV_OK)
+        return c.status;
+    a.y = y; a.ldy = ldy; a.h = h;
+    return launch_attention_step(a, stream);
+}
+
+int dwconv_attention_grad(const void *dy, long long lddy, const void *q, long long ldq,
+                          const void *k, long long ldk, const void *v, long long ldv, int type,
+                          const float *log_decay, float scale, const float *h0, const float *dhT,
+                          void *dq, long long lddq, void *dk, long long lddk, void *dv,
+                          long long lddv, float *dh0, void *workspace, long long workspace_bytes,
+                          int seqs, long long tokens, const int *offsets, int H, int KV, int Dk,
+                          int Dv, void *stream)
+{
+    AttentionArgs a{};
+    int st = check_attention(type, H, KV, Dk, Dv);
+    if (st == DWCONV_OK)
+        st = make_batch(seqs, tokens, offsets, offsets != nullptr, &a.batch);
+    if (st != DWCONV_OK)
+        return st;
+    if (!std::isfinite(scale))
+        return DWCONV_ERR_BAD_EPILOGUE;
+    a.log_decay = log_decay; a.scale = scale; a.type = type; a.H = H; a.KV = KV; a.Dk = Dk;
+    a.Dv = Dv;
+    const long long e = elem_size(type), rows = a.batch.rows, states = 4LL * seqs * H * Dk * Dv;
+    const long long need = attention_workspace(true, a.batch, offsets != nullptr, H, KV, Dk, Dv);
+    if (!short_ld_ok(lddy, (long long)H * Dv) ||
+        (dq && !short_ld_ok(lddq, (long long)H * Dk)) ||
+        (dk && !short_ld_ok(lddk, (long long)KV * Dk)) ||
+        (dv && !short_ld_ok(lddv, (long long)KV * Dv)))
+        return DWCONV_ERR_ROW_STRIDE;
+    Check c;
+    take_qkv(c, a, q, ldq, k, ldk, v, ldv, rows);
+    c.in(dy, region(dy, rows, lddy * e, e * H * Dv), (int)e);
+    c.in(h0, dense(h0, states), 4, false);
+    c.in(dhT, dense(dhT, states), 4, false);
+    c.in(offsets, dense(offsets, 4LL * (seqs + 1LL)), 4, false);
+    c.out(dq, region(dq, rows, lddq * e, e * H * Dk), (int)e, false);
+    c.out(dk, region(dk, rows, lddk * e, e * KV * Dk), (int)e, false);
+    c.out(dv, region(dv, rows, lddv * e, e * KV * Dv), (int)e, false);
+    c.out(dh0, dense(dh0, states), 4, false);
+    c.out(workspace, dense(workspace, need), 1, false);
+    if (c.done() != DWCONV_OK)
+        return c.status;
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != DWCONV_OK)
+        return st;
+    a.dy = dy; a.lddy = lddy; a.h0 = h0; a.dhT = dhT; a.dq = dq; a.lddq = lddq; a.dk = dk;
+    a.lddk = lddk; a.dv = dv; a.lddv = lddv; a.dh0 = dh0; a.workspace = workspace;
+    return launch_attention_grad(a, stream);
+}
 
 int dwconv_norm_workspace_size(int grad, int type, long long N, long long P, int C, int groups,
                                long long *bytes)

@@ -1,0 +1,945 @@
+// dwmix_attention.h -- the walk along the tokens behind dwconv_attention_*, one
+// translation unit per element type (dwmix_attention_*.hip).
+//
+//   out[i] = s0 * sum_{j <= i} a^(i-j) (q[i] . k[j]) v[j] + s1 * a^(i+1-late) q[i] S
+//   S     <- a^n S + s2 * sum_j a^(n-1-j+late) k[j] v[j]^T          (n tokens)
+//
+// The forward is this walk over (q, k, v) with late = 0.  Each gradient is the
+// same walk over other tensors: dq over (dy, v, k), with the transposed state; dk
+// and dv from the last token to the first, with late = 1 (the cotangent of a state
+// reaches the token that made it without a decay), over (v, dy, q) and (k, q, dy).
+//
+// A sequence is cut into segments, which run side by side: first the state that each
+// adds by itself (k_states), then those linked one after the other (k_link), then
+// the walk, each segment from its own start.  Where there are enough sequences
+// and heads to fill the chip a sequence is one segment, and the walk is all.
+//
+// A workgroup of 4 waves walks one head of one segment, a tile of DVT of the state's
+// columns, in chunks of 128 bytes of tokens (64 16-bit, 32 float32):
+//
+//   scores   P[i, j] of 16 rows i a wave, times their decay, through LDS to all waves
+//   output   a wave takes DVT / 4 columns for all rows: its part of S is in registers
+//            (float32, as the matrix instructions leave it), which is already the
+//            layout of an operand that is summed over dk, so q S reads only q;
+//            then P V on top
+//   state    S = a^n S + K^T (V with its decays), the same columns
+//
+// so that LDS holds q, k, v and P (56 KB for widths of 128), a state never
+// leaves its registers, and two workgroups share a CU.
+//
+// Roundings of 16-bit types.  P and the chunk's S are rounded once where they become
+// operands, each by half a step of the type, as the output is afterwards: with
+// independent roundings the output's error grows from one rounding's to sqrt(2) of
+// it.  A second part would double the products.  V with its decays, which the
+// state is built from, is split into parts (three bfloat16, two float16) that hold
+// 22 bits and more: what is lost there would add up in the float32 state.
+// float16 has too few exponents for scores and states: the values are scaled by a power
+// of two, one for each wave, where their largest would be too large or too small.
+#pragma once
+
+#include "dwmix_internal.h"
+#include "dwseq_device.h"
+#include "../../include/dwconv_mix.h"
+
+namespace dwmix {
+
+// One walk.
+struct Walk {
+    const void *q, *k, *v;
+    void *out;                          // nullptr: only the state is wanted
+    const float *log_decay, *state0;    // state0 nullptr: zero
+    float *state1;                      // nullptr: not kept
+    float *slots;                       // states that segments start from, [item][H][Dk][Dv]
+    long long ldq, ldk, ldv, ldo;
+    int gq, gk, gv;                     // heads that share one of the tensor's
+    int H, Dk, Dv;
+    float s0, s1, s2;
+    int late, back;
+    bool flip;                          // state0 and state1 are [..][Dv][Dk]
+    bool out32;                         // out is float32
+    Batch batch;
+    int segment, per_seq, items;        // tokens; segments of a dense sequence; of all
+};
+
+template <typename T> int launch_walk(const Walk &w, hipStream_t st);
+// columns of the state that a workgroup takes
+inline int walk_tile(int Dk, int Dv) { return Dk > 128 || Dv <= 64 ? 64 : 128; }
+
+#ifdef DWMIX_ATTENTION_KERNELS
+namespace {
+
+using namespace dwseq;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) char *lds_ptr;
+typedef __attribute__((address_space(3))) u32x4 *lds_u4;
+typedef __attribute__((address_space(3))) u32x2 *lds_u2;
+typedef __attribute__((address_space(3))) unsigned *lds_u1;
+
+// c += a b of 16 x 16, over 32 16-bit or 16 float32 numbers
+template <typename T>
+__device__ __forceinline__ void mma(const u32x4 &a, const u32x4 &b, f32x4 &c)
+{
+    if constexpr (std::is_same_v<T, bf16>) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    } else if constexpr (std::is_same_v<T, f16>) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    } else {
+        const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[j], fb[j], c, 0, 0, 0);
+    }
+}
+
+// Waits until the results of all matrix instructions may be read.  The compiler
+// counts those waits itself, but not along every branch (seen: one that skipped
+// further matrix instructions, and the last word of a result read too early), so
+// no branch lies between a matrix instruction and this.
+__device__ __forceinline__ void settle()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// V floats as elements of T, two 16-bit ones to a word
+template <typename T, int V>
+__device__ __forceinline__ void narrow(const float (&f)[V], unsigned *w)
+{
+    const Raw<T, V> r(f);
+#pragma unroll
+    for (int i = 0; i < Raw<T, V>::words; ++i)
+        w[i] = r.w[i];
+}
+
+// Whether a word holds an infinity or a NaN (16-bit types: either of its two).
+template <typename T> __device__ __forceinline__ unsigned odd_bits(unsigned w)
+{
+    if constexpr (std::is_same_v<T, bf16>)
+        return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    else if constexpr (std::is_same_v<T, f16>)
+        return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+    else
+        return ((w & 0x7f800000u) + 0x00800000u) & 0x80000000u;
+}
+
+// The word with infinities and NaN replaced by zero.
+template <typename T> __device__ __forceinline__ unsigned cleaned(unsigned w)
+{
+    const unsigned odd = odd_bits<T>(w);
+    if constexpr (sizeof(T) == 4)
+        return odd ? 0u : w;
+    else
+        return w & ~((odd >> 15) * 0xffffu);
+}
+
+// Sequence and segment of an item: sequence s has the items from
+// start(s) / segment + s on (packed), which are at least as many as its segments.
+struct Item {
+    int seq, seg, row0, length;     // of the sequence
+    __device__ __forceinline__ Item(const Walk &w, int item)
+    {
+        const Batch &b = w.batch;
+        if (!b.off) {
+            seq = item / w.per_seq;
+            seg = item - seq * w.per_seq;
+        } else {
+            int lo = 0, hi = b.seqs - 1;
+            while (lo < hi) {
+                const int mid = lo + ((hi - lo + 1) >> 1);
+                if (seq_start(b, mid) / w.segment + mid <= item)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            seq = lo;
+            seg = item - (seq_start(b, seq) / w.segment + seq);
+        }
+        row0 = seq_start(b, seq);
+        length = max(seq_start(b, seq + 1) - row0, 0);
+    }
+    __device__ __forceinline__ int segments(const Walk &w) const
+    {
+        return max(1, (int)(((long long)length + w.segment - 1) / w.segment));
+    }
+};
+
+// log a of a head: 0 at most; finite, so that its product with 0 is 0
+__device__ __forceinline__ float log_decay_of(const float *p, int h)
+{
+    const float g = p[h];
+    return g != g ? g : fmaxf(fminf(g, 0.0f), -1e4f);
+}
+
+// Element [dk][dv] of a state array that is [Dk][Dv], or flipped.
+__device__ __forceinline__ long long state_at(const Walk &w, bool flip, int dk, int dv)
+{
+    return flip ? (long long)dv * w.Dk + dk : (long long)dk * w.Dv + dv;
+}
+
+constexpr int kWaves = 4, kThr = kWaves * 64, kChunkBytes = 128;
+
+constexpr int kFar = 0x7ffffff0;        // beyond every descriptor's bounds
+
+// A tile of C rows of D elements in LDS, 16 bytes between the rows: the reads below,
+// of 16 rows at one chunk of 16 bytes, of 8 rows two apart at 32 bytes, or of 4 at 64,
+// fall on different banks, and what differs between the reads of a lane is a constant.
+template <typename T, int C, int D> struct Tile {
+    static constexpr int size = (int)sizeof(T), elems = 16 / size;
+    static constexpr int per_row = D / elems, pitch = D * size + 16, bytes = C * pitch;
+    static constexpr int count = C * per_row / kThr;    // chunks a thread stages
+    static constexpr int apart = kThr / per_row;        // rows between them
+    static_assert(count >= 1 && C * per_row % kThr == 0);
+
+    // The bytes from the chunk of tokens' lowest row on of what a thread stages, and
+    // from one of its rows to the next.
+    struct From {
+        int first, step, row, col;
+        __device__ __forceinline__ From(long long ld, bool back)
+            : row((int)threadIdx.x / per_row), col((int)threadIdx.x % per_row * elems)
+        {
+            const int pitch_in = (int)ld * size;
+            first = (back ? C - 1 - row : row) * pitch_in + col * size;
+            step = (back ? -apart : apart) * pitch_in;
+        }
+    };
+    // The chunk's rows, `left` of them, columns up to `wide`, from the row of lowest
+    // address on (which may lie before the array where `left` is less than C).
+    static __device__ __forceinline__ void fetch(u32x4 (&regs)[count], const T *lowest,
+                                                 const From &f, int left, int wide)
+    {
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(lowest, kFar - 16);
+        if (wide % elems == 0) {
+#pragma unroll
+            for (int k = 0; k < count; ++k) {
+                const bool in = f.row + k * apart < left && f.col < wide;
+                regs[k] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               rsrc, in ? f.first + k * f.step : kFar, 0, 0));
+            }
+        } else {        // rows that end within a chunk: element by element
+#pragma unroll
+            for (int k = 0; k < count; ++k) {
+                unsigned v[elems];
+#pragma unroll
+                for (int e = 0; e < elems; ++e) {
+                    const bool in = f.row + k * apart < left && f.col + e < wide;
+                    const int at = in ? f.first + k * f.step + e * size : kFar;
+                    if constexpr (size == 2)
+                        v[e] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
+                    else
+                        v[e] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+                }
+                if constexpr (size == 2)
+                    regs[k] = u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                                    v[6] | v[7] << 16};
+                else
+                    regs[k] = u32x4{v[0], v[1], v[2], v[3]};
+            }
+        }
+    }
+    static __device__ __forceinline__ void keep(lds_ptr lds, const u32x4 (&regs)[count])
+    {
+        const int row = (int)threadIdx.x / per_row, c = (int)threadIdx.x % per_row;
+#pragma unroll
+        for (int k = 0; k < count; ++k)
+            *(lds_u4)(lds + (row + k * apart) * pitch + c * 16) = regs[k];
+    }
+
+    // 16 bytes of row `row`, chunk `c`
+    static __device__ __forceinline__ u32x4 chunk(lds_ptr lds, int row, int c)
+    {
+        return *(lds_u4)(lds + row * pitch + c * 16);
+    }
+    // An operand that is summed along the row: row `row`, part u of it (32 16-bit
+    // or 16 float32 columns), the numbers of lane group g.  In the order that a
+    // matrix instruction leaves its results in: 4 of each 16.
+    static __device__ __forceinline__ u32x4 along(lds_ptr lds, int row, int u, int g)
+    {
+        if constexpr (size == 4) {
+            return chunk(lds, row, u * 4 + g);
+        } else {
+            const lds_ptr at = lds + row * pitch + g * 8 + u * 64;
+            const u32x2 lo = *(lds_u2)at, hi = *(lds_u2)(at + 32);
+            return u32x4{lo.x, lo.y, hi.x, hi.y};
+        }
+    }
+    // An operand that is summed across the rows: column col + (lane & 15), part
+    // ks of the rows (32 or 16), the numbers of lane group g, in the order of row_of().
+    static __device__ __forceinline__ u32x4 across(lds_ptr lds, int col, int ks, int lane)
+    {
+        const int g = lane >> 4, i = lane & 15;
+        u32x4 v;
+        if constexpr (size == 4) {
+            const lds_ptr at = lds + g * 4 * pitch + i * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = *(__attribute__((address_space(3))) const unsigned *)(
+                    at + (ks * 16 + j) * pitch + col * 4);
+        } else {
+            // 4 rows, two apart, a read
+            const lds_ptr at = lds + (g * 8 + (i >> 2) * 2) * pitch + (i & 3) * 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4 *)(at + (ks * 32 + h) * pitch +
+                                                                col * 2));
+                const uint2 w = __builtin_bit_cast(uint2, t);
+                v[h * 2] = w.x;
+                v[h * 2 + 1] = w.y;
+            }
+        }
+        return v;
+    }
+    // The row of number e of such an operand.
+    static __device__ __forceinline__ int row_of(int ks, int g, int e)
+    {
+        return size == 4 ? ks * 16 + g * 4 + e : ks * 32 + g * 8 + (e & 3) * 2 + (e >> 2);
+    }
+    static __device__ __forceinline__ float one(lds_ptr lds, int row, int col)
+    {
+        return (float)*(__attribute__((address_space(3))) const T *)(lds + row * pitch +
+                                                                     col * size);
+    }
+};
+
+// Element e of a fragment.  (The word is taken out first: a bit cast of a vector's
+// element reads element 0 on this compiler.)
+template <typename T> __device__ __forceinline__ float element(const u32x4 &v, int e)
+{
+    const unsigned word = v[sizeof(T) == 4 ? e : e / 2];
+    if constexpr (sizeof(T) == 4)
+        return __builtin_bit_cast(float, word);
+    else if constexpr (std::is_same_v<T, bf16>)
+        return __builtin_bit_cast(float, e & 1 ? word & 0xffff0000u : word << 16);
+    else
+        return (float)__builtin_bit_cast(f16, (unsigned short)(word >> (16 * (e & 1))));
+}
+
+__device__ __forceinline__ float wave_max(float m)
+{
+    for (int d = 1; d < 64; d *= 2)
+        m = fmaxf(m, __shfl_xor(m, d));
+    return m;
+}
+
+// The power of two that brings a largest value of m to [1, 2), or 1 while it lies
+// between lo and hi (float16: where its numbers are normal and far from their end).
+__device__ __forceinline__ float range_scale(float m, float lo, float hi)
+{
+    if (!(m > 0.0f) || (m >= lo && m <= hi))
+        return 1.0f;
+    const int e = (int)((__builtin_bit_cast(unsigned, m) >> 23) & 255) - 127;
+    return __builtin_bit_cast(float, (unsigned)(127 - min(max(e, -120), 120)) << 23);
+}
+
+__device__ __forceinline__ float finite_size(float v)
+{
+    return fabsf(v) <= 3.4e38f ? fabsf(v) : 0.0f;
+}
+
+template <typename T, int DK, int DVT> struct Body {
+    static constexpr int size = (int)sizeof(T), elems = 16 / size;
+    static constexpr int C = kChunkBytes / size;        // tokens of a chunk
+    static constexpr int CT = C / 16;                   // 16-row tiles of it
+    static constexpr int span = 4 * elems;              // that a product sums over
+    static constexpr int KS = C / span;                 // parts of a chunk's tokens
+    static constexpr int NT = DK / 16, US = DK / span;  // tiles and parts of dk
+    static constexpr int MT = DVT / kWaves / 16;        // tiles of a wave's columns
+    static constexpr int parts = std::is_same_v<T, bf16> ? 3 : std::is_same_v<T, f16> ? 2 : 1;
+    static constexpr bool is_f16 = std::is_same_v<T, f16>;
+    using QK = Tile<T, C, DK>;
+    using VV = Tile<T, C, DVT>;
+    using PP = Tile<T, C, C>;                           // scores
+
+    // powers of the decay in LDS: number k is a^(C - k), and 0 from C + 1 on
+    static constexpr int powers = 2 * C;
+    typedef __attribute__((address_space(3))) const float *table;
+
+    f32x4 S[NT][MT];
+    int lane, wave, g, i;
+    table pw;
+
+    __device__ __forceinline__ explicit Body(table powers_)
+        : lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+          g(lane >> 4), i(lane & 15), pw(powers_)
+    {
+    }
+    static __device__ __forceinline__ void fill(float *to, float ld)
+    {
+        if ((int)threadIdx.x < powers)
+            to[threadIdx.x] =
+                (int)threadIdx.x <= C ? expf(ld * (float)(C - (int)threadIdx.x)) : 0.0f;
+    }
+    // At the start of a chunk: what follows from the lane is made anew, as it would
+    // otherwise be kept for all chunks, in more registers than there are.
+    __device__ __forceinline__ void next_chunk()
+    {
+        asm volatile("" : "+v"(lane));
+        g = lane >> 4;
+        i = lane & 15;
+    }
+
+    // first of the wave's columns within the tile
+    __device__ __forceinline__ int col0() const { return wave * (DVT / kWaves); }
+
+    // f(S element, dk, dv) for what the state has; dv counts from the tile's first
+    template <typename F> __device__ __forceinline__ void each(const Walk &w, int dv0, F f)
+    {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int dk = n * 16 + g * 4 + r, dv = dv0 + col0() + m * 16 + i;
+                    float v = S[n][m][r];
+                    f(v, dk, dv, dk < w.Dk && dv < w.Dv);
+                    S[n][m][r] = v;
+                }
+    }
+
+    // The wave's columns of V, as operands that are summed across the rows.
+    __device__ __forceinline__ void columns(lds_ptr v, u32x4 (&f)[KS][MT]) const
+    {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                f[ks][m] = VV::across(v, col0() + m * 16, ks, lane);
+    }
+
+    // Whether the wave's columns hold an infinity or a NaN.
+    __device__ __forceinline__ bool strange(const u32x4 (&f)[KS][MT]) const
+    {
+        unsigned odd = 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    odd |= odd_bits<T>(f[ks][m][e]);
+        return __any(odd != 0);
+    }
+
+    // S = a^n S + s2 K^T (V with its decays)
+    __device__ __forceinline__ void update(const Walk &w, lds_ptr k, const u32x4 (&vf)[KS][MT],
+                                           bool any, int n, float a_n)
+    {
+        const float s2 = w.s2;
+        const int late = w.late;
+        float up = 1.0f;
+        if constexpr (is_f16) {     // small values would lose their last bits
+            float most = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < elems; ++e)
+                        most = fmaxf(most, finite_size(element<T>(vf[ks][m], e)));
+            up = range_scale(wave_max(most) * fabsf(s2), 0x1p-3f, 0x1p14f);
+        }
+        const float keep = a_n * up;
+        const table late_pw = pw + (C - n + 1 - late) + VV::row_of(0, g, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                S[t][m] *= keep;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            u32x4 p[MT][parts];
+            float f[elems];
+#pragma unroll
+            for (int e = 0; e < elems; ++e)     // a^(n - 1 - j + late) for row j
+                f[e] = late_pw[VV::row_of(ks, 0, e)] * (s2 * up);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float rest[elems];
+#pragma unroll
+                for (int e = 0; e < elems; ++e)
+                    rest[e] = element<T>(vf[ks][m], e) * f[e];
+#pragma unroll
+                for (int q = 0; q < parts; ++q) {
+                    unsigned word[4];
+                    narrow<T, elems>(rest, word);
+                    p[m][q] = u32x4{word[0], word[1], word[2], word[3]};
+                    if (q + 1 < parts)
+#pragma unroll
+                        for (int e = 0; e < elems; ++e) {
+                            const float head = element<T>(p[m][q], e);
+                            // what an infinity leaves is not a number
+                            rest[e] = fabsf(head) <= 3.4e38f ? rest[e] - head : 0.0f;
+                        }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const u32x4 kf = QK::across(k, t * 16, ks, lane);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int q = 0; q < parts; ++q)
+                        mma<T>(kf, p[m][q], S[t][m]);
+            }
+        }
+        settle();
+        if constexpr (is_f16)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    S[t][m] *= 1.0f / up;
+        if (any && w.Dk < DK)       // an infinity times the zeros beside k
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (t * 16 + g * 4 + r >= w.Dk)
+                            S[t][m][r] = 0.0f;
+    }
+
+    // The scores of 16 rows, times their decay, to LDS; the power of two that they
+    // were divided by (float16) is returned.
+    __device__ __forceinline__ float scores(lds_ptr q, lds_ptr k, lds_ptr p, float s0) const
+    {
+        if (wave >= CT)
+            return 1.0f;
+        f32x4 acc[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+            acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < US; ++u) {
+            const u32x4 qf = QK::chunk(q, wave * 16 + i, u * 4 + g);
+#pragma unroll
+            for (int t = 0; t < CT; ++t)    // later tiles too: no branch (see settle)
+                mma<T>(QK::chunk(k, t * 16 + i, u * 4 + g), qf, acc[t]);
+        }
+        const table gap_pw = pw + (C - wave * 16 - i + g * 4);
+        float most = 0.0f, down = 1.0f, v[CT][4];
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int gap = wave * 16 + i - (t * 16 + g * 4 + r);
+                // a score of a later token may be anything
+                v[t][r] = gap >= 0 ? acc[t][r] * (s0 * gap_pw[t * 16 + r]) : 0.0f;
+                most = fmaxf(most, finite_size(v[t][r]));
+            }
+        if constexpr (is_f16)
+            down = range_scale(wave_max(most), 0x1p-2f, 0x1p14f);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            const int row = wave * 16 + i;
+            if constexpr (is_f16)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    v[t][r] *= down;
+            // column 8a + 2m + h of a row is kept as number 4h + m of its chunk a: the
+            // order in which across() reads the rows of V
+            if constexpr (size == 4) {
+                unsigned word[4];
+                narrow<T, 4>(v[t], word);
+                *(lds_u4)(p + row * PP::pitch + (t * 4 + g) * 16) =
+                    u32x4{word[0], word[1], word[2], word[3]};
+            } else {
+                const lds_ptr at = p + row * PP::pitch + (t * 2 + (g >> 1)) * 16 + (g & 1) * 4;
+                const float even[2] = {v[t][0], v[t][2]}, odd[2] = {v[t][1], v[t][3]};
+                unsigned w0, w1;
+                narrow<T, 2>(even, &w0);
+                narrow<T, 2>(odd, &w1);
+                *(lds_u1)at = w0;
+                *(lds_u1)(at + 8) = w1;
+            }
+        }
+        return down;
+    }
+
+    // o[m][t]: 4 columns of m and row i of the 16 of tile t:  s1 a^(i+1-late) q S
+    __device__ __forceinline__ void from_state(lds_ptr q, f32x4 (&o)[MT][CT], float s1, int late)
+    {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                o[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        float down = 1.0f;
+        if constexpr (is_f16) {
+            float most = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        most = fmaxf(most, finite_size(S[n][m][r]));
+            down = range_scale(wave_max(most), 0x1p-2f, 0x1p14f);
+        }
+#pragma unroll
+        for (int u = 0; u < US; ++u) {
+            u32x4 sf[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float f[elems];
+#pragma unroll
+                for (int e = 0; e < elems; ++e)
+                    f[e] = S[u * (elems / 4) + e / 4][m][e % 4] * (is_f16 ? down : 1.0f);
+                unsigned word[4];
+                narrow<T, elems>(f, word);
+                sf[m] = u32x4{word[0], word[1], word[2], word[3]};
+            }
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                const u32x4 qf = QK::along(q, t * 16 + i, u, g);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    mma<T>(sf[m], qf, o[m][t]);
+            }
+        }
+        const table row_pw = pw + (C - 1 + late - (CT - 1) * 16 - i);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            const float f = s1 * row_pw[(CT - 1 - t) * 16] / down;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                o[m][t] *= f;
+        }
+    }
+
+    // o += P V.  A V with infinities or NaN is taken apart: a zero score of a later
+    // token times those would be NaN.
+    __device__ __forceinline__ void from_scores(lds_ptr p, lds_ptr v, const float *downs,
+                                                const u32x4 (&vf)[KS][MT], bool any,
+                                                f32x4 (&o)[MT][CT])
+    {
+        auto scaled = [&](bool back) {
+            if constexpr (is_f16)
+#pragma unroll
+                for (int t = 0; t < CT; ++t) {
+                    const float d = downs[t];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        o[m][t] *= back ? 1.0f / d : d;
+                }
+        };
+        scaled(false);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            u32x4 f[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                f[m] = vf[ks][m];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)     // a select: no branch (see settle)
+                    f[m][e] = any ? cleaned<T>(f[m][e]) : f[m][e];
+            }
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                if (ks * span <= t * 16 + 15) {
+                    const u32x4 pf = PP::chunk(p, t * 16 + i, ks * 4 + g);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        mma<T>(f[m], pf, o[m][t]);
+                }
+        }
+        settle();
+        if (any)
+            for (int j = 0; j < C; ++j) {
+                const int slot = (j & ~7) | (j & 1) << 2 | (j >> 1 & 3);    // of column j
+                float x[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        x[m][r] = VV::one(v, j, col0() + m * 16 + g * 4 + r);
+#pragma unroll
+                for (int t = 0; t < CT; ++t) {
+                    const float s = PP::one(p, t * 16 + i, size == 4 ? j : slot);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (j <= t * 16 + i && !(fabsf(x[m][r]) <= 3.4e38f))
+                                o[m][t][r] += s * x[m][r];
+                }
+            }
+        scaled(true);
+    }
+
+    // The rows `here` of the chunk from token t on, 4 adjacent columns a lane.
+    template <typename E>
+    __device__ __forceinline__ void store(E *out, const Walk &w, const f32x4 (&o)[MT][CT],
+                                          long long row0, int t, int here, int h, int dv0) const
+    {
+        const int wide = w.Dv - dv0, ldo = (int)w.ldo * (int)sizeof(E);
+        const long long lowest = w.back ? row0 - t - (C - 1) : row0 + t;
+        const __amdgpu_buffer_rsrc_t rsrc =
+            dwconv::make_rsrc(out + lowest * w.ldo + h * w.Dv + dv0, kFar - 16);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            const int r = c * 16 + i, first = (w.back ? C - 1 - r : r) * ldo;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int dv = col0() + m * 16 + g * 4;
+                const f32x4 v = o[m][c];
+                const float s[4] = {v[0], v[1], v[2], v[3]};
+                const int at = first + dv * (int)sizeof(E);
+                if (wide % 4 == 0) {
+                    Raw<E, 4>(s).store(rsrc, r < here && dv < wide ? at : kFar, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float one[1] = {s[e]};
+                        Raw<E, 1>(one).store(
+                            rsrc, r < here && dv + e < wide ? at + e * (int)sizeof(E) : kFar, 0);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// The rows of a walk's tensor: from token t on, the row of lowest address of a chunk.
+template <typename T, int C> struct Rows {
+    const T *base;          // token 0's row
+    long long step;         // elements from a token to the next
+    bool back;
+    __device__ __forceinline__ Rows(const void *p, long long ld, bool turned, long long row,
+                                    int column)
+        : base(static_cast<const T *>(p) + row * ld + column), step(turned ? -ld : ld),
+          back(turned)
+    {
+    }
+    __device__ __forceinline__ const T *at(int t) const
+    {
+        return base + (back ? t + C - 1 : t) * step;
+    }
+};
+
+// What a workgroup walks.
+struct Part {
+    int item, h, dv0;
+    __device__ __forceinline__ Part(const Walk &w, int tile)
+    {
+        const int tiles = (w.Dv + tile - 1) / tile;
+        const int b = dwconv::xcd_tile((int)block_id(), w.items * w.H * tiles);
+        dv0 = b % tiles * tile;
+        h = b / tiles % w.H;
+        item = b / tiles / w.H;
+    }
+};
+
+// The state that a segment adds by itself, to the slot of the next one.
+template <typename T, int DK, int DVT>
+__global__ __launch_bounds__(kThr, 2) void k_states(Walk w)
+{
+    using B = Body<T, DK, DVT>;
+    __shared__ alignas(16) char lds[B::QK::bytes + B::VV::bytes];
+    __shared__ float powers[B::powers];
+    const lds_ptr lk = (lds_ptr)lds, lv = lk + B::QK::bytes;
+    if ((int)block_id() >= w.items * w.H * (int)((w.Dv + DVT - 1) / DVT))
+        return;
+    const Part part(w, DVT);
+    const Item at(w, part.item);
+    if (at.seg + 1 >= at.segments(w))
+        return;
+    const float ld = log_decay_of(w.log_decay, part.h);
+    B::fill(powers, ld);
+    B b((typename B::table)powers);
+    b.each(w, part.dv0, [](float &v, int, int, bool) { v = 0.0f; });
+    const int t0 = at.seg * w.segment, n = w.segment;       // a whole one
+    const long long row = w.back ? (long long)at.row0 + at.length - 1 - t0 : at.row0 + t0;
+    const Rows<T, B::C> k(w.k, w.ldk, w.back, row, part.h / w.gk * w.Dk),
+        v(w.v, w.ldv, w.back, row, part.h / w.gv * w.Dv + part.dv0);
+    const typename B::QK::From fk(w.ldk, w.back);
+    const typename B::VV::From fv(w.ldv, w.back);
+    const int wide = w.Dv - part.dv0;
+    const float whole = (float)exp((double)ld * B::C);
+    u32x4 rk[B::QK::count], rv[B::VV::count];
+    B::QK::fetch(rk, k.at(0), fk, n, w.Dk);
+    B::VV::fetch(rv, v.at(0), fv, n, wide);
+    for (int t = 0; t < n; t += B::C) {
+        const int here = min(B::C, n - t);
+        b.next_chunk();
+        B::QK::keep(lk, rk);
+        B::VV::keep(lv, rv);
+        __syncthreads();
+        B::QK::fetch(rk, k.at(t + B::C), fk, n - t - B::C, w.Dk);
+        B::VV::fetch(rv, v.at(t + B::C), fv, n - t - B::C, wide);
+        u32x4 vf[B::KS][B::MT];
+        b.columns(lv, vf);
+        b.update(w, lk, vf, b.strange(vf), here,
+                 here == B::C ? whole : expf(ld * (float)here));
+        __syncthreads();
+    }
+    float *to = w.slots + ((long long)(part.item + 1) * w.H + part.h) * w.Dk * w.Dv;
+    b.each(w, part.dv0, [&](float &v, int dk, int dv, bool has) {
+        if (has)
+            to[state_at(w, false, dk, dv)] = v;
+    });
+}
+
+// The segments' own states, each to be added to what it gets from those before it.  A
+// thread takes an element; the segments of a sequence one after the other.
+__global__ __launch_bounds__(256) void k_link(Walk w, int blocks)
+{
+    const long long id = block_id();
+    const int at = (int)(id % blocks) * 256 + (int)threadIdx.x;
+    const int h = (int)(id / blocks % w.H);
+    const long long seq = id / blocks / w.H;
+    if (seq >= w.batch.seqs || at >= w.Dk * w.Dv)
+        return;
+    const int first = w.batch.off ? seq_start(w.batch, (int)seq) / w.segment + (int)seq
+                                  : (int)seq * w.per_seq;
+    const Item it(w, first);
+    const int count = it.segments(w);
+    if (count == 1)
+        return;
+    const float ld = log_decay_of(w.log_decay, h);
+    const float a = (float)exp((double)ld * w.segment);
+    const long long size = (long long)w.Dk * w.Dv;
+    float run = 0.0f;
+    if (w.state0)
+        run = w.state0[(seq * w.H + h) * size + state_at(w, w.flip, at / w.Dv, at % w.Dv)];
+    float *slot = w.slots + ((long long)first * w.H + h) * size + at;
+    const long long next = w.H * size;
+    constexpr int kAhead = 8;
+    for (int j = 1; j < count; j += kAhead) {
+        float v[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            v[u] = j + u < count ? slot[(j + u) * next] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (j + u < count) {
+                run = a * run + v[u];
+                slot[(j + u) * next] = run;
+            }
+    }
+}
+
+template <typename T, int DK, int DVT>
+__global__ __launch_bounds__(kThr, 2) void k_walk(Walk w)
+{
+    using B = Body<T, DK, DVT>;
+    __shared__ alignas(16) char lds[2 * B::QK::bytes + B::VV::bytes + B::PP::bytes];
+    __shared__ float downs[kWaves], powers[B::powers];
+    const lds_ptr lq = (lds_ptr)lds, lk = lq + B::QK::bytes, lv = lk + B::QK::bytes,
+                  lp = lv + B::VV::bytes;
+    if ((int)block_id() >= w.items * w.H * (int)((w.Dv + DVT - 1) / DVT))
+        return;
+    const Part part(w, DVT);
+    const Item at(w, part.item);
+    const int count = at.segments(w);
+    if (at.seg >= count)
+        return;
+    const float ld = log_decay_of(w.log_decay, part.h);
+    B::fill(powers, ld);
+    B b((typename B::table)powers);
+    const long long size = (long long)w.Dk * w.Dv;
+    const long long own = ((long long)at.seq * w.H + part.h) * size;
+    const float *from = at.seg ? w.slots + ((long long)part.item * w.H + part.h) * size
+                               : w.state0 ? w.state0 + own : nullptr;
+    const bool flip = at.seg ? false : w.flip;
+    b.each(w, part.dv0, [&](float &v, int dk, int dv, bool has) {
+        v = from && has ? from[state_at(w, flip, dk, dv)] : 0.0f;
+    });
+    const int t0 = at.seg * w.segment, n = min(w.segment, at.length - t0);
+    const long long row = w.back ? (long long)at.row0 + at.length - 1 - t0 : at.row0 + t0;
+    const Rows<T, B::C> q(w.q, w.ldq, w.back, row, part.h / w.gq * w.Dk),
+        k(w.k, w.ldk, w.back, row, part.h / w.gk * w.Dk),
+        v(w.v, w.ldv, w.back, row, part.h / w.gv * w.Dv + part.dv0);
+    const typename B::QK::From fq(w.ldq, w.back), fk(w.ldk, w.back);
+    const typename B::VV::From fv(w.ldv, w.back);
+    const int wide = w.Dv - part.dv0;
+    const float whole = (float)exp((double)ld * B::C);
+    u32x4 rq[B::QK::count], rk[B::QK::count], rv[B::VV::count];
+    B::QK::fetch(rq, q.at(0), fq, n, w.Dk);
+    B::QK::fetch(rk, k.at(0), fk, n, w.Dk);
+    B::VV::fetch(rv, v.at(0), fv, n, wide);
+    for (int t = 0; t < n; t += B::C) {
+        const int here = min(B::C, n - t);
+        b.next_chunk();
+        B::QK::keep(lq, rq);
+        B::QK::keep(lk, rk);
+        B::VV::keep(lv, rv);
+        __syncthreads();
+        B::QK::fetch(rq, q.at(t + B::C), fq, n - t - B::C, w.Dk);
+        B::QK::fetch(rk, k.at(t + B::C), fk, n - t - B::C, w.Dk);
+        B::VV::fetch(rv, v.at(t + B::C), fv, n - t - B::C, wide);
+        __builtin_amdgcn_sched_barrier(0);
+        const float down = b.scores(lq, lk, lp, w.s0);
+        if (B::is_f16 && b.lane == 0)
+            downs[b.wave] = down;
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 o[B::MT][B::CT];
+        b.from_state(lq, o, w.s1, w.late);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 vf[B::KS][B::MT];
+        b.columns(lv, vf);
+        const bool any = b.strange(vf);
+        b.from_scores(lp, lv, downs, vf, any, o);
+        b.update(w, lk, vf, any, here, here == B::C ? whole : expf(ld * (float)here));
+        __builtin_amdgcn_sched_barrier(0);
+        if (w.out32)
+            b.store(static_cast<float *>(w.out), w, o, row, t, here, part.h, part.dv0);
+        else if (w.out)
+            b.store(static_cast<T *>(w.out), w, o, row, t, here, part.h, part.dv0);
+        __syncthreads();
+    }
+    if (w.state1 && at.seg + 1 == count)
+        b.each(w, part.dv0, [&](float &v, int dk, int dv, bool has) {
+            if (has)
+                w.state1[own + state_at(w, w.flip, dk, dv)] = v;
+        });
+}
+
+}  // namespace
+
+template <typename T> int launch_walk(const Walk &w, hipStream_t st)
+{
+    const long long blocks = (long long)w.items * w.H * cdiv(w.Dv, walk_tile(w.Dk, w.Dv));
+    if (blocks > 0x7fffffffLL)
+        return DWCONV_ERR_BAD_DIM;
+    auto run = [&](auto dk, auto dvt) {
+        constexpr int DK = decltype(dk)::value, DVT = decltype(dvt)::value;
+        int rc = DWCONV_OK;
+        if (w.slots) {
+            rc = dwconv::launch_kernel(k_states<T, DK, DVT>, grid_of(blocks), dim3(kThr), 0, st, w);
+            const int links = (int)cdiv(w.Dk * w.Dv, 256);
+            if ((long long)w.batch.seqs * w.H * links > 0x7fffffffLL)
+                return (int)DWCONV_ERR_BAD_DIM;
+            if (rc == DWCONV_OK)
+                rc = dwconv::launch_kernel(k_link, grid_of((long long)w.batch.seqs * w.H * links),
+                                           dim3(256), 0, st, w, links);
+        }
+        if (rc == DWCONV_OK)
+            rc = dwconv::launch_kernel(k_walk<T, DK, DVT>, grid_of(blocks), dim3(kThr), 0, st, w);
+        return rc;
+    };
+    using std::integral_constant;
+    if (w.Dk > 128)
+        return run(integral_constant<int, 256>(), integral_constant<int, 64>());
+    if (w.Dk > 64)
+        return w.Dv > 64 ? run(integral_constant<int, 128>(), integral_constant<int, 128>())
+                         : run(integral_constant<int, 128>(), integral_constant<int, 64>());
+    return w.Dv > 64 ? run(integral_constant<int, 64>(), integral_constant<int, 128>())
+                     : run(integral_constant<int, 64>(), integral_constant<int, 64>());
+}
+#endif  // DWMIX_ATTENTION_KERNELS
+
+}  // namespace dwmix

@@ -1,0 +1,285 @@
+// dwmix_attention.hip -- linear attention with a decay for each head
+// (include/dwconv_mix.h): the single-token step, and the walks that the forward
+// and the gradients are made of (dwmix_attention.h).
+#include "dwmix_attention.h"
+
+#include <algorithm>
+
+namespace dwmix {
+namespace {
+
+using namespace dwseq;
+
+// ------------------------------------------------------------ one token
+// S = a S + k v^T, y = scale q S, in float32.  Bound by reading and writing the states:
+// a workgroup takes one head of one sequence; the lanes of a row of threads take V
+// adjacent columns each, the rows of threads every `ty`-th row of S, and their parts
+// of y are added in LDS in order.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_attention_step(AttentionArgs a, int tx, int ty)
+{
+    __shared__ float qk[2][DWCONV_ATTENTION_MAX_DIM], sums[256 * V];
+    const long long id = block_id();
+    if (id >= (long long)a.batch.seqs * a.H)
+        return;
+    const long long seq = id / a.H;
+    const int h = (int)(id % a.H), kv = h / (a.H / a.KV);
+    const T *q = static_cast<const T *>(a.q) + seq * a.ldq + h * a.Dk;
+    const T *k = static_cast<const T *>(a.k) + seq * a.ldk + kv * a.Dk;
+    const T *v = static_cast<const T *>(a.v) + seq * a.ldv + kv * a.Dv;
+    if ((int)threadIdx.x < a.Dk) {
+        qk[0][threadIdx.x] = (float)q[threadIdx.x] * a.scale;
+        qk[1][threadIdx.x] = (float)k[threadIdx.x];
+    }
+    const int x = (int)threadIdx.x % tx, y = (int)threadIdx.x / tx, dv = x * V;
+    const bool mine = y < ty && dv < a.Dv;
+    const float g = a.log_decay[h];
+    const float decay = g > 0.0f ? 1.0f : expf(g);
+    float add[V] = {}, out[V] = {};
+    if (mine)
+        load<T, V>(v + dv, add);
+    __syncthreads();
+    float *s = a.h + (seq * a.H + h) * a.Dk * a.Dv + dv;
+    if (mine) {
+        constexpr int kAhead = 8;
+        int d = y;
+        for (; d + (kAhead - 1) * ty < a.Dk; d += kAhead * ty) {
+            float r[kAhead][V];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                load<float, V>(s + (d + u * ty) * a.Dv, r[u]);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const float kd = qk[1][d + u * ty], qd = qk[0][d + u * ty];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    r[u][e] = decay * r[u][e] + kd * add[e];
+                    out[e] += qd * r[u][e];
+                }
+                store<float, V>(s + (d + u * ty) * a.Dv, r[u]);
+            }
+        }
+        for (; d < a.Dk; d += ty) {
+            float r[V];
+            load<float, V>(s + d * a.Dv, r);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                r[e] = decay * r[e] + qk[1][d] * add[e];
+                out[e] += qk[0][d] * r[e];
+            }
+            store<float, V>(s + d * a.Dv, r);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        sums[threadIdx.x * V + e] = out[e];
+    __syncthreads();
+    if (y != 0 || !mine)
+        return;
+    for (int r = 1; r < ty; ++r)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            out[e] += sums[(r * tx + x) * V + e];
+    store<T, V>(static_cast<T *>(a.y) + seq * a.ldy + h * a.Dv + dv, out);
+}
+
+// ------------------------------------------------------- shared heads
+// The gradients of a key or value head: the sum of its query heads', in order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_shared(const float *part, T *out, long long ldo, int rows,
+                                                int H, int KV, int D)
+{
+    const long long wide = (long long)KV * D, id = (long long)block_id() * 256 + threadIdx.x;
+    const long long row = id / wide;
+    if (row >= rows)
+        return;
+    const int at = (int)(id % wide), group = H / KV;
+    const float *from = part + row * H * D + (long long)(at / D) * group * D + at % D;
+    float s = from[0];
+    for (int g = 1; g < group; ++g)
+        s += from[(long long)g * D];
+    out[row * ldo + at] = (T)s;
+}
+
+// -------------------------------------------------------------- planning
+// Segments: where sequences, heads and column tiles make fewer workgroups than the
+// chip holds (two a CU), sequences are cut, into parts of 4 chunks at least.
+struct SegmentPlan {
+    int segment, per_seq, items;
+    bool cut;
+    long long slots;            // bytes
+};
+
+constexpr int kChunk = 64, kLeast = 4 * kChunk, kWanted = 1024, kFull = 512;
+
+SegmentPlan segment_plan(const Batch &b, bool packed, int H, int Dk, int Dv)
+{
+    SegmentPlan p;
+    const long long tiles = (long long)H * cdiv(Dv, walk_tile(Dk, Dv));
+    const long long tokens = packed ? b.rows : b.tokens;
+    long long segment = std::max(tokens, 1LL);
+    if (packed)
+        segment = std::min(segment, cdiv(b.rows * tiles, kWanted));
+    else if (b.seqs * tiles < kFull)
+        segment = cdiv(tokens, cdiv(kWanted, b.seqs * tiles));
+    segment = cdiv(std::max<long long>(segment, kLeast), kChunk) * kChunk;
+    p.segment = (int)std::min(segment, 0x40000000LL);
+    p.per_seq = (int)std::max(1LL, cdiv(b.tokens, p.segment));
+    const long long items = packed ? b.rows / p.segment + (long long)b.seqs
+                                   : (long long)b.seqs * p.per_seq;
+    p.items = (int)std::min(items, 0x7fffffffLL);
+    p.cut = tokens > p.segment;
+    p.slots = p.cut ? 4LL * p.items * H * Dk * Dv : 0;
+    return p;
+}
+
+long long round16(long long bytes) { return cdiv(bytes, 16) * 16; }
+
+int walk(int type, const Walk &w, hipStream_t st)
+{
+    return with_type(type, [&](auto *t) {
+        return launch_walk<std::remove_pointer_t<decltype(t)>>(w, st);
+    });
+}
+
+// The parts of the walk that a batch and its plan set.
+void place(Walk &w, const Batch &b, int H, int Dk, int Dv, void *slots)
+{
+    const SegmentPlan p = segment_plan(b, b.off != nullptr, H, Dk, Dv);
+    w.batch = b;
+    w.H = H;
+    w.Dk = Dk;
+    w.Dv = Dv;
+    w.segment = p.segment;
+    w.per_seq = p.per_seq;
+    w.items = p.items;
+    w.slots = p.cut ? static_cast<float *>(slots) : nullptr;
+}
+
+}  // namespace
+
+long long attention_workspace(bool grad, const Batch &b, bool packed, int H, int KV, int Dk,
+                              int Dv)
+{
+    const long long fwd = segment_plan(b, packed, H, Dk, Dv).slots;
+    if (!grad)
+        return round16(fwd);
+    const long long turned = segment_plan(b, packed, H, Dv, Dk).slots;
+    const long long parts = KV == H ? 0 : 4LL * b.rows * H * std::max(Dk, Dv);
+    return round16(std::max(fwd, turned)) + round16(parts);
+}
+
+int launch_attention_fwd(const AttentionArgs &a, void *stream)
+{
+    Walk w{};
+    place(w, a.batch, a.H, a.Dk, a.Dv, a.workspace);
+    w.q = a.q; w.k = a.k; w.v = a.v; w.out = a.y;
+    w.ldq = a.ldq; w.ldk = a.ldk; w.ldv = a.ldv; w.ldo = a.ldy;
+    w.gq = 1;
+    w.gk = w.gv = a.H / a.KV;
+    w.log_decay = a.log_decay; w.state0 = a.h0; w.state1 = a.hT;
+    w.s0 = w.s1 = a.scale;
+    w.s2 = 1.0f;
+    return walk(a.type, w, static_cast<hipStream_t>(stream));
+}
+
+int launch_attention_grad(const AttentionArgs &a, void *stream)
+{
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int group = a.H / a.KV;
+    const long long slots = round16(
+        std::max(segment_plan(a.batch, a.batch.off != nullptr, a.H, a.Dk, a.Dv).slots,
+                 segment_plan(a.batch, a.batch.off != nullptr, a.H, a.Dv, a.Dk).slots));
+    float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + slots);
+    auto shared = [&](void *out, long long ldo, int D) {
+        return with_type(a.type, [&](auto *t) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            const long long blocks = cdiv((long long)a.batch.rows * a.KV * D, 256);
+            if (blocks > 0x7fffffffLL)
+                return (int)DWCONV_ERR_BAD_DIM;
+            return blocks == 0 ? (int)DWCONV_OK
+                               : dwconv::launch_kernel(k_shared<T>, grid_of(blocks), dim3(256), 0,
+                                                       st, (const float *)part,
+                                                       static_cast<T *>(out), ldo, a.batch.rows,
+                                                       a.H, a.KV, D);
+        });
+    };
+    int rc = DWCONV_OK;
+    if (a.dq) {
+        Walk w{};
+        place(w, a.batch, a.H, a.Dv, a.Dk, a.workspace);
+        w.q = a.dy; w.k = a.v; w.v = a.k; w.out = a.dq;
+        w.ldq = a.lddy; w.ldk = a.ldv; w.ldv = a.ldk; w.ldo = a.lddq;
+        w.gq = 1;
+        w.gk = w.gv = group;
+        w.log_decay = a.log_decay; w.state0 = a.h0; w.flip = true;
+        w.s0 = w.s1 = a.scale;
+        w.s2 = 1.0f;
+        rc = walk(a.type, w, st);
+    }
+    // dk, and the state's gradient with it
+    if (rc == DWCONV_OK && (a.dk || a.dh0)) {
+        Walk w{};
+        place(w, a.batch, a.H, a.Dv, a.Dk, a.workspace);
+        w.q = a.v; w.k = a.dy; w.v = a.q;
+        w.ldq = a.ldv; w.ldk = a.lddy; w.ldv = a.ldq;
+        w.gq = group;
+        w.gk = w.gv = 1;
+        w.out = a.dk; w.ldo = a.lddk;
+        if (group > 1 && a.dk) {
+            w.out = part;
+            w.ldo = (long long)a.H * a.Dk;
+            w.out32 = true;
+        }
+        w.log_decay = a.log_decay; w.state0 = a.dhT; w.state1 = a.dh0; w.flip = true;
+        w.s0 = w.s2 = a.scale;
+        w.s1 = 1.0f;
+        w.late = w.back = 1;
+        rc = walk(a.type, w, st);
+        if (rc == DWCONV_OK && w.out32)
+            rc = shared(a.dk, a.lddk, a.Dk);
+    }
+    if (rc == DWCONV_OK && a.dv) {
+        Walk w{};
+        place(w, a.batch, a.H, a.Dk, a.Dv, a.workspace);
+        w.q = a.k; w.k = a.q; w.v = a.dy;
+        w.ldq = a.ldk; w.ldk = a.ldq; w.ldv = a.lddy;
+        w.gq = group;
+        w.gk = w.gv = 1;
+        w.out = a.dv; w.ldo = a.lddv;
+        if (group > 1) {
+            w.out = part;
+            w.ldo = (long long)a.H * a.Dv;
+            w.out32 = true;
+        }
+        w.log_decay = a.log_decay; w.state0 = a.dhT;
+        w.s0 = w.s2 = a.scale;
+        w.s1 = 1.0f;
+        w.late = w.back = 1;
+        rc = walk(a.type, w, st);
+        if (rc == DWCONV_OK && w.out32)
+            rc = shared(a.dv, a.lddv, a.Dv);
+    }
+    return rc;
+}
+
+int launch_attention_step(const AttentionArgs &a, void *stream)
+{
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const long long blocks = (long long)a.batch.seqs * a.H;
+    if (blocks > 0x7fffffffLL)
+        return DWCONV_ERR_BAD_DIM;
+    return with_type(a.type, [&](auto *t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        auto run = [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            const int tx = (int)cdiv(a.Dv, V), ty = 256 / tx;
+            return dwconv::launch_kernel(k_attention_step<T, V>, grid_of(blocks), dim3(256), 0, st,
+                                         a, tx, ty);
+        };
+        return a.Dv % 4 == 0 ? run(std::integral_constant<int, 4>())
+                             : run(std::integral_constant<int, 1>());
+    });
+}
+
+}  // namespace dwmix

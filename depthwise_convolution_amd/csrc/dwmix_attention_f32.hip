@@ -1,0 +1,7 @@
+// dwmix_attention_f32.hip -- the walk of linear attention for float32 elements.
+#define DWMIX_ATTENTION_KERNELS
+#include "dwmix_attention.h"
+
+namespace dwmix {
+template int launch_walk<float>(const Walk &w, hipStream_t st);
+}  // namespace dwmix

@@ -10,6 +10,23 @@ namespace dwmix {
 using dwseq::Batch;
 using dwseq::cdiv;
 
+// ---- linear attention with a decay for each head ----
+struct AttentionArgs {
+    const void *q, *k, *v, *dy;
+    const float *log_decay, *h0, *dhT;
+    void *y, *dq, *dk, *dv, *workspace;
+    float *hT, *h, *dh0;
+    long long ldq, ldk, ldv, ldy, lddy, lddq, lddk, lddv;
+    float scale;
+    int type, H, KV, Dk, Dv;
+    Batch batch;
+};
+long long attention_workspace(bool grad, const Batch &b, bool packed, int H, int KV, int Dk,
+                              int Dv);
+int launch_attention_fwd(const AttentionArgs &a, void *stream);
+int launch_attention_step(const AttentionArgs &a, void *stream);
+int launch_attention_grad(const AttentionArgs &a, void *stream);
+
 // ---- group normalisation ----
 struct NormArgs {
     const void *x, *dy;

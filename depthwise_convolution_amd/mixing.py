@@ -3,6 +3,8 @@
 What a token-mixing block or a separable convolution net has beside its filters
 and the operators of ``sequence``:
 
+* ``linear_attention``, ``linear_attention_step``, ``linear_attention_grad``:
+  linear attention with a decay for each head;
 * ``group_norm``, ``group_norm_grad``: group normalisation with an activation,
   channels last;
 * ``quantize_rows``, ``linear_i8``: matrix product in 8-bit integers with a
@@ -22,11 +24,16 @@ from .sequence import (_act, _dense, _gpu, _needed, _rows, _size, _space, _start
 T_I8 = 3                     # DWCONV_T_I8
 I8_MAX_K = 131071            # DWCONV_I8_MAX_K
 
-MIX_EXPORTS = ("dwconv_norm_workspace_size", "dwconv_norm_fwd", "dwconv_norm_grad",
+ATTENTION_MAX_DIM = 256      # DWCONV_ATTENTION_MAX_DIM
+
+MIX_EXPORTS = ("dwconv_attention_workspace_size", "dwconv_attention_fwd", "dwconv_attention_step",
+               "dwconv_attention_grad",
+               "dwconv_norm_workspace_size", "dwconv_norm_fwd", "dwconv_norm_grad",
                "dwconv_quantize_rows", "dwconv_linear_i8_workspace_size",
                "dwconv_linear_i8_describe", "dwconv_linear_i8")
 
-__all__ = ["group_norm", "group_norm_grad", "quantize_rows", "linear_i8", "T_I8", "I8_MAX_K", "MIX_EXPORTS", *MIX_EXPORTS]
+__all__ = ["linear_attention", "linear_attention_step", "linear_attention_grad",
+           "ATTENTION_MAX_DIM", "group_norm", "group_norm_grad", "quantize_rows", "linear_i8", "T_I8", "I8_MAX_K", "MIX_EXPORTS", *MIX_EXPORTS]
 
 
 def declare(L):
@@ -34,6 +41,12 @@ def declare(L):
     i, vp, ll, f = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_float
     out = ctypes.POINTER(ll)
     row = [vp, ll]
+    seq, heads = [i, ll, vp], [i, i, i, i]
+    L.dwconv_attention_workspace_size.argtypes = [i, i, i, ll, i, *heads, out]
+    L.dwconv_attention_fwd.argtypes = [*row * 3, i, vp, f, vp, *row, vp, vp, ll, *seq, *heads, vp]
+    L.dwconv_attention_step.argtypes = [*row * 3, i, vp, f, vp, *row, i, *heads, vp]
+    L.dwconv_attention_grad.argtypes = [*row * 4, i, vp, f, vp, vp, *row * 3, vp, vp, ll, *seq,
+                                        *heads, vp]
     L.dwconv_norm_workspace_size.argtypes = [i, i, ll, ll, i, i, out]
     L.dwconv_norm_fwd.argtypes = [*row, i, vp, vp, f, i, *row, vp, vp, ll, ll, ll, i, i, vp]
     L.dwconv_norm_grad.argtypes = [*row * 2, i, vp, vp, i, vp, *row, vp, vp, vp, ll, ll, ll, i, i,
@@ -63,6 +76,186 @@ def _is(t, dtype, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+# ---------------------------- linear attention with a decay for each head
+def _flat(t, name, x, shape=None):
+    """(address, row stride) of a tensor (..., heads, width) of x's type whose
+    rows are its last two axes."""
+    if not isinstance(t, _seq.torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t is not x:
+        _gpu(t, name, x)
+        if t.dtype is not x.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {x.dtype}")
+    if not t.is_contiguous():
+        heads, width = t.shape[-2:]
+        if (width > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != width):
+            raise ValueError(f"{name}: the last two axes must be contiguous")
+        # a head axis of one may have any stride, which a view of the rows must not see
+        t = t.as_strided((*t.shape[:-2], heads * width), (*t.stride()[:-2], 1))
+    else:
+        return t.data_ptr(), t.shape[-2] * t.shape[-1]
+    return _rows(t, name, t)
+
+
+def _heads(q, k, v, lead):
+    """(H, KV, Dk, Dv) of q (..., H, Dk), k (..., KV, Dk) and v (..., KV, Dv), which
+    have `lead` leading axes."""
+    T = _seq.torch.Tensor
+    if not isinstance(k, T) or not isinstance(v, T):
+        raise TypeError("k and v must be torch.Tensors")
+    if q.dim() != lead + 2:
+        raise ValueError(f"q must have {lead + 2} axes here, (..., heads, width)")
+    H, Dk = q.shape[-2:]
+    if k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != Dk:
+        raise ValueError("k must be (..., KV heads, Dk) with q's tokens and width")
+    KV = k.shape[-2]
+    if v.dim() != q.dim() or v.shape[:-1] != k.shape[:-1]:
+        raise ValueError("v must be (..., KV heads, Dv) with k's tokens and heads")
+    if KV < 1 or H % KV:
+        raise ValueError(f"{KV} heads of k and v do not divide the {H} heads of q")
+    return H, KV, Dk, v.shape[-1]
+
+
+def _sequences(q, offsets):
+    """(sequences, tokens, offsets' address, leading axes) of a dense or packed q."""
+    if offsets is None:
+        if q.dim() != 4:
+            raise ValueError("q must be (sequences, tokens, heads, width), or (tokens, heads, "
+                             "width) with offsets")
+        return q.shape[0], q.shape[1], None, 2
+    if q.dim() != 3:
+        raise ValueError("q must be (tokens, heads, width) when offsets are given")
+    seqs, tokens, off = _seq._batch(q.select(1, 0), offsets)
+    return seqs, tokens, off, 1
+
+
+def _scale(scale, Dk):
+    return Dk ** -0.5 if scale is None else scale
+
+
+def dwconv_attention_workspace_size(grad, dtype, seqs, tokens, packed, H, KV, Dk, Dv):
+    """Workspace bytes of dwconv_attention_fwd (grad false) or dwconv_attention_grad
+    (tokens: per sequence, or in all when packed)."""
+    return _size("dwconv_attention_workspace_size", int(bool(grad)), _code(dtype), seqs, tokens,
+                 int(bool(packed)), H, KV, Dk, Dv)
+
+
+def dwconv_attention_fwd(q, k, v, log_decay, y, hT=None, workspace=None, scale=None, h0=None,
+                         offsets=None, stream=None):
+    """y (..., H, Dv) of linear attention; hT receives the last states."""
+    code, st, ctx = _start(q, stream, "q")
+    if ctx is not None:
+        with ctx:
+            return dwconv_attention_fwd(q, k, v, log_decay, y, hT, workspace, scale, h0, offsets,
+                                        st)
+    seqs, tokens, off, lead = _sequences(q, offsets)
+    H, KV, Dk, Dv = _heads(q, k, v, lead)
+    f32, state = _seq._f32, (seqs, H, Dk, Dv)
+    _status(_library().dwconv_attention_fwd(
+        *_flat(q, "q", q), *_flat(k, "k", q), *_flat(v, "v", q), code,
+        _dense(_needed(log_decay, "log_decay"), "log_decay", q, f32, (H,)), _scale(scale, Dk),
+        _dense(h0, "h0", q, f32, state), *_flat(y, "y", q, (*q.shape[:-1], Dv)),
+        _dense(hT, "hT", q, f32, state), *_space(workspace, q), seqs, tokens, off, H, KV, Dk, Dv,
+        st), "dwconv_attention_fwd")
+    return y
+
+
+def linear_attention(q, k, v, log_decay, h0=None, offsets=None, scale=None, stream=None):
+    """(y, hT): linear attention with a decay for each head,
+
+        S = exp(log_decay) * S + k v^T,    y = scale * q S
+
+    token by token within each sequence.  q is (sequences, tokens, H, Dk), or
+    (tokens, H, Dk) with offsets, k (..., KV, Dk) and v (..., KV, Dv) alike; KV
+    divides H, adjacent query heads sharing a key and value head.  log_decay is
+    (H,) float32, at most 0, a constant.  y is (..., H, Dv) of q's type; h0 and
+    hT, the states before the first and after the last token, are (sequences, H,
+    Dk, Dv) float32.  scale is Dk ** -0.5 by default."""
+    _, st, ctx = _start(q, stream, "q")
+    if ctx is not None:
+        with ctx:
+            return linear_attention(q, k, v, log_decay, h0, offsets, scale, st)
+    seqs, tokens, off, lead = _sequences(q, offsets)
+    H, KV, Dk, Dv = _heads(q, k, v, lead)
+    ws = _workspace(dwconv_attention_workspace_size(False, q.dtype, seqs, tokens, off is not None,
+                                                    H, KV, Dk, Dv), q)
+    y = q.new_empty((*q.shape[:-1], Dv))
+    hT = q.new_empty((seqs, H, Dk, Dv), dtype=_seq._f32)
+    dwconv_attention_fwd(q, k, v, log_decay, y, hT, ws, scale, h0, offsets, st)
+    return y, hT
+
+
+def dwconv_attention_step(q, k, v, log_decay, h, y, scale=None, stream=None):
+    """One token for each sequence; h (sequences, H, Dk, Dv) float32 in place."""
+    code, st, ctx = _start(q, stream, "q")
+    if ctx is not None:
+        with ctx:
+            return dwconv_attention_step(q, k, v, log_decay, h, y, scale, st)
+    H, KV, Dk, Dv = _heads(q, k, v, 1)
+    seqs, f32 = q.shape[0], _seq._f32
+    _status(_library().dwconv_attention_step(
+        *_flat(q, "q", q), *_flat(k, "k", q), *_flat(v, "v", q), code,
+        _dense(_needed(log_decay, "log_decay"), "log_decay", q, f32, (H,)), _scale(scale, Dk),
+        _dense(_needed(h, "h"), "h", q, f32, (seqs, H, Dk, Dv)),
+        *_flat(y, "y", q, (seqs, H, Dv)), seqs, H, KV, Dk, Dv, st), "dwconv_attention_step")
+    return y
+
+
+def linear_attention_step(q, k, v, log_decay, h, scale=None, stream=None):
+    """y (sequences, H, Dv) for one token of each sequence, q (sequences, H, Dk);
+    the states h (sequences, H, Dk, Dv) float32 are updated in place."""
+    _, st, ctx = _start(q, stream, "q")
+    if ctx is not None:
+        with ctx:
+            return linear_attention_step(q, k, v, log_decay, h, scale, st)
+    _, _, _, Dv = _heads(q, k, v, 1)
+    return dwconv_attention_step(q, k, v, log_decay, h, q.new_empty((*q.shape[:-1], Dv)), scale,
+                                 st)
+
+
+def dwconv_attention_grad(dy, q, k, v, log_decay, dq, dk, dv, dh0=None, workspace=None, scale=None,
+                          h0=None, dhT=None, offsets=None, stream=None):
+    """Gradients of linear_attention into dq, dk, dv and dh0, each of which may be None."""
+    code, st, ctx = _start(q, stream, "q")
+    if ctx is not None:
+        with ctx:
+            return dwconv_attention_grad(dy, q, k, v, log_decay, dq, dk, dv, dh0, workspace,
+                                         scale, h0, dhT, offsets, st)
+    seqs, tokens, off, lead = _sequences(q, offsets)
+    H, KV, Dk, Dv = _heads(q, k, v, lead)
+    f32, state = _seq._f32, (seqs, H, Dk, Dv)
+    out = [(None, 0) if t is None else _flat(t, name, q, like.shape)
+           for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v))]
+    _status(_library().dwconv_attention_grad(
+        *_flat(dy, "dy", q, (*q.shape[:-1], Dv)), *_flat(q, "q", q), *_flat(k, "k", q),
+        *_flat(v, "v", q), code, _dense(_needed(log_decay, "log_decay"), "log_decay", q, f32,
+                                        (H,)), _scale(scale, Dk),
+        _dense(h0, "h0", q, f32, state), _dense(dhT, "dhT", q, f32, state), *out[0], *out[1],
+        *out[2], _dense(dh0, "dh0", q, f32, state), *_space(workspace, q), seqs, tokens, off, H,
+        KV, Dk, Dv, st), "dwconv_attention_grad")
+    return dq, dk, dv, dh0
+
+
+def linear_attention_grad(dy, q, k, v, log_decay, h0=None, dhT=None, offsets=None, scale=None,
+                          stream=None):
+    """(dq, dk, dv, dh0) of linear_attention for the cotangents dy of y and dhT (or
+    None) of hT.  dh0 (sequences, H, Dk, Dv) float32 is None unless h0 is given."""
+    _, st, ctx = _start(q, stream, "q")
+    if ctx is not None:
+        with ctx:
+            return linear_attention_grad(dy, q, k, v, log_decay, h0, dhT, offsets, scale, st)
+    seqs, tokens, off, lead = _sequences(q, offsets)
+    H, KV, Dk, Dv = _heads(q, k, v, lead)
+    ws = _workspace(dwconv_attention_workspace_size(True, q.dtype, seqs, tokens, off is not None,
+                                                    H, KV, Dk, Dv), q)
+    dq, dk, dv = (q.new_empty(t.shape) for t in (q, k, v))
+    dh0 = None if h0 is None else q.new_empty((seqs, H, Dk, Dv), dtype=_seq._f32)
+    return dwconv_attention_grad(dy, q, k, v, log_decay, dq, dk, dv, dh0, ws, scale, h0, dhT,
+                                 offsets, st)
 
 
 # ------------------------------- group normalisation with an activation

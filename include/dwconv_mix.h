@@ -28,7 +28,7 @@ extern "C" {
  * numbers above 0 count as 0, minus infinity forgets everything.  h0 and hT,
  * the state after the last token (h0 itself for a sequence of none; NULL to
  * skip), are [seqs][H][Dk][Dv] float32.  scale is finite.  Dk and Dv are at most
- * DWCONV_ATTENTION_MAX_DIM.
+ * DWCONV_ATTENTION_MAX_DIM; row strides are below 2^21 elements.
  *
  * Tokens are taken in chunks.  For 16-bit types the scores q[i] . k[j] of a
  * chunk, times their decay, and the state that a chunk starts from are rounded
