@@ -166,7 +166,8 @@ struct Item {
         row0 = seq_start(b, seq);
         length = max(seq_start(b, seq + 1) - row0, 0);
     }
-    __device__ __forceinline__ int segments(const Walk &w) const
+    __device__ __forceinline__ int segments(const Walk &w) const { return count(w, length); }
+    static __device__ __forceinline__ int count(const Walk &w, int length)
     {
         return max(1, (int)(((long long)length + w.segment - 1) / w.segment));
     }
@@ -802,10 +803,11 @@ __global__ __launch_bounds__(256) void k_link(Walk w, int blocks)
     const long long seq = id / blocks / w.H;
     if (seq >= w.batch.seqs || at >= w.Dk * w.Dv)
         return;
-    const int first = w.batch.off ? seq_start(w.batch, (int)seq) / w.segment + (int)seq
-                                  : (int)seq * w.per_seq;
-    const Item it(w, first);
-    const int count = it.segments(w);
+    // (from the sequence itself: offsets that break the rules might lead an item's
+    // search to another one, with more slots than there are from here on)
+    const int row0 = seq_start(w.batch, (int)seq), end = seq_start(w.batch, (int)seq + 1);
+    const int first = w.batch.off ? row0 / w.segment + (int)seq : (int)seq * w.per_seq;
+    const int count = Item::count(w, max(end - row0, 0));
     if (count == 1)
         return;
     const float ld = log_decay_of(w.log_decay, h);
