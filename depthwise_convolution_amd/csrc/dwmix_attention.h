@@ -14,17 +14,18 @@
 // the walk, each segment from its own start.  Where there are enough sequences
 // and heads to fill the chip a sequence is one segment, and the walk is all.
 //
-// A workgroup of 4 waves walks one head of one segment, a tile of DVT of the state's
-// columns, in chunks of 128 bytes of tokens (64 16-bit, 32 float32):
+// A workgroup walks one head of one segment, a tile of DVT of the state's columns
+// with a wave for each 16 of them, in chunks of 128 bytes of tokens (64 16-bit, 32
+// float32):
 //
-//   scores   P[i, j] of 16 rows i a wave, times their decay, through LDS to all waves
-//   output   a wave takes DVT / 4 columns for all rows: its part of S is in registers
+//   scores   P[i, j], some tiles of 16 x 16 a wave, times their decay, through LDS
+//   output   a wave takes its 16 columns for all rows: its part of S is in registers
 //            (float32, as the matrix instructions leave it), which is already the
 //            layout of an operand that is summed over dk, so q S reads only q;
 //            then P V on top
 //   state    S = a^n S + K^T (V with its decays), the same columns
 //
-// so that LDS holds q, k, v and P (56 KB for widths of 128), a state never
+// so that LDS holds q, k, v and P (60 KB for widths of 128), a state never
 // leaves its registers, and two workgroups share a CU.
 //
 // Roundings of 16-bit types.  P and the chunk's S are rounded once where they become
@@ -186,45 +187,39 @@ __device__ __forceinline__ long long state_at(const Walk &w, bool flip, int dk, 
     return flip ? (long long)dv * w.Dk + dk : (long long)dk * w.Dv + dv;
 }
 
-constexpr int kWaves = 4, kThr = kWaves * 64, kChunkBytes = 128;
+constexpr int kChunkBytes = 128;
 
 constexpr int kFar = 0x7ffffff0;        // beyond every descriptor's bounds
 
 // A tile of C rows of D elements in LDS, 16 bytes between the rows: the reads below,
 // of 16 rows at one chunk of 16 bytes, of 8 rows two apart at 32 bytes, or of 4 at 64,
 // fall on different banks, and what differs between the reads of a lane is a constant.
-template <typename T, int C, int D> struct Tile {
+template <typename T, int C, int D, int kThr> struct Tile {
     static constexpr int size = (int)sizeof(T), elems = 16 / size;
     static constexpr int per_row = D / elems, pitch = D * size + 16, bytes = C * pitch;
     static constexpr int count = C * per_row / kThr;    // chunks a thread stages
     static constexpr int apart = kThr / per_row;        // rows between them
     static_assert(count >= 1 && C * per_row % kThr == 0);
 
-    // The bytes from the chunk of tokens' lowest row on of what a thread stages, and
-    // from one of its rows to the next.
-    struct From {
-        int first, step, row, col;
-        __device__ __forceinline__ From(long long ld, bool back)
-            : row((int)threadIdx.x / per_row), col((int)threadIdx.x % per_row * elems)
-        {
-            const int pitch_in = (int)ld * size;
-            first = (back ? C - 1 - row : row) * pitch_in + col * size;
-            step = (back ? -apart : apart) * pitch_in;
-        }
-    };
     // The chunk's rows, `left` of them, columns up to `wide`, from the row of lowest
     // address on (which may lie before the array where `left` is less than C).
-    static __device__ __forceinline__ void fetch(u32x4 (&regs)[count], const T *lowest,
-                                                 const From &f, int left, int wide)
+    // ODD: some width is no whole number of chunks (kernels of their own, as what
+    // they need for it would cost the others their registers).
+    template <bool ODD>
+    static __device__ __forceinline__ void fetch(u32x4 (&regs)[count], const T *lowest, int ld,
+                                                 bool back, int left, int wide, int thread)
     {
         const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(lowest, kFar - 16);
-        if (wide % elems == 0) {
+        const int row = thread / per_row, col = thread % per_row * elems;
+        const int first = (back ? C - 1 - row : row) * (ld * size) + col * size;
+        const int step = (back ? -apart : apart) * (ld * size);
+        if constexpr (!ODD) {
 #pragma unroll
             for (int k = 0; k < count; ++k) {
-                const bool in = f.row + k * apart < left && f.col < wide;
+                const bool in = row + k * apart < left && col < wide;
                 regs[k] = __builtin_bit_cast(
                     u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                               rsrc, in ? f.first + k * f.step : kFar, 0, 0));
+                               rsrc, in ? first + k * step : kFar, 0, 0));
             }
         } else {        // rows that end within a chunk: element by element
 #pragma unroll
@@ -232,8 +227,8 @@ template <typename T, int C, int D> struct Tile {
                 unsigned v[elems];
 #pragma unroll
                 for (int e = 0; e < elems; ++e) {
-                    const bool in = f.row + k * apart < left && f.col + e < wide;
-                    const int at = in ? f.first + k * f.step + e * size : kFar;
+                    const bool in = row + k * apart < left && col + e < wide;
+                    const int at = in ? first + k * step + e * size : kFar;
                     if constexpr (size == 2)
                         v[e] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
                     else
@@ -247,9 +242,10 @@ template <typename T, int C, int D> struct Tile {
             }
         }
     }
-    static __device__ __forceinline__ void keep(lds_ptr lds, const u32x4 (&regs)[count])
+    static __device__ __forceinline__ void keep(lds_ptr lds, const u32x4 (&regs)[count],
+                                                int thread)
     {
-        const int row = (int)threadIdx.x / per_row, c = (int)threadIdx.x % per_row;
+        const int row = thread / per_row, c = thread % per_row;
 #pragma unroll
         for (int k = 0; k < count; ++k)
             *(lds_u4)(lds + (row + k * apart) * pitch + c * 16) = regs[k];
@@ -349,29 +345,31 @@ __device__ __forceinline__ float finite_size(float v)
 
 template <typename T, int DK, int DVT> struct Body {
     static constexpr int size = (int)sizeof(T), elems = 16 / size;
+    static constexpr int waves = DVT / 16, threads = waves * 64;
     static constexpr int C = kChunkBytes / size;        // tokens of a chunk
     static constexpr int CT = C / 16;                   // 16-row tiles of it
     static constexpr int span = 4 * elems;              // that a product sums over
     static constexpr int KS = C / span;                 // parts of a chunk's tokens
     static constexpr int NT = DK / 16, US = DK / span;  // tiles and parts of dk
-    static constexpr int MT = DVT / kWaves / 16;        // tiles of a wave's columns
+    // score tiles of a wave, side by side in a row of tiles
+    static constexpr int JT = CT * CT > waves ? CT * CT / waves : 1;
     static constexpr int parts = std::is_same_v<T, bf16> ? 3 : std::is_same_v<T, f16> ? 2 : 1;
     static constexpr bool is_f16 = std::is_same_v<T, f16>;
-    using QK = Tile<T, C, DK>;
-    using VV = Tile<T, C, DVT>;
-    using PP = Tile<T, C, C>;                           // scores
-
+    using QK = Tile<T, C, DK, threads>;
+    using VV = Tile<T, C, DVT, threads>;
+    static constexpr int pitch = kChunkBytes + 16;      // of the scores' rows in LDS
     // powers of the decay in LDS: number k is a^(C - k), and 0 from C + 1 on
     static constexpr int powers = 2 * C;
     typedef __attribute__((address_space(3))) const float *table;
 
-    f32x4 S[NT][MT];
-    int lane, wave, g, i;
+    f32x4 S[NT];        // rows 16 n + 4 g .. + 3 of column i of the wave's
+    int thread, lane, wave, g, i;
     table pw;
 
     __device__ __forceinline__ explicit Body(table powers_)
-        : lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
-          g(lane >> 4), i(lane & 15), pw(powers_)
+        : thread(threadIdx.x), lane(thread & 63),
+          wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), g(lane >> 4), i(lane & 15),
+          pw(powers_)
     {
     }
     static __device__ __forceinline__ void fill(float *to, float ld)
@@ -380,188 +378,229 @@ template <typename T, int DK, int DVT> struct Body {
             to[threadIdx.x] =
                 (int)threadIdx.x <= C ? expf(ld * (float)(C - (int)threadIdx.x)) : 0.0f;
     }
-    // At the start of a chunk: what follows from the lane is made anew, as it would
-    // otherwise be kept for all chunks, in more registers than there are.
+    // At the start of a chunk and at the end: what follows from the lane is made anew, as
+    // it would otherwise be kept over all chunks, in more registers than there are.
     __device__ __forceinline__ void next_chunk()
     {
-        asm volatile("" : "+v"(lane));
+        asm volatile("" : "+v"(thread));
+        lane = thread & 63;
         g = lane >> 4;
         i = lane & 15;
     }
 
-    // first of the wave's columns within the tile
-    __device__ __forceinline__ int col0() const { return wave * (DVT / kWaves); }
-
-    // f(S element, dk, dv) for what the state has; dv counts from the tile's first
-    template <typename F> __device__ __forceinline__ void each(const Walk &w, int dv0, F f)
+    // Where an element is in a state array that is [Dk][Dv], or flipped: bytes from its
+    // start, or far away.
+    __device__ __forceinline__ int place(const Walk &w, bool flip, int dv0, int n, int r) const
     {
+        const int dk = n * 16 + g * 4 + r, dv = dv0 + wave * 16 + i;
+        return dk < w.Dk && dv < w.Dv ? (flip ? dv * w.Dk + dk : dk * w.Dv + dv) * 4 : kFar;
+    }
+    // The state from memory (nullptr: zero) and to it.
+    __device__ __forceinline__ void load_state(const Walk &w, const float *from, bool flip,
+                                               int dv0)
+    {
+        // an empty descriptor reads as zero
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(from, from ? kFar - 16 : 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            unsigned v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, place(w, flip, dv0, n, r), 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[n][r] = __builtin_bit_cast(float, v[r]);
+        }
+    }
+    __device__ __forceinline__ void store_state(const Walk &w, float *to, bool flip,
+                                                int dv0) const
+    {
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(to, kFar - 16);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int dk = n * 16 + g * 4 + r, dv = dv0 + col0() + m * 16 + i;
-                    float v = S[n][m][r];
-                    f(v, dk, dv, dk < w.Dk && dv < w.Dv);
-                    S[n][m][r] = v;
-                }
+            for (int r = 0; r < 4; ++r) {
+                const float v = S[n][r];
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rsrc,
+                                                      place(w, flip, dv0, n, r), 0, 0);
+            }
     }
 
     // The wave's columns of V, as operands that are summed across the rows.
-    __device__ __forceinline__ void columns(lds_ptr v, u32x4 (&f)[KS][MT]) const
+    __device__ __forceinline__ void columns(lds_ptr v, u32x4 (&f)[KS]) const
     {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                f[ks][m] = VV::across(v, col0() + m * 16, ks, lane);
+            f[ks] = VV::across(v, wave * 16, ks, lane);
     }
 
-    // Whether the wave's columns hold an infinity or a NaN.
-    __device__ __forceinline__ bool strange(const u32x4 (&f)[KS][MT]) const
+    // Whether they hold an infinity or a NaN, which are taken out.  (No matrix
+    // instruction is at work here: see settle.)
+    __device__ __forceinline__ bool strange(u32x4 (&f)[KS]) const
     {
         unsigned odd = 0;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int e = 0; e < 4; ++e)
+                odd |= odd_bits<T>(f[ks][e]);
+        const bool any = __any(odd != 0);
+        if (any)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    odd |= odd_bits<T>(f[ks][m][e]);
-        return __any(odd != 0);
+                    f[ks][e] = cleaned<T>(f[ks][e]);
+        return any;
     }
 
-    // S = a^n S + s2 K^T (V with its decays)
-    __device__ __forceinline__ void update(const Walk &w, lds_ptr k, const u32x4 (&vf)[KS][MT],
-                                           bool any, int n, float a_n)
+    // x as `parts` numbers of T, pairs of them to a word.  bfloat16: the upper halves
+    // of x, of what they leave, and of what that leaves, 8 bits each.
+    static __device__ __forceinline__ void split(const float (&x)[elems], u32x4 (&p)[parts])
     {
-        const float s2 = w.s2;
-        const int late = w.late;
+        if constexpr (std::is_same_v<T, bf16>) {
+            unsigned w[elems];
+#pragma unroll
+            for (int e = 0; e < elems; ++e)
+                w[e] = __builtin_bit_cast(unsigned, x[e]);
+#pragma unroll
+            for (int q = 0; q < parts; ++q) {
+#pragma unroll
+                for (int e = 0; e < elems; e += 2)      // the upper halves of two words
+                    p[q][e / 2] = __builtin_amdgcn_perm(w[e + 1], w[e], 0x07060302u);
+                if (q + 1 < parts)
+#pragma unroll
+                    for (int e = 0; e < elems; ++e)
+                        w[e] = __builtin_bit_cast(
+                            unsigned, __builtin_bit_cast(float, w[e]) -
+                                          __builtin_bit_cast(float, w[e] & 0xffff0000u));
+            }
+        } else {
+            float rest[elems];
+#pragma unroll
+            for (int e = 0; e < elems; ++e)
+                rest[e] = x[e];
+#pragma unroll
+            for (int q = 0; q < parts; ++q) {
+                unsigned word[4];
+                narrow<T, elems>(rest, word);
+                p[q] = u32x4{word[0], word[1], word[2], word[3]};
+                if (q + 1 < parts)
+#pragma unroll
+                    for (int e = 0; e < elems; ++e)
+                        rest[e] -= element<T>(p[q], e);
+            }
+        }
+    }
+
+    // S = a^n S + s2 K^T (V with its decays).  vf: the wave's columns of V, without
+    // infinities and NaN where there are `any`, which are added one by one: split in
+    // parts they would leave NaN, and so would the zeros beside k's columns.
+    __device__ __forceinline__ void update(const Walk &w, lds_ptr k, lds_ptr v,
+                                           const u32x4 (&vf)[KS], bool any, int n, float a_n)
+    {
         float up = 1.0f;
         if constexpr (is_f16) {     // small values would lose their last bits
             float most = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int e = 0; e < elems; ++e)
-                        most = fmaxf(most, finite_size(element<T>(vf[ks][m], e)));
-            up = range_scale(wave_max(most) * fabsf(s2), 0x1p-3f, 0x1p14f);
+                for (int e = 0; e < elems; ++e)
+                    most = fmaxf(most, finite_size(element<T>(vf[ks], e)));
+            up = range_scale(wave_max(most) * fabsf(w.s2), 0x1p-3f, 0x1p14f);
         }
-        const float keep = a_n * up;
-        const table late_pw = pw + (C - n + 1 - late) + VV::row_of(0, g, 0);
+        const float keep = a_n * up, s2 = w.s2 * up;
+        // a^(n - 1 - j + late) for row j
+        const table late_pw = pw + (C - n + 1 - w.late) + VV::row_of(0, g, 0);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                S[t][m] *= keep;
+            S[t] *= keep;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            u32x4 p[MT][parts];
-            float f[elems];
+            float x[elems];
+            u32x4 p[parts];
 #pragma unroll
-            for (int e = 0; e < elems; ++e)     // a^(n - 1 - j + late) for row j
-                f[e] = late_pw[VV::row_of(ks, 0, e)] * (s2 * up);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float rest[elems];
-#pragma unroll
-                for (int e = 0; e < elems; ++e)
-                    rest[e] = element<T>(vf[ks][m], e) * f[e];
-#pragma unroll
-                for (int q = 0; q < parts; ++q) {
-                    unsigned word[4];
-                    narrow<T, elems>(rest, word);
-                    p[m][q] = u32x4{word[0], word[1], word[2], word[3]};
-                    if (q + 1 < parts)
-#pragma unroll
-                        for (int e = 0; e < elems; ++e) {
-                            const float head = element<T>(p[m][q], e);
-                            // what an infinity leaves is not a number
-                            rest[e] = fabsf(head) <= 3.4e38f ? rest[e] - head : 0.0f;
-                        }
-                }
-            }
+            for (int e = 0; e < elems; ++e)
+                x[e] = element<T>(vf[ks], e) * (late_pw[VV::row_of(ks, 0, e)] * s2);
+            split(x, p);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const u32x4 kf = QK::across(k, t * 16, ks, lane);
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int q = 0; q < parts; ++q)
-                        mma<T>(kf, p[m][q], S[t][m]);
+                for (int q = 0; q < parts; ++q)
+                    mma<T>(kf, p[q], S[t]);
             }
         }
         settle();
         if constexpr (is_f16)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
+                S[t] *= 1.0f / up;
+        if (any)
+            for (int j = 0; j < n; ++j) {
+                const float x = VV::one(v, j, wave * 16 + i);
+                const float f = pw[C - n + 1 - w.late + j] * w.s2;
+                if (!(fabsf(x) <= 3.4e38f))
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    S[t][m] *= 1.0f / up;
-        if (any && w.Dk < DK)       // an infinity times the zeros beside k
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (t * 16 + g * 4 + r >= w.Dk)
-                            S[t][m][r] = 0.0f;
+                        for (int r = 0; r < 4; ++r)
+                            if (t * 16 + g * 4 + r < w.Dk)
+                                S[t][r] += f * QK::one(k, j, t * 16 + g * 4 + r) * x;
+            }
     }
 
-    // The scores of 16 rows, times their decay, to LDS; the power of two that they
-    // were divided by (float16) is returned.
+    // Some tiles of a row of scores, times their decay, to LDS; the power of two that
+    // they were divided by (float16) is returned.
     __device__ __forceinline__ float scores(lds_ptr q, lds_ptr k, lds_ptr p, float s0) const
     {
-        if (wave >= CT)
+        const int row = wave % CT * 16 + i, col0 = wave / CT * JT * 16;
+        if (wave / CT * JT >= CT)
             return 1.0f;
-        f32x4 acc[CT];
+        f32x4 acc[JT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
+        for (int t = 0; t < JT; ++t)
             acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int u = 0; u < US; ++u) {
-            const u32x4 qf = QK::chunk(q, wave * 16 + i, u * 4 + g);
+            const u32x4 qf = QK::chunk(q, row, u * 4 + g);
 #pragma unroll
-            for (int t = 0; t < CT; ++t)    // later tiles too: no branch (see settle)
-                mma<T>(QK::chunk(k, t * 16 + i, u * 4 + g), qf, acc[t]);
+            for (int t = 0; t < JT; ++t)    // later tokens' too: no branch (see settle)
+                mma<T>(QK::chunk(k, col0 + t * 16 + i, u * 4 + g), qf, acc[t]);
         }
-        const table gap_pw = pw + (C - wave * 16 - i + g * 4);
-        float most = 0.0f, down = 1.0f, v[CT][4];
+        const int ahead = row - col0 - g * 4;       // of the first of the lane's columns
+        const table gap_pw = pw + (C - ahead);
+        float most = 0.0f, down = 1.0f, v[JT][4];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
+        for (int t = 0; t < JT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int gap = wave * 16 + i - (t * 16 + g * 4 + r);
                 // a score of a later token may be anything
-                v[t][r] = gap >= 0 ? acc[t][r] * (s0 * gap_pw[t * 16 + r]) : 0.0f;
-                most = fmaxf(most, finite_size(v[t][r]));
+                v[t][r] = ahead >= t * 16 + r ? acc[t][r] * (s0 * gap_pw[t * 16 + r]) : 0.0f;
+                if constexpr (is_f16)
+                    most = fmaxf(most, finite_size(v[t][r]));
             }
         if constexpr (is_f16)
             down = range_scale(wave_max(most), 0x1p-2f, 0x1p14f);
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const int row = wave * 16 + i;
+        for (int t = 0; t < JT; ++t) {
             if constexpr (is_f16)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     v[t][r] *= down;
             // column 8a + 2m + h of a row is kept as number 4h + m of its chunk a: the
             // order in which across() reads the rows of V
+            const lds_ptr to = p + row * pitch + (col0 + t * 16) * size;
             if constexpr (size == 4) {
                 unsigned word[4];
                 narrow<T, 4>(v[t], word);
-                *(lds_u4)(p + row * PP::pitch + (t * 4 + g) * 16) =
-                    u32x4{word[0], word[1], word[2], word[3]};
+                *(lds_u4)(to + g * 16) = u32x4{word[0], word[1], word[2], word[3]};
             } else {
-                const lds_ptr at = p + row * PP::pitch + (t * 2 + (g >> 1)) * 16 + (g & 1) * 4;
                 const float even[2] = {v[t][0], v[t][2]}, odd[2] = {v[t][1], v[t][3]};
                 unsigned w0, w1;
                 narrow<T, 2>(even, &w0);
                 narrow<T, 2>(odd, &w1);
+                const lds_ptr at = to + (g >> 1) * 16 + (g & 1) * 4;
                 *(lds_u1)at = w0;
                 *(lds_u1)(at + 8) = w1;
             }
@@ -569,144 +608,112 @@ template <typename T, int DK, int DVT> struct Body {
         return down;
     }
 
-    // o[m][t]: 4 columns of m and row i of the 16 of tile t:  s1 a^(i+1-late) q S
-    __device__ __forceinline__ void from_state(lds_ptr q, f32x4 (&o)[MT][CT], float s1, int late)
+    // o[t]: columns 4 g .. + 3 of the wave's, row i of the 16 of tile t:
+    // s1 a^(i+1-late) q S
+    __device__ __forceinline__ void from_state(lds_ptr q, f32x4 (&o)[CT], float s1, int late)
     {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-                o[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < CT; ++t)
+            o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         float down = 1.0f;
         if constexpr (is_f16) {
             float most = 0.0f;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        most = fmaxf(most, finite_size(S[n][m][r]));
+                for (int r = 0; r < 4; ++r)
+                    most = fmaxf(most, finite_size(S[n][r]));
             down = range_scale(wave_max(most), 0x1p-2f, 0x1p14f);
         }
 #pragma unroll
         for (int u = 0; u < US; ++u) {
-            u32x4 sf[MT];
+            float f[elems];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float f[elems];
+            for (int e = 0; e < elems; ++e)
+                f[e] = S[u * (elems / 4) + e / 4][e % 4] * (is_f16 ? down : 1.0f);
+            unsigned word[4];
+            narrow<T, elems>(f, word);
+            const u32x4 sf = {word[0], word[1], word[2], word[3]};
 #pragma unroll
-                for (int e = 0; e < elems; ++e)
-                    f[e] = S[u * (elems / 4) + e / 4][m][e % 4] * (is_f16 ? down : 1.0f);
-                unsigned word[4];
-                narrow<T, elems>(f, word);
-                sf[m] = u32x4{word[0], word[1], word[2], word[3]};
-            }
-#pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                const u32x4 qf = QK::along(q, t * 16 + i, u, g);
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    mma<T>(sf[m], qf, o[m][t]);
-            }
+            for (int t = 0; t < CT; ++t)
+                mma<T>(sf, QK::along(q, t * 16 + i, u, g), o[t]);
         }
         const table row_pw = pw + (C - 1 + late - (CT - 1) * 16 - i);
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const float f = s1 * row_pw[(CT - 1 - t) * 16] / down;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                o[m][t] *= f;
-        }
+        for (int t = 0; t < CT; ++t)
+            o[t] *= s1 * row_pw[(CT - 1 - t) * 16] / down;
     }
 
-    // o += P V.  A V with infinities or NaN is taken apart: a zero score of a later
+    // o += P V.  Infinities and NaN of V are added one by one: a zero score of a later
     // token times those would be NaN.
     __device__ __forceinline__ void from_scores(lds_ptr p, lds_ptr v, const float *downs,
-                                                const u32x4 (&vf)[KS][MT], bool any,
-                                                f32x4 (&o)[MT][CT])
+                                                const u32x4 (&f)[KS], bool any, f32x4 (&o)[CT])
     {
-        auto scaled = [&](bool back) {
-            if constexpr (is_f16)
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    const float d = downs[t];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        o[m][t] *= back ? 1.0f / d : d;
-                }
+        // what the scores of row tile t, part ks, were divided by
+        auto down_of = [&](int t, int ks) {
+            return is_f16 ? downs[t + ks * (span / 16) / JT * CT] : 1.0f;
         };
-        scaled(false);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            u32x4 f[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                f[m] = vf[ks][m];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)     // a select: no branch (see settle)
-                    f[m][e] = any ? cleaned<T>(f[m][e]) : f[m][e];
-            }
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int t = 0; t < CT; ++t)
                 if (ks * span <= t * 16 + 15) {
-                    const u32x4 pf = PP::chunk(p, t * 16 + i, ks * 4 + g);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        mma<T>(f[m], pf, o[m][t]);
+                    const u32x4 pf = *(lds_u4)(p + (t * 16 + i) * pitch + (ks * 4 + g) * 16);
+                    if constexpr (is_f16) {
+                        const float d = down_of(t, ks);
+                        o[t] *= d;
+                        mma<T>(f[ks], pf, o[t]);
+                        o[t] *= 1.0f / d;
+                    } else {
+                        mma<T>(f[ks], pf, o[t]);
+                    }
                 }
-        }
         settle();
         if (any)
             for (int j = 0; j < C; ++j) {
-                const int slot = (j & ~7) | (j & 1) << 2 | (j >> 1 & 3);    // of column j
-                float x[MT][4];
+                // where column j of the scores is kept
+                const int slot = size == 4 ? j : (j & ~7) | (j & 1) << 2 | (j >> 1 & 3);
+                float x[4];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        x[m][r] = VV::one(v, j, col0() + m * 16 + g * 4 + r);
+                for (int r = 0; r < 4; ++r)
+                    x[r] = VV::one(v, j, wave * 16 + g * 4 + r);
 #pragma unroll
                 for (int t = 0; t < CT; ++t) {
-                    const float s = PP::one(p, t * 16 + i, size == 4 ? j : slot);
+                    const float s =
+                        (float)*(__attribute__((address_space(3))) const T *)(
+                            p + (t * 16 + i) * pitch + slot * size) / down_of(t, j / span);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (j <= t * 16 + i && !(fabsf(x[m][r]) <= 3.4e38f))
-                                o[m][t][r] += s * x[m][r];
+                    for (int r = 0; r < 4; ++r)
+                        if (j <= t * 16 + i && !(fabsf(x[r]) <= 3.4e38f))
+                            o[t][r] += s * x[r];
                 }
             }
-        scaled(true);
     }
 
     // The rows `here` of the chunk from token t on, 4 adjacent columns a lane.
-    template <typename E>
-    __device__ __forceinline__ void store(E *out, const Walk &w, const f32x4 (&o)[MT][CT],
+    template <bool ODD, typename E>
+    __device__ __forceinline__ void store(E *out, const Walk &w, const f32x4 (&o)[CT],
                                           long long row0, int t, int here, int h, int dv0) const
     {
         const int wide = w.Dv - dv0, ldo = (int)w.ldo * (int)sizeof(E);
         const long long lowest = w.back ? row0 - t - (C - 1) : row0 + t;
         const __amdgpu_buffer_rsrc_t rsrc =
             dwconv::make_rsrc(out + lowest * w.ldo + h * w.Dv + dv0, kFar - 16);
+        const int dv = wave * 16 + g * 4;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-            const int r = c * 16 + i, first = (w.back ? C - 1 - r : r) * ldo;
+            const int r = c * 16 + i;
+            const int at = (w.back ? C - 1 - r : r) * ldo + dv * (int)sizeof(E);
+            const f32x4 v = o[c];
+            const float s[4] = {v[0], v[1], v[2], v[3]};
+            if constexpr (!ODD) {
+                Raw<E, 4>(s).store(rsrc, r < here && dv < wide ? at : kFar, 0);
+            } else {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int dv = col0() + m * 16 + g * 4;
-                const f32x4 v = o[m][c];
-                const float s[4] = {v[0], v[1], v[2], v[3]};
-                const int at = first + dv * (int)sizeof(E);
-                if (wide % 4 == 0) {
-                    Raw<E, 4>(s).store(rsrc, r < here && dv < wide ? at : kFar, 0);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float one[1] = {s[e]};
-                        Raw<E, 1>(one).store(
-                            rsrc, r < here && dv + e < wide ? at + e * (int)sizeof(E) : kFar, 0);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float one[1] = {s[e]};
+                    Raw<E, 1>(one).store(
+                        rsrc, r < here && dv + e < wide ? at + e * (int)sizeof(E) : kFar, 0);
                 }
             }
         }
@@ -743,9 +750,12 @@ struct Part {
     }
 };
 
+// Two workgroups a CU, with registers for them.
+constexpr int waves_a_simd(int DK, int DVT) { return DK > 128 ? 1 : DVT / 16 * 2 / 4; }
+
 // The state that a segment adds by itself, to the slot of the next one.
-template <typename T, int DK, int DVT>
-__global__ __launch_bounds__(kThr, 2) void k_states(Walk w)
+template <typename T, int DK, int DVT, bool ODD>
+__global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_states(Walk w)
 {
     using B = Body<T, DK, DVT>;
     __shared__ alignas(16) char lds[B::QK::bytes + B::VV::bytes];
@@ -760,37 +770,37 @@ __global__ __launch_bounds__(kThr, 2) void k_states(Walk w)
     const float ld = log_decay_of(w.log_decay, part.h);
     B::fill(powers, ld);
     B b((typename B::table)powers);
-    b.each(w, part.dv0, [](float &v, int, int, bool) { v = 0.0f; });
+#pragma unroll
+    for (int n = 0; n < B::NT; ++n)
+        b.S[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int t0 = at.seg * w.segment, n = w.segment;       // a whole one
     const long long row = w.back ? (long long)at.row0 + at.length - 1 - t0 : at.row0 + t0;
     const Rows<T, B::C> k(w.k, w.ldk, w.back, row, part.h / w.gk * w.Dk),
         v(w.v, w.ldv, w.back, row, part.h / w.gv * w.Dv + part.dv0);
-    const typename B::QK::From fk(w.ldk, w.back);
-    const typename B::VV::From fv(w.ldv, w.back);
-    const int wide = w.Dv - part.dv0;
+    const int wide = w.Dv - part.dv0, ldk = (int)w.ldk, ldv = (int)w.ldv;
     const float whole = (float)exp((double)ld * B::C);
     u32x4 rk[B::QK::count], rv[B::VV::count];
-    B::QK::fetch(rk, k.at(0), fk, n, w.Dk);
-    B::VV::fetch(rv, v.at(0), fv, n, wide);
+    B::QK::template fetch<ODD>(rk, k.at(0), ldk, w.back, n, w.Dk, b.thread);
+    B::VV::template fetch<ODD>(rv, v.at(0), ldv, w.back, n, wide, b.thread);
     for (int t = 0; t < n; t += B::C) {
         const int here = min(B::C, n - t);
         b.next_chunk();
-        B::QK::keep(lk, rk);
-        B::VV::keep(lv, rv);
+        B::QK::keep(lk, rk, b.thread);
+        B::VV::keep(lv, rv, b.thread);
         __syncthreads();
-        B::QK::fetch(rk, k.at(t + B::C), fk, n - t - B::C, w.Dk);
-        B::VV::fetch(rv, v.at(t + B::C), fv, n - t - B::C, wide);
-        u32x4 vf[B::KS][B::MT];
+        B::QK::template fetch<ODD>(rk, k.at(t + B::C), ldk, w.back, n - t - B::C, w.Dk,
+                                   b.thread);
+        B::VV::template fetch<ODD>(rv, v.at(t + B::C), ldv, w.back, n - t - B::C, wide,
+                                   b.thread);
+        u32x4 vf[B::KS];
         b.columns(lv, vf);
-        b.update(w, lk, vf, b.strange(vf), here,
-                 here == B::C ? whole : expf(ld * (float)here));
+        const bool any = b.strange(vf);
+        b.update(w, lk, lv, vf, any, here, here == B::C ? whole : expf(ld * (float)here));
         __syncthreads();
     }
-    float *to = w.slots + ((long long)(part.item + 1) * w.H + part.h) * w.Dk * w.Dv;
-    b.each(w, part.dv0, [&](float &v, int dk, int dv, bool has) {
-        if (has)
-            to[state_at(w, false, dk, dv)] = v;
-    });
+    b.next_chunk();
+    b.store_state(w, w.slots + ((long long)(part.item + 1) * w.H + part.h) * w.Dk * w.Dv, false,
+                  part.dv0);
 }
 
 // The segments' own states, each to be added to what it gets from those before it.  A
@@ -833,12 +843,12 @@ __global__ __launch_bounds__(256) void k_link(Walk w, int blocks)
     }
 }
 
-template <typename T, int DK, int DVT>
-__global__ __launch_bounds__(kThr, 2) void k_walk(Walk w)
+template <typename T, int DK, int DVT, bool ODD>
+__global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_walk(Walk w)
 {
     using B = Body<T, DK, DVT>;
-    __shared__ alignas(16) char lds[2 * B::QK::bytes + B::VV::bytes + B::PP::bytes];
-    __shared__ float downs[kWaves], powers[B::powers];
+    __shared__ alignas(16) char lds[2 * B::QK::bytes + B::VV::bytes + B::C * B::pitch];
+    __shared__ float downs[B::waves], powers[B::powers];
     const lds_ptr lq = (lds_ptr)lds, lk = lq + B::QK::bytes, lv = lk + B::QK::bytes,
                   lp = lv + B::VV::bytes;
     if ((int)block_id() >= w.items * w.H * (int)((w.Dv + DVT - 1) / DVT))
@@ -855,59 +865,56 @@ __global__ __launch_bounds__(kThr, 2) void k_walk(Walk w)
     const long long own = ((long long)at.seq * w.H + part.h) * size;
     const float *from = at.seg ? w.slots + ((long long)part.item * w.H + part.h) * size
                                : w.state0 ? w.state0 + own : nullptr;
-    const bool flip = at.seg ? false : w.flip;
-    b.each(w, part.dv0, [&](float &v, int dk, int dv, bool has) {
-        v = from && has ? from[state_at(w, flip, dk, dv)] : 0.0f;
-    });
+    b.load_state(w, from, at.seg ? false : w.flip, part.dv0);
     const int t0 = at.seg * w.segment, n = min(w.segment, at.length - t0);
     const long long row = w.back ? (long long)at.row0 + at.length - 1 - t0 : at.row0 + t0;
     const Rows<T, B::C> q(w.q, w.ldq, w.back, row, part.h / w.gq * w.Dk),
         k(w.k, w.ldk, w.back, row, part.h / w.gk * w.Dk),
         v(w.v, w.ldv, w.back, row, part.h / w.gv * w.Dv + part.dv0);
-    const typename B::QK::From fq(w.ldq, w.back), fk(w.ldk, w.back);
-    const typename B::VV::From fv(w.ldv, w.back);
-    const int wide = w.Dv - part.dv0;
+    const int wide = w.Dv - part.dv0, ldq = (int)w.ldq, ldk = (int)w.ldk, ldv = (int)w.ldv;
     const float whole = (float)exp((double)ld * B::C);
     u32x4 rq[B::QK::count], rk[B::QK::count], rv[B::VV::count];
-    B::QK::fetch(rq, q.at(0), fq, n, w.Dk);
-    B::QK::fetch(rk, k.at(0), fk, n, w.Dk);
-    B::VV::fetch(rv, v.at(0), fv, n, wide);
+    B::QK::template fetch<ODD>(rq, q.at(0), ldq, w.back, n, w.Dk, b.thread);
+    B::QK::template fetch<ODD>(rk, k.at(0), ldk, w.back, n, w.Dk, b.thread);
+    B::VV::template fetch<ODD>(rv, v.at(0), ldv, w.back, n, wide, b.thread);
     for (int t = 0; t < n; t += B::C) {
         const int here = min(B::C, n - t);
         b.next_chunk();
-        B::QK::keep(lq, rq);
-        B::QK::keep(lk, rk);
-        B::VV::keep(lv, rv);
+        B::QK::keep(lq, rq, b.thread);
+        B::QK::keep(lk, rk, b.thread);
+        B::VV::keep(lv, rv, b.thread);
         __syncthreads();
-        B::QK::fetch(rq, q.at(t + B::C), fq, n - t - B::C, w.Dk);
-        B::QK::fetch(rk, k.at(t + B::C), fk, n - t - B::C, w.Dk);
-        B::VV::fetch(rv, v.at(t + B::C), fv, n - t - B::C, wide);
+        B::QK::template fetch<ODD>(rq, q.at(t + B::C), ldq, w.back, n - t - B::C, w.Dk,
+                                   b.thread);
+        B::QK::template fetch<ODD>(rk, k.at(t + B::C), ldk, w.back, n - t - B::C, w.Dk,
+                                   b.thread);
+        B::VV::template fetch<ODD>(rv, v.at(t + B::C), ldv, w.back, n - t - B::C, wide,
+                                   b.thread);
         __builtin_amdgcn_sched_barrier(0);
         const float down = b.scores(lq, lk, lp, w.s0);
         if (B::is_f16 && b.lane == 0)
             downs[b.wave] = down;
         __builtin_amdgcn_sched_barrier(0);
-        f32x4 o[B::MT][B::CT];
+        f32x4 o[B::CT];
         b.from_state(lq, o, w.s1, w.late);
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
-        u32x4 vf[B::KS][B::MT];
+        u32x4 vf[B::KS];
         b.columns(lv, vf);
         const bool any = b.strange(vf);
         b.from_scores(lp, lv, downs, vf, any, o);
-        b.update(w, lk, vf, any, here, here == B::C ? whole : expf(ld * (float)here));
-        __builtin_amdgcn_sched_barrier(0);
         if (w.out32)
-            b.store(static_cast<float *>(w.out), w, o, row, t, here, part.h, part.dv0);
+            b.template store<ODD>(static_cast<float *>(w.out), w, o, row, t, here, part.h,
+                                  part.dv0);
         else if (w.out)
-            b.store(static_cast<T *>(w.out), w, o, row, t, here, part.h, part.dv0);
+            b.template store<ODD>(static_cast<T *>(w.out), w, o, row, t, here, part.h, part.dv0);
+        __builtin_amdgcn_sched_barrier(0);
+        b.update(w, lk, lv, vf, any, here, here == B::C ? whole : expf(ld * (float)here));
         __syncthreads();
     }
+    b.next_chunk();
     if (w.state1 && at.seg + 1 == count)
-        b.each(w, part.dv0, [&](float &v, int dk, int dv, bool has) {
-            if (has)
-                w.state1[own + state_at(w, w.flip, dk, dv)] = v;
-        });
+        b.store_state(w, w.state1 + own, w.flip, part.dv0);
 }
 
 }  // namespace
@@ -917,11 +924,12 @@ template <typename T> int launch_walk(const Walk &w, hipStream_t st)
     const long long blocks = (long long)w.items * w.H * cdiv(w.Dv, walk_tile(w.Dk, w.Dv));
     if (blocks > 0x7fffffffLL)
         return DWCONV_ERR_BAD_DIM;
-    auto run = [&](auto dk, auto dvt) {
+    auto run_as = [&](auto dk, auto dvt, auto odd) {
         constexpr int DK = decltype(dk)::value, DVT = decltype(dvt)::value;
+        constexpr bool ODD = decltype(odd)::value;
         int rc = DWCONV_OK;
         if (w.slots) {
-            rc = dwconv::launch_kernel(k_states<T, DK, DVT>, grid_of(blocks), dim3(kThr), 0, st, w);
+            rc = dwconv::launch_kernel(k_states<T, DK, DVT, ODD>, grid_of(blocks), dim3(DVT * 4), 0, st, w);
             const int links = (int)cdiv(w.Dk * w.Dv, 256);
             if ((long long)w.batch.seqs * w.H * links > 0x7fffffffLL)
                 return (int)DWCONV_ERR_BAD_DIM;
@@ -930,8 +938,13 @@ template <typename T> int launch_walk(const Walk &w, hipStream_t st)
                                            dim3(256), 0, st, w, links);
         }
         if (rc == DWCONV_OK)
-            rc = dwconv::launch_kernel(k_walk<T, DK, DVT>, grid_of(blocks), dim3(kThr), 0, st, w);
+            rc = dwconv::launch_kernel(k_walk<T, DK, DVT, ODD>, grid_of(blocks), dim3(DVT * 4), 0, st, w);
         return rc;
+    };
+    const int whole = 16 / (int)sizeof(T);
+    auto run = [&](auto dk, auto dvt) {
+        return w.Dk % whole || w.Dv % whole ? run_as(dk, dvt, std::true_type())
+                                            : run_as(dk, dvt, std::false_type());
     };
     using std::integral_constant;
     if (w.Dk > 128)
