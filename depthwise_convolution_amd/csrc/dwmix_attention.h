@@ -153,15 +153,20 @@ struct Item {
             seq = item / w.per_seq;
             seg = item - seq * w.per_seq;
         } else {
-            int lo = 0, hi = b.seqs - 1;
-            while (lo < hi) {
-                const int mid = lo + ((hi - lo + 1) >> 1);
-                if (seq_start(b, mid) / w.segment + mid <= item)
-                    lo = mid;
-                else
-                    hi = mid - 1;
+            // a wave probes 64 places at once: a step for each 64-fold of sequences, not
+            // for each doubling (a load's latency each).  lo is a place that does not lie
+            // behind the item; the probes that do not are the first ones.
+            int lo = 0, count = b.seqs;
+            while (count > 1) {
+                const int step = (count + 63) >> 6, at = (int)(threadIdx.x & 63) * step;
+                const bool before = at < count &&
+                                    seq_start(b, lo + at) / w.segment + lo + at <= item;
+                const unsigned long long votes = ~__ballot(before);
+                const int last = votes ? max((int)__builtin_ctzll(votes) - 1, 0) : 63;
+                lo += last * step;
+                count = min(step, count - last * step);
             }
-            seq = lo;
+            seq = __builtin_amdgcn_readfirstlane(lo);
             seg = item - (seq_start(b, seq) / w.segment + seq);
         }
         row0 = seq_start(b, seq);
@@ -189,6 +194,11 @@ __device__ __forceinline__ long long state_at(const Walk &w, bool flip, int dk, 
 
 constexpr int kChunkBytes = 128;
 
+// Kernels of their own, so that none pays registers for what it does not do: widths of
+// whole chunks of 16 bytes with results of T, or (the parts of shared heads) of
+// float32; and other widths.
+enum Mode { ROWS, PARTS, ODD };
+
 constexpr int kFar = 0x7ffffff0;        // beyond every descriptor's bounds
 
 // A tile of C rows of D elements in LDS, 16 bytes between the rows: the reads below,
@@ -201,22 +211,21 @@ template <typename T, int C, int D, int kThr> struct Tile {
     static constexpr int apart = kThr / per_row;        // rows between them
     static_assert(count >= 1 && C * per_row % kThr == 0);
 
-    // The chunk's rows, `left` of them, columns up to `wide`, from the row of lowest
-    // address on (which may lie before the array where `left` is less than C).
-    // ODD: some width is no whole number of chunks (kernels of their own, as what
-    // they need for it would cost the others their registers).
-    template <bool ODD>
+    // The chunk's rows from `from` on, columns up to `wide`; `lowest` is the row of lowest
+    // address (which may lie before the array where `from` is not 0).
+    // CUT: some width is no whole number of chunks.
+    template <bool CUT>
     static __device__ __forceinline__ void fetch(u32x4 (&regs)[count], const T *lowest, int ld,
-                                                 bool back, int left, int wide, int thread)
+                                                 bool back, int from, int wide, int thread)
     {
         const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(lowest, kFar - 16);
         const int row = thread / per_row, col = thread % per_row * elems;
         const int first = (back ? C - 1 - row : row) * (ld * size) + col * size;
         const int step = (back ? -apart : apart) * (ld * size);
-        if constexpr (!ODD) {
+        if constexpr (!CUT) {
 #pragma unroll
             for (int k = 0; k < count; ++k) {
-                const bool in = row + k * apart < left && col < wide;
+                const bool in = row + k * apart >= from && col < wide;
                 regs[k] = __builtin_bit_cast(
                     u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                rsrc, in ? first + k * step : kFar, 0, 0));
@@ -227,7 +236,7 @@ template <typename T, int C, int D, int kThr> struct Tile {
                 unsigned v[elems];
 #pragma unroll
                 for (int e = 0; e < elems; ++e) {
-                    const bool in = row + k * apart < left && col + e < wide;
+                    const bool in = row + k * apart >= from && col + e < wide;
                     const int at = in ? first + k * step + e * size : kFar;
                     if constexpr (size == 2)
                         v[e] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
@@ -242,32 +251,48 @@ template <typename T, int C, int D, int kThr> struct Tile {
             }
         }
     }
+    // PAIRED: of each 32 16-bit columns, numbers 4g .. + 3 of both halves side by side,
+    // which is the order that a matrix instruction leaves its results in.
+    template <bool PAIRED = false>
     static __device__ __forceinline__ void keep(lds_ptr lds, const u32x4 (&regs)[count],
                                                 int thread)
     {
         const int row = thread / per_row, c = thread % per_row;
 #pragma unroll
-        for (int k = 0; k < count; ++k)
-            *(lds_u4)(lds + (row + k * apart) * pitch + c * 16) = regs[k];
+        for (int k = 0; k < count; ++k) {
+            const lds_ptr at = lds + (row + k * apart) * pitch;
+            if constexpr (PAIRED && size == 2) {
+                const lds_ptr to = at + paired(c);
+                *(lds_u2)to = u32x2{regs[k][0], regs[k][1]};
+                *(lds_u2)(to + 16) = u32x2{regs[k][2], regs[k][3]};
+            } else {
+                *(lds_u4)(at + c * 16) = regs[k];
+            }
+        }
+    }
+    // Where the first half of chunk c of a row is kept; the second half is 16 bytes on.
+    static __device__ __forceinline__ int paired(int c)
+    {
+        return (c >> 2) * 64 + (c & 1) * 32 + (c >> 1 & 1) * 8;
     }
 
-    // 16 bytes of row `row`, chunk `c`
-    static __device__ __forceinline__ u32x4 chunk(lds_ptr lds, int row, int c)
+    // An operand that is summed along the row, the columns in their order: row `row`,
+    // part u of it (32 16-bit or 16 float32 columns), the numbers of lane group g.
+    template <bool PAIRED = false>
+    static __device__ __forceinline__ u32x4 chunk(lds_ptr lds, int row, int u, int g)
     {
-        return *(lds_u4)(lds + row * pitch + c * 16);
+        if constexpr (PAIRED && size == 2) {
+            const lds_ptr at = lds + row * pitch + u * 64 + (g & 1) * 32 + (g >> 1) * 8;
+            const u32x2 lo = *(lds_u2)at, hi = *(lds_u2)(at + 16);
+            return u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {
+            return *(lds_u4)(lds + row * pitch + u * 64 + g * 16);
+        }
     }
-    // An operand that is summed along the row: row `row`, part u of it (32 16-bit
-    // or 16 float32 columns), the numbers of lane group g.  In the order that a
-    // matrix instruction leaves its results in: 4 of each 16.
+    // The same of a PAIRED tile in the order that it is kept in.
     static __device__ __forceinline__ u32x4 along(lds_ptr lds, int row, int u, int g)
     {
-        if constexpr (size == 4) {
-            return chunk(lds, row, u * 4 + g);
-        } else {
-            const lds_ptr at = lds + row * pitch + g * 8 + u * 64;
-            const u32x2 lo = *(lds_u2)at, hi = *(lds_u2)(at + 32);
-            return u32x4{lo.x, lo.y, hi.x, hi.y};
-        }
+        return *(lds_u4)(lds + row * pitch + u * 64 + g * 16);
     }
     // An operand that is summed across the rows: column col + (lane & 15), part
     // ks of the rows (32 or 16), the numbers of lane group g, in the order of row_of().
@@ -328,10 +353,16 @@ __device__ __forceinline__ float wave_max(float m)
     return m;
 }
 
-// The power of two that brings a largest value of m to [1, 2), or 1 while it lies
-// between lo and hi (float16: where its numbers are normal and far from their end).
-__device__ __forceinline__ float range_scale(float m, float lo, float hi)
+// The power of two that brings the largest finite size of a wave's numbers to [1, 2),
+// or 1 while it lies between lo and hi (float16: where its numbers are normal and far
+// from their end), which takes two votes.  `most`: a lane's largest size; finite():
+// its largest finite one.
+template <typename F>
+__device__ __forceinline__ float range_scale(float most, float lo, float hi, F finite)
 {
+    if (!__any(most > hi) && __any(most >= lo))
+        return 1.0f;
+    const float m = wave_max(finite());
     if (!(m > 0.0f) || (m >= lo && m <= hi))
         return 1.0f;
     const int e = (int)((__builtin_bit_cast(unsigned, m) >> 23) & 255) - 127;
@@ -343,9 +374,9 @@ __device__ __forceinline__ float finite_size(float v)
     return fabsf(v) <= 3.4e38f ? fabsf(v) : 0.0f;
 }
 
-template <typename T, int DK, int DVT> struct Body {
+template <typename T, int DK, int DVT, int MT> struct Body {
     static constexpr int size = (int)sizeof(T), elems = 16 / size;
-    static constexpr int waves = DVT / 16, threads = waves * 64;
+    static constexpr int waves = DVT / (16 * MT), threads = waves * 64;
     static constexpr int C = kChunkBytes / size;        // tokens of a chunk
     static constexpr int CT = C / 16;                   // 16-row tiles of it
     static constexpr int span = 4 * elems;              // that a product sums over
@@ -362,15 +393,21 @@ template <typename T, int DK, int DVT> struct Body {
     static constexpr int powers = 2 * C;
     typedef __attribute__((address_space(3))) const float *table;
 
-    f32x4 S[NT];        // rows 16 n + 4 g .. + 3 of column i of the wave's
+    f32x4 S[NT][MT];    // rows 16 n + 4 g .. + 3 of column i of 16 of the wave's
     int thread, lane, wave, g, i;
     table pw;
+    float near_pw[elems];       // a^(elems - 1 - m)
 
-    __device__ __forceinline__ explicit Body(table powers_)
+    __device__ __forceinline__ Body(table powers_, float ld)
         : thread(threadIdx.x), lane(thread & 63),
           wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), g(lane >> 4), i(lane & 15),
           pw(powers_)
     {
+#pragma unroll
+        for (int m = 0; m < elems; ++m)
+            near_pw[m] = __builtin_bit_cast(
+                float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(
+                           int, expf(ld * (float)(elems - 1 - m)))));
     }
     static __device__ __forceinline__ void fill(float *to, float ld)
     {
@@ -388,69 +425,82 @@ template <typename T, int DK, int DVT> struct Body {
         i = lane & 15;
     }
 
-    // Where an element is in a state array that is [Dk][Dv], or flipped: bytes from its
-    // start, or far away.
-    __device__ __forceinline__ int place(const Walk &w, bool flip, int dv0, int n, int r) const
+    // first of the wave's columns within the tile
+    __device__ __forceinline__ int col0() const { return wave * 16 * MT; }
+
+    // f(n, m, r, bytes) for the elements of a state array that is [Dk][Dv], or flipped:
+    // bytes from its start, or (elements that it does not have) far away.
+    template <typename F>
+    __device__ __forceinline__ void places(const Walk &w, bool flip, int dv0, F f) const
     {
-        const int dk = n * 16 + g * 4 + r, dv = dv0 + wave * 16 + i;
-        return dk < w.Dk && dv < w.Dv ? (flip ? dv * w.Dk + dk : dk * w.Dv + dv) * 4 : kFar;
+        const int dk_step = (flip ? 1 : w.Dv) * 4, dv_step = (flip ? w.Dk : 1) * 4;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int dv = dv0 + col0() + m * 16 + i;
+            const int at = dv < w.Dv ? g * 4 * dk_step + dv * dv_step : kFar - DK * 1024;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int to = at + (n * 16 + r) * dk_step;
+                    f(n, m, r, w.Dk == DK || n * 16 + g * 4 + r < w.Dk ? to : kFar);
+                }
+        }
     }
     // The state from memory (nullptr: zero) and to it.
     __device__ __forceinline__ void load_state(const Walk &w, const float *from, bool flip,
                                                int dv0)
     {
         // an empty descriptor reads as zero
-        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(from, from ? kFar - 16 : 0);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            unsigned v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                v[r] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, place(w, flip, dv0, n, r), 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                S[n][r] = __builtin_bit_cast(float, v[r]);
-        }
+        const __amdgpu_buffer_rsrc_t rsrc =
+            dwconv::make_rsrc(from, from ? w.Dk * w.Dv * 4 : 0);
+        places(w, flip, dv0, [&](int n, int m, int r, int at) {
+            const unsigned v = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+            S[n][m][r] = __builtin_bit_cast(float, v);
+        });
     }
     __device__ __forceinline__ void store_state(const Walk &w, float *to, bool flip,
                                                 int dv0) const
     {
-        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(to, kFar - 16);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float v = S[n][r];
-                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rsrc,
-                                                      place(w, flip, dv0, n, r), 0, 0);
-            }
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(to, w.Dk * w.Dv * 4);
+        places(w, flip, dv0, [&](int n, int m, int r, int at) {
+            const float v = S[n][m][r];
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rsrc, at, 0,
+                                                  0);
+        });
     }
 
     // The wave's columns of V, as operands that are summed across the rows.
-    __device__ __forceinline__ void columns(lds_ptr v, u32x4 (&f)[KS]) const
+    __device__ __forceinline__ void columns(lds_ptr v, u32x4 (&f)[KS][MT]) const
     {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-            f[ks] = VV::across(v, wave * 16, ks, lane);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                f[ks][m] = VV::across(v, col0() + m * 16, ks, lane);
     }
 
     // Whether they hold an infinity or a NaN, which are taken out.  (No matrix
     // instruction is at work here: see settle.)
-    __device__ __forceinline__ bool strange(u32x4 (&f)[KS]) const
+    __device__ __forceinline__ bool strange(u32x4 (&f)[KS][MT]) const
     {
         unsigned odd = 0;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                odd |= odd_bits<T>(f[ks][e]);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    odd |= odd_bits<T>(f[ks][m][e]);
         const bool any = __any(odd != 0);
         if (any)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    f[ks][e] = cleaned<T>(f[ks][e]);
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[ks][m][e] = cleaned<T>(f[ks][m][e]);
         return any;
     }
 
@@ -497,57 +547,75 @@ template <typename T, int DK, int DVT> struct Body {
     // infinities and NaN where there are `any`, which are added one by one: split in
     // parts they would leave NaN, and so would the zeros beside k's columns.
     __device__ __forceinline__ void update(const Walk &w, lds_ptr k, lds_ptr v,
-                                           const u32x4 (&vf)[KS], bool any, int n, float a_n)
+                                           const u32x4 (&vf)[KS][MT], bool any, float a_n)
     {
         float up = 1.0f;
         if constexpr (is_f16) {     // small values would lose their last bits
-            float most = 0.0f;
+            const auto largest = [&] {      // of columns without infinities
+                float most = 0.0f;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int e = 0; e < elems; ++e)
-                    most = fmaxf(most, finite_size(element<T>(vf[ks], e)));
-            up = range_scale(wave_max(most) * fabsf(w.s2), 0x1p-3f, 0x1p14f);
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < elems; ++e)
+                            most = fmaxf(most, fabsf(element<T>(vf[ks][m], e)));
+                return most * fabsf(w.s2);
+            };
+            up = range_scale(largest(), 0x1p-3f, 0x1p14f, largest);
         }
         const float keep = a_n * up, s2 = w.s2 * up;
-        // a^(n - 1 - j + late) for row j
-        const table late_pw = pw + (C - n + 1 - w.late) + VV::row_of(0, g, 0);
+        const table late_pw = pw + (1 - w.late);        // a^(C - 1 - j + late) for row j
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            S[t] *= keep;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                S[t][m] *= keep;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            float x[elems];
-            u32x4 p[parts];
+            // the lane's rows lie within `elems` adjacent ones: the last one's power,
+            // times those of what the others are before it, which all lanes share
+            const float last = late_pw[ks * span + g * elems + elems - 1] * s2;
+            u32x4 p[MT][parts];
 #pragma unroll
-            for (int e = 0; e < elems; ++e)
-                x[e] = element<T>(vf[ks], e) * (late_pw[VV::row_of(ks, 0, e)] * s2);
-            split(x, p);
+            for (int m = 0; m < MT; ++m) {
+                float x[elems];
+#pragma unroll
+                for (int e = 0; e < elems; ++e)
+                    x[e] = element<T>(vf[ks][m], e) * (last * near_pw[VV::row_of(0, 0, e)]);
+                split(x, p[m]);
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const u32x4 kf = QK::across(k, t * 16, ks, lane);
 #pragma unroll
-                for (int q = 0; q < parts; ++q)
-                    mma<T>(kf, p[q], S[t]);
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int q = 0; q < parts; ++q)
+                        mma<T>(kf, p[m][q], S[t][m]);
             }
         }
         settle();
         if constexpr (is_f16)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-                S[t] *= 1.0f / up;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    S[t][m] *= 1.0f / up;
         if (any)
-            for (int j = 0; j < n; ++j) {
-                const float x = VV::one(v, j, wave * 16 + i);
-                const float f = pw[C - n + 1 - w.late + j] * w.s2;
-                if (!(fabsf(x) <= 3.4e38f))
+            for (int j = 0; j < C; ++j)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                for (int m = 0; m < MT; ++m) {
+                    const float x = VV::one(v, j, col0() + m * 16 + i);
+                    const float f = late_pw[j] * w.s2;
+                    if (!(fabsf(x) <= 3.4e38f))
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (t * 16 + g * 4 + r < w.Dk)
-                                S[t][r] += f * QK::one(k, j, t * 16 + g * 4 + r) * x;
-            }
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (t * 16 + g * 4 + r < w.Dk)
+                                    S[t][m][r] += f * QK::one(k, j, t * 16 + g * 4 + r) * x;
+                }
     }
 
     // Some tiles of a row of scores, times their decay, to LDS; the power of two that
@@ -563,10 +631,10 @@ template <typename T, int DK, int DVT> struct Body {
             acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int u = 0; u < US; ++u) {
-            const u32x4 qf = QK::chunk(q, row, u * 4 + g);
+            const u32x4 qf = QK::template chunk<true>(q, row, u, g);
 #pragma unroll
             for (int t = 0; t < JT; ++t)    // later tokens' too: no branch (see settle)
-                mma<T>(QK::chunk(k, col0 + t * 16 + i, u * 4 + g), qf, acc[t]);
+                mma<T>(QK::chunk(k, col0 + t * 16 + i, u, g), qf, acc[t]);
         }
         const int ahead = row - col0 - g * 4;       // of the first of the lane's columns
         const table gap_pw = pw + (C - ahead);
@@ -578,10 +646,18 @@ template <typename T, int DK, int DVT> struct Body {
                 // a score of a later token may be anything
                 v[t][r] = ahead >= t * 16 + r ? acc[t][r] * (s0 * gap_pw[t * 16 + r]) : 0.0f;
                 if constexpr (is_f16)
-                    most = fmaxf(most, finite_size(v[t][r]));
+                    most = fmaxf(most, fabsf(v[t][r]));
             }
         if constexpr (is_f16)
-            down = range_scale(wave_max(most), 0x1p-2f, 0x1p14f);
+            down = range_scale(most, 0x1p-2f, 0x1p14f, [&] {
+                float m = 0.0f;
+#pragma unroll
+                for (int t = 0; t < JT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        m = fmaxf(m, finite_size(v[t][r]));
+                return m;
+            });
 #pragma unroll
         for (int t = 0; t < JT; ++t) {
             if constexpr (is_f16)
@@ -608,115 +684,199 @@ template <typename T, int DK, int DVT> struct Body {
         return down;
     }
 
-    // o[t]: columns 4 g .. + 3 of the wave's, row i of the 16 of tile t:
-    // s1 a^(i+1-late) q S
-    __device__ __forceinline__ void from_state(lds_ptr q, f32x4 (&o)[CT], float s1, int late)
+    // o[t][m]: columns 4 g .. + 3 of 16 of the wave's, row i of the 16 of tile t:
+    // s1 a^(row - first + 1 - late) q S, `first` the chunk's first row
+    __device__ __forceinline__ void from_state(lds_ptr q, f32x4 (&o)[CT][MT], float s1, int late,
+                                               int first)
     {
 #pragma unroll
         for (int t = 0; t < CT; ++t)
-            o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                o[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         float down = 1.0f;
         if constexpr (is_f16) {
-            float most = 0.0f;
+            const auto largest = [&](auto size_of) {
+                float most = 0.0f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    most = fmaxf(most, finite_size(S[n][r]));
-            down = range_scale(wave_max(most), 0x1p-2f, 0x1p14f);
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            most = fmaxf(most, size_of(S[n][m][r]));
+                return most;
+            };
+            down = range_scale(largest([](float v) { return fabsf(v); }), 0x1p-2f, 0x1p14f,
+                               [&] { return largest(finite_size); });
         }
 #pragma unroll
         for (int u = 0; u < US; ++u) {
-            float f[elems];
+            u32x4 sf[MT];
 #pragma unroll
-            for (int e = 0; e < elems; ++e)
-                f[e] = S[u * (elems / 4) + e / 4][e % 4] * (is_f16 ? down : 1.0f);
-            unsigned word[4];
-            narrow<T, elems>(f, word);
-            const u32x4 sf = {word[0], word[1], word[2], word[3]};
+            for (int m = 0; m < MT; ++m) {
+                float f[elems];
 #pragma unroll
-            for (int t = 0; t < CT; ++t)
-                mma<T>(sf, QK::along(q, t * 16 + i, u, g), o[t]);
+                for (int e = 0; e < elems; ++e)
+                    f[e] = S[u * (elems / 4) + e / 4][m][e % 4] * (is_f16 ? down : 1.0f);
+                unsigned word[4];
+                narrow<T, elems>(f, word);
+                sf[m] = u32x4{word[0], word[1], word[2], word[3]};
+            }
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                const u32x4 qf = QK::along(q, t * 16 + i, u, g);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    mma<T>(sf[m], qf, o[t][m]);
+            }
         }
-        const table row_pw = pw + (C - 1 + late - (CT - 1) * 16 - i);
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-            o[t] *= s1 * row_pw[(CT - 1 - t) * 16] / down;
+        for (int t = 0; t < CT; ++t) {
+            const int n = max(t * 16 + i + 1 - late - first, 0);
+            const float f = s1 * pw[C - n] / down;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                o[t][m] *= f;
+        }
     }
 
     // o += P V.  Infinities and NaN of V are added one by one: a zero score of a later
     // token times those would be NaN.
     __device__ __forceinline__ void from_scores(lds_ptr p, lds_ptr v, const float *downs,
-                                                const u32x4 (&f)[KS], bool any, f32x4 (&o)[CT])
+                                                const u32x4 (&f)[KS][MT], bool any,
+                                                f32x4 (&o)[CT][MT])
     {
         // what the scores of row tile t, part ks, were divided by
         auto down_of = [&](int t, int ks) {
             return is_f16 ? downs[t + ks * (span / 16) / JT * CT] : 1.0f;
         };
+        auto product = [&](auto scaled) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int t = 0; t < CT; ++t)
-                if (ks * span <= t * 16 + 15) {
-                    const u32x4 pf = *(lds_u4)(p + (t * 16 + i) * pitch + (ks * 4 + g) * 16);
-                    if constexpr (is_f16) {
-                        const float d = down_of(t, ks);
-                        o[t] *= d;
-                        mma<T>(f[ks], pf, o[t]);
-                        o[t] *= 1.0f / d;
-                    } else {
-                        mma<T>(f[ks], pf, o[t]);
+                for (int t = 0; t < CT; ++t)
+                    if (ks * span <= t * 16 + 15) {
+                        const u32x4 pf = *(lds_u4)(p + (t * 16 + i) * pitch + (ks * 4 + g) * 16);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            if constexpr (scaled.value)
+                                o[t][m] *= down_of(t, ks);
+                            mma<T>(f[ks][m], pf, o[t][m]);
+                            if constexpr (scaled.value)
+                                o[t][m] *= 1.0f / down_of(t, ks);
+                        }
                     }
-                }
+        };
+        if constexpr (is_f16) {
+            const float mine = downs[lane % waves];
+            if (__any(mine != 1.0f))
+                product(std::true_type());
+            else
+                product(std::false_type());
+        } else {
+            product(std::false_type());
+        }
         settle();
         if (any)
             for (int j = 0; j < C; ++j) {
                 // where column j of the scores is kept
                 const int slot = size == 4 ? j : (j & ~7) | (j & 1) << 2 | (j >> 1 & 3);
-                float x[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    x[r] = VV::one(v, j, wave * 16 + g * 4 + r);
 #pragma unroll
                 for (int t = 0; t < CT; ++t) {
                     const float s =
                         (float)*(__attribute__((address_space(3))) const T *)(
                             p + (t * 16 + i) * pitch + slot * size) / down_of(t, j / span);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (j <= t * 16 + i && !(fabsf(x[r]) <= 3.4e38f))
-                            o[t][r] += s * x[r];
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float x = VV::one(v, j, col0() + m * 16 + g * 4 + r);
+                            if (j <= t * 16 + i && !(fabsf(x) <= 3.4e38f))
+                                o[t][m][r] += s * x;
+                        }
                 }
             }
     }
 
-    // The rows `here` of the chunk from token t on, 4 adjacent columns a lane.
-    template <bool ODD, typename E>
-    __device__ __forceinline__ void store(E *out, const Walk &w, const f32x4 (&o)[CT],
-                                          long long row0, int t, int here, int h, int dv0) const
+    // Results of T go through the tile of V, whose columns a wave has read and writes
+    // alone, so that whole rows are stored, 16 bytes a lane.
+    static constexpr int words = 4 * size / 4;
+    __device__ __forceinline__ void pack(const f32x4 (&o)[CT][MT],
+                                         unsigned (&to)[CT][MT][words]) const
+    {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const f32x4 v = o[c][m];
+                const float s[4] = {v[0], v[1], v[2], v[3]};
+                narrow<T, 4>(s, to[c][m]);
+            }
+    }
+    __device__ __forceinline__ void spread(lds_ptr v, const unsigned (&w)[CT][MT][words]) const
+    {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const lds_ptr at = v + (c * 16 + i) * VV::pitch + (col0() + m * 16 + g * 4) * size;
+                if constexpr (size == 4)
+                    *(lds_u4)at = u32x4{w[c][m][0], w[c][m][1], w[c][m][2], w[c][m][3]};
+                else
+                    *(lds_u2)at = u32x2{w[c][m][0], w[c][m][1]};
+            }
+    }
+    // (A thread reads what it will write of the next V itself.)
+    __device__ __forceinline__ void store_rows(lds_ptr v, const Walk &w, long long row0, int t,
+                                               int first, int h, int dv0) const
+    {
+        const int wide = w.Dv - dv0, ldo = (int)w.ldo * size;
+        const long long lowest = w.back ? row0 - t - (C - 1) : row0 + t;
+        const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(
+            static_cast<T *>(w.out) + lowest * w.ldo + h * w.Dv + dv0, kFar - 16);
+        const int row = thread / VV::per_row, col = thread % VV::per_row * elems;
+        typedef unsigned u4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int k = 0; k < VV::count; ++k) {
+            const int r = row + k * VV::apart;
+            const u4 x = *(__attribute__((address_space(3))) u4 *)(v + r * VV::pitch + col * size);
+            const int at = (w.back ? C - 1 - r : r) * ldo + col * size;
+            __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, r >= first && col < wide ? at : kFar,
+                                                   0, 0);
+        }
+    }
+
+    // The chunk's rows from `first` on, 4 adjacent columns a lane; its row 0 is token t.
+    template <bool CUT, typename E>
+    __device__ __forceinline__ void store(E *out, const Walk &w, const f32x4 (&o)[CT][MT],
+                                          long long row0, int t, int first, int h,
+                                          int dv0) const
     {
         const int wide = w.Dv - dv0, ldo = (int)w.ldo * (int)sizeof(E);
         const long long lowest = w.back ? row0 - t - (C - 1) : row0 + t;
         const __amdgpu_buffer_rsrc_t rsrc =
             dwconv::make_rsrc(out + lowest * w.ldo + h * w.Dv + dv0, kFar - 16);
-        const int dv = wave * 16 + g * 4;
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            const int r = c * 16 + i;
-            const int at = (w.back ? C - 1 - r : r) * ldo + dv * (int)sizeof(E);
-            const f32x4 v = o[c];
-            const float s[4] = {v[0], v[1], v[2], v[3]};
-            if constexpr (!ODD) {
-                Raw<E, 4>(s).store(rsrc, r < here && dv < wide ? at : kFar, 0);
-            } else {
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float one[1] = {s[e]};
-                    Raw<E, 1>(one).store(
-                        rsrc, r < here && dv + e < wide ? at + e * (int)sizeof(E) : kFar, 0);
+            for (int m = 0; m < MT; ++m) {
+                const int r = c * 16 + i, dv = col0() + m * 16 + g * 4;
+                const int at = (w.back ? C - 1 - r : r) * ldo + dv * (int)sizeof(E);
+                const f32x4 v = o[c][m];
+                const float s[4] = {v[0], v[1], v[2], v[3]};
+                if constexpr (!CUT) {
+                    Raw<E, 4>(s).store(rsrc, r >= first && dv < wide ? at : kFar, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float one[1] = {s[e]};
+                        Raw<E, 1>(one).store(
+                            rsrc, r >= first && dv + e < wide ? at + e * (int)sizeof(E) : kFar,
+                            0);
+                    }
                 }
             }
-        }
     }
 };
 
@@ -737,6 +897,20 @@ template <typename T, int C> struct Rows {
     }
 };
 
+// A chunk of a segment of n tokens: its row 0 is token t, and rows before `first` are
+// zero.  The last chunk ends with the segment, so that a row is as far from the end
+// of its chunk in all of them.
+struct Chunk {
+    int done, n, C, t, first;
+    __device__ __forceinline__ Chunk(int n_, int C_, int done_ = 0) : done(done_), n(n_), C(C_)
+    {
+        first = C - max(min(C, n - done), 0);
+        t = done - first;
+    }
+    __device__ __forceinline__ bool any() const { return done < n; }
+    __device__ __forceinline__ Chunk next() const { return Chunk(n, C, done + C); }
+};
+
 // What a workgroup walks.
 struct Part {
     int item, h, dv0;
@@ -751,13 +925,16 @@ struct Part {
 };
 
 // Two workgroups a CU, with registers for them.
-constexpr int waves_a_simd(int DK, int DVT) { return DK > 128 ? 1 : DVT / 16 * 2 / 4; }
+constexpr int waves_a_simd(int DK, int DVT, int MT)
+{
+    return DK > 128 || DVT < 32 * MT ? 1 : DVT / (16 * MT) * 2 / 4;
+}
 
 // The state that a segment adds by itself, to the slot of the next one.
-template <typename T, int DK, int DVT, bool ODD>
-__global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_states(Walk w)
+template <typename T, int DK, int DVT, int MT, Mode MODE>
+__global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_states(Walk w)
 {
-    using B = Body<T, DK, DVT>;
+    using B = Body<T, DK, DVT, MT>;
     __shared__ alignas(16) char lds[B::QK::bytes + B::VV::bytes];
     __shared__ float powers[B::powers];
     const lds_ptr lk = (lds_ptr)lds, lv = lk + B::QK::bytes;
@@ -769,34 +946,48 @@ __global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_states(Walk 
         return;
     const float ld = log_decay_of(w.log_decay, part.h);
     B::fill(powers, ld);
-    B b((typename B::table)powers);
+    B b((typename B::table)powers, ld);
 #pragma unroll
     for (int n = 0; n < B::NT; ++n)
-        b.S[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            b.S[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int t0 = at.seg * w.segment, n = w.segment;       // a whole one
     const long long row = w.back ? (long long)at.row0 + at.length - 1 - t0 : at.row0 + t0;
     const Rows<T, B::C> k(w.k, w.ldk, w.back, row, part.h / w.gk * w.Dk),
         v(w.v, w.ldv, w.back, row, part.h / w.gv * w.Dv + part.dv0);
     const int wide = w.Dv - part.dv0, ldk = (int)w.ldk, ldv = (int)w.ldv;
     const float whole = (float)exp((double)ld * B::C);
-    u32x4 rk[B::QK::count], rv[B::VV::count];
-    B::QK::template fetch<ODD>(rk, k.at(0), ldk, w.back, n, w.Dk, b.thread);
-    B::VV::template fetch<ODD>(rv, v.at(0), ldv, w.back, n, wide, b.thread);
-    for (int t = 0; t < n; t += B::C) {
-        const int here = min(B::C, n - t);
+    // two chunks on their way: there are fewer workgroups than the chip holds, and
+    // little to do but to wait for memory
+    Chunk c(n, B::C);
+    u32x4 rk[2][B::QK::count], rv[2][B::VV::count];
+    auto fetch = [&](auto p, const Chunk &x) {
+        B::QK::template fetch<MODE == ODD>(rk[p.value], k.at(x.t), ldk, w.back, x.first, w.Dk, b.thread);
+        B::VV::template fetch<MODE == ODD>(rv[p.value], v.at(x.t), ldv, w.back, x.first, wide, b.thread);
+    };
+    auto step = [&](auto p) {
         b.next_chunk();
-        B::QK::keep(lk, rk, b.thread);
-        B::VV::keep(lv, rv, b.thread);
+        B::QK::keep(lk, rk[p.value], b.thread);
+        B::VV::keep(lv, rv[p.value], b.thread);
         __syncthreads();
-        B::QK::template fetch<ODD>(rk, k.at(t + B::C), ldk, w.back, n - t - B::C, w.Dk,
-                                   b.thread);
-        B::VV::template fetch<ODD>(rv, v.at(t + B::C), ldv, w.back, n - t - B::C, wide,
-                                   b.thread);
-        u32x4 vf[B::KS];
+        fetch(p, c.next().next());
+        u32x4 vf[B::KS][MT];
         b.columns(lv, vf);
         const bool any = b.strange(vf);
-        b.update(w, lk, lv, vf, any, here, here == B::C ? whole : expf(ld * (float)here));
+        b.update(w, lk, lv, vf, any,
+                 c.first == 0 ? whole : expf(ld * (float)(B::C - c.first)));
         __syncthreads();
+        c = c.next();
+    };
+    constexpr std::integral_constant<int, 0> even;
+    constexpr std::integral_constant<int, 1> odd;
+    fetch(even, c);
+    fetch(odd, c.next());
+    while (c.any()) {
+        step(even);
+        if (c.any())
+            step(odd);
     }
     b.next_chunk();
     b.store_state(w, w.slots + ((long long)(part.item + 1) * w.H + part.h) * w.Dk * w.Dv, false,
@@ -804,49 +995,54 @@ __global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_states(Walk 
 }
 
 // The segments' own states, each to be added to what it gets from those before it.  A
-// thread takes an element; the segments of a sequence one after the other.
+// thread takes 4 adjacent elements (or one, where a state is no whole number of 4); the
+// segments of a sequence one after the other.
+template <int V>
 __global__ __launch_bounds__(256) void k_link(Walk w, int blocks)
 {
-    const long long id = block_id();
-    const int at = (int)(id % blocks) * 256 + (int)threadIdx.x;
-    const int h = (int)(id / blocks % w.H);
-    const long long seq = id / blocks / w.H;
-    if (seq >= w.batch.seqs || at >= w.Dk * w.Dv)
+    const unsigned id = block_id();
+    const int at = ((int)(id % blocks) * 256 + (int)threadIdx.x) * V;
+    const int h = (int)(id / blocks % w.H), seq = (int)(id / blocks / w.H), size = w.Dk * w.Dv;
+    if (seq >= w.batch.seqs || at >= size)
         return;
     // (from the sequence itself: offsets that break the rules might lead an item's
     // search to another one, with more slots than there are from here on)
-    const int row0 = seq_start(w.batch, (int)seq), end = seq_start(w.batch, (int)seq + 1);
-    const int first = w.batch.off ? row0 / w.segment + (int)seq : (int)seq * w.per_seq;
+    const int row0 = seq_start(w.batch, seq), end = seq_start(w.batch, seq + 1);
+    const int first = w.batch.off ? row0 / w.segment + seq : seq * w.per_seq;
     const int count = Item::count(w, max(end - row0, 0));
     if (count == 1)
         return;
     const float ld = log_decay_of(w.log_decay, h);
     const float a = (float)exp((double)ld * w.segment);
-    const long long size = (long long)w.Dk * w.Dv;
-    float run = 0.0f;
+    float run[V] = {};
     if (w.state0)
-        run = w.state0[(seq * w.H + h) * size + state_at(w, w.flip, at / w.Dv, at % w.Dv)];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            run[e] = w.state0[((long long)seq * w.H + h) * size +
+                              state_at(w, w.flip, (at + e) / w.Dv, (at + e) % w.Dv)];
     float *slot = w.slots + ((long long)first * w.H + h) * size + at;
-    const long long next = w.H * size;
-    constexpr int kAhead = 8;
+    const long long next = (long long)w.H * size;
+    constexpr int kAhead = 4;
     for (int j = 1; j < count; j += kAhead) {
-        float v[kAhead];
+        float v[kAhead][V];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            v[u] = j + u < count ? slot[(j + u) * next] : 0.0f;
+            load<float, V>(slot + min(j + u, count - 1) * next, v[u]);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
             if (j + u < count) {
-                run = a * run + v[u];
-                slot[(j + u) * next] = run;
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    run[e] = a * run[e] + v[u][e];
+                store<float, V>(slot + (j + u) * next, run);
             }
     }
 }
 
-template <typename T, int DK, int DVT, bool ODD>
-__global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_walk(Walk w)
+template <typename T, int DK, int DVT, int MT, Mode MODE>
+__global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_walk(Walk w)
 {
-    using B = Body<T, DK, DVT>;
+    using B = Body<T, DK, DVT, MT>;
     __shared__ alignas(16) char lds[2 * B::QK::bytes + B::VV::bytes + B::C * B::pitch];
     __shared__ float downs[B::waves], powers[B::powers];
     const lds_ptr lq = (lds_ptr)lds, lk = lq + B::QK::bytes, lv = lk + B::QK::bytes,
@@ -860,7 +1056,7 @@ __global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_walk(Walk w)
         return;
     const float ld = log_decay_of(w.log_decay, part.h);
     B::fill(powers, ld);
-    B b((typename B::table)powers);
+    B b((typename B::table)powers, ld);
     const long long size = (long long)w.Dk * w.Dv;
     const long long own = ((long long)at.seq * w.H + part.h) * size;
     const float *from = at.seg ? w.slots + ((long long)part.item * w.H + part.h) * size
@@ -873,44 +1069,53 @@ __global__ __launch_bounds__(DVT * 4, waves_a_simd(DK, DVT)) void k_walk(Walk w)
         v(w.v, w.ldv, w.back, row, part.h / w.gv * w.Dv + part.dv0);
     const int wide = w.Dv - part.dv0, ldq = (int)w.ldq, ldk = (int)w.ldk, ldv = (int)w.ldv;
     const float whole = (float)exp((double)ld * B::C);
+    Chunk c(n, B::C);
     u32x4 rq[B::QK::count], rk[B::QK::count], rv[B::VV::count];
-    B::QK::template fetch<ODD>(rq, q.at(0), ldq, w.back, n, w.Dk, b.thread);
-    B::QK::template fetch<ODD>(rk, k.at(0), ldk, w.back, n, w.Dk, b.thread);
-    B::VV::template fetch<ODD>(rv, v.at(0), ldv, w.back, n, wide, b.thread);
-    for (int t = 0; t < n; t += B::C) {
-        const int here = min(B::C, n - t);
+    B::QK::template fetch<MODE == ODD>(rq, q.at(c.t), ldq, w.back, c.first, w.Dk, b.thread);
+    B::QK::template fetch<MODE == ODD>(rk, k.at(c.t), ldk, w.back, c.first, w.Dk, b.thread);
+    B::VV::template fetch<MODE == ODD>(rv, v.at(c.t), ldv, w.back, c.first, wide, b.thread);
+    for (; c.any(); c = c.next()) {
+        const Chunk next = c.next();
         b.next_chunk();
-        B::QK::keep(lq, rq, b.thread);
+        B::QK::template keep<true>(lq, rq, b.thread);
         B::QK::keep(lk, rk, b.thread);
         B::VV::keep(lv, rv, b.thread);
         __syncthreads();
-        B::QK::template fetch<ODD>(rq, q.at(t + B::C), ldq, w.back, n - t - B::C, w.Dk,
-                                   b.thread);
-        B::QK::template fetch<ODD>(rk, k.at(t + B::C), ldk, w.back, n - t - B::C, w.Dk,
-                                   b.thread);
-        B::VV::template fetch<ODD>(rv, v.at(t + B::C), ldv, w.back, n - t - B::C, wide,
-                                   b.thread);
+        B::QK::template fetch<MODE == ODD>(rq, q.at(next.t), ldq, w.back, next.first, w.Dk, b.thread);
+        B::QK::template fetch<MODE == ODD>(rk, k.at(next.t), ldk, w.back, next.first, w.Dk, b.thread);
+        B::VV::template fetch<MODE == ODD>(rv, v.at(next.t), ldv, w.back, next.first, wide, b.thread);
         __builtin_amdgcn_sched_barrier(0);
         const float down = b.scores(lq, lk, lp, w.s0);
         if (B::is_f16 && b.lane == 0)
             downs[b.wave] = down;
         __builtin_amdgcn_sched_barrier(0);
-        f32x4 o[B::CT];
-        b.from_state(lq, o, w.s1, w.late);
+        f32x4 o[B::CT][MT];
+        b.from_state(lq, o, w.s1, w.late, c.first);
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
-        u32x4 vf[B::KS];
+        u32x4 vf[B::KS][MT];
         b.columns(lv, vf);
         const bool any = b.strange(vf);
         b.from_scores(lp, lv, downs, vf, any, o);
-        if (w.out32)
-            b.template store<ODD>(static_cast<float *>(w.out), w, o, row, t, here, part.h,
-                                  part.dv0);
-        else if (w.out)
-            b.template store<ODD>(static_cast<T *>(w.out), w, o, row, t, here, part.h, part.dv0);
+        unsigned ow[B::CT][MT][B::words];
+        if constexpr (MODE == ROWS) {
+            b.pack(o, ow);
+        } else {
+            if (MODE == PARTS || w.out32)
+                b.template store<MODE == ODD>(static_cast<float *>(w.out), w, o, row, c.t,
+                                              c.first, part.h, part.dv0);
+            else if (w.out)
+                b.template store<MODE == ODD>(static_cast<T *>(w.out), w, o, row, c.t, c.first,
+                                              part.h, part.dv0);
+        }
         __builtin_amdgcn_sched_barrier(0);
-        b.update(w, lk, lv, vf, any, here, here == B::C ? whole : expf(ld * (float)here));
+        b.update(w, lk, lv, vf, any,
+                 c.first == 0 ? whole : expf(ld * (float)(B::C - c.first)));
+        if constexpr (MODE == ROWS)
+            b.spread(lv, ow);
         __syncthreads();
+        if (MODE == ROWS && w.out)
+            b.store_rows(lv, w, row, c.t, c.first, part.h, part.dv0);
     }
     b.next_chunk();
     if (w.state1 && at.seg + 1 == count)
@@ -924,27 +1129,35 @@ template <typename T> int launch_walk(const Walk &w, hipStream_t st)
     const long long blocks = (long long)w.items * w.H * cdiv(w.Dv, walk_tile(w.Dk, w.Dv));
     if (blocks > 0x7fffffffLL)
         return DWCONV_ERR_BAD_DIM;
-    auto run_as = [&](auto dk, auto dvt, auto odd) {
-        constexpr int DK = decltype(dk)::value, DVT = decltype(dvt)::value;
-        constexpr bool ODD = decltype(odd)::value;
+    auto run_as = [&](auto dk, auto dvt, auto mode) {
+        constexpr int DK = decltype(dk)::value, DVT = decltype(dvt)::value, MT = 1;
+        constexpr Mode MODE = decltype(mode)::value;
         int rc = DWCONV_OK;
         if (w.slots) {
-            rc = dwconv::launch_kernel(k_states<T, DK, DVT, ODD>, grid_of(blocks), dim3(DVT * 4), 0, st, w);
-            const int links = (int)cdiv(w.Dk * w.Dv, 256);
-            if ((long long)w.batch.seqs * w.H * links > 0x7fffffffLL)
+            rc = dwconv::launch_kernel(k_states<T, DK, DVT, MT, MODE == ODD ? ODD : ROWS>, grid_of(blocks), dim3(DVT / MT * 4), 0, st, w);
+            const bool by4 = w.Dk * w.Dv % 4 == 0;
+            const int links = (int)cdiv(w.Dk * w.Dv, by4 ? 1024 : 256);
+            const long long all = (long long)w.batch.seqs * w.H * links;
+            if (all > 0x7fffffffLL)
                 return (int)DWCONV_ERR_BAD_DIM;
             if (rc == DWCONV_OK)
-                rc = dwconv::launch_kernel(k_link, grid_of((long long)w.batch.seqs * w.H * links),
-                                           dim3(256), 0, st, w, links);
+                rc = by4 ? dwconv::launch_kernel(k_link<4>, grid_of(all), dim3(256), 0, st, w,
+                                                 links)
+                         : dwconv::launch_kernel(k_link<1>, grid_of(all), dim3(256), 0, st, w,
+                                                 links);
         }
         if (rc == DWCONV_OK)
-            rc = dwconv::launch_kernel(k_walk<T, DK, DVT, ODD>, grid_of(blocks), dim3(DVT * 4), 0, st, w);
+            rc = dwconv::launch_kernel(k_walk<T, DK, DVT, MT, MODE>, grid_of(blocks), dim3(DVT / MT * 4), 0, st, w);
         return rc;
     };
     const int whole = 16 / (int)sizeof(T);
     auto run = [&](auto dk, auto dvt) {
-        return w.Dk % whole || w.Dv % whole ? run_as(dk, dvt, std::true_type())
-                                            : run_as(dk, dvt, std::false_type());
+        if (w.Dk % whole || w.Dv % whole)
+            return run_as(dk, dvt, std::integral_constant<Mode, ODD>());
+        if constexpr (sizeof(T) == 2)
+            if (w.out32)
+                return run_as(dk, dvt, std::integral_constant<Mode, PARTS>());
+        return run_as(dk, dvt, std::integral_constant<Mode, ROWS>());
     };
     using std::integral_constant;
     if (w.Dk > 128)
