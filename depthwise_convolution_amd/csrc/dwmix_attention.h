@@ -197,6 +197,7 @@ constexpr int kChunkBytes = 128;
 // Kernels of their own, so that none pays registers for what it does not do: widths of
 // whole chunks of 16 bytes with results of T, or (the parts of shared heads) of
 // float32; and other widths.
+constexpr int kStatesIn = 0, kWalkIn = 0, kWalkOut = 2;
 enum Mode { ROWS, PARTS, ODD };
 
 constexpr int kFar = 0x7ffffff0;        // beyond every descriptor's bounds
@@ -214,7 +215,7 @@ template <typename T, int C, int D, int kThr> struct Tile {
     // The chunk's rows from `from` on, columns up to `wide`; `lowest` is the row of lowest
     // address (which may lie before the array where `from` is not 0).
     // CUT: some width is no whole number of chunks.
-    template <bool CUT>
+    template <bool CUT, int HINT>
     static __device__ __forceinline__ void fetch(u32x4 (&regs)[count], const T *lowest, int ld,
                                                  bool back, int from, int wide, int thread)
     {
@@ -228,7 +229,7 @@ template <typename T, int C, int D, int kThr> struct Tile {
                 const bool in = row + k * apart >= from && col < wide;
                 regs[k] = __builtin_bit_cast(
                     u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                               rsrc, in ? first + k * step : kFar, 0, 0));
+                               rsrc, in ? first + k * step : kFar, 0, HINT));
             }
         } else {        // rows that end within a chunk: element by element
 #pragma unroll
@@ -239,9 +240,9 @@ template <typename T, int C, int D, int kThr> struct Tile {
                     const bool in = row + k * apart >= from && col + e < wide;
                     const int at = in ? first + k * step + e * size : kFar;
                     if constexpr (size == 2)
-                        v[e] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
+                        v[e] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, HINT);
                     else
-                        v[e] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+                        v[e] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, HINT);
                 }
                 if constexpr (size == 2)
                     regs[k] = u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
@@ -843,7 +844,7 @@ template <typename T, int DK, int DVT, int MT> struct Body {
             const u4 x = *(__attribute__((address_space(3))) u4 *)(v + r * VV::pitch + col * size);
             const int at = (w.back ? C - 1 - r : r) * ldo + col * size;
             __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, r >= first && col < wide ? at : kFar,
-                                                   0, 0);
+                                                   0, kWalkOut);
         }
     }
 
@@ -963,8 +964,8 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_sta
     Chunk c(n, B::C);
     u32x4 rk[2][B::QK::count], rv[2][B::VV::count];
     auto fetch = [&](auto p, const Chunk &x) {
-        B::QK::template fetch<MODE == ODD>(rk[p.value], k.at(x.t), ldk, w.back, x.first, w.Dk, b.thread);
-        B::VV::template fetch<MODE == ODD>(rv[p.value], v.at(x.t), ldv, w.back, x.first, wide, b.thread);
+        B::QK::template fetch<MODE == ODD, kStatesIn>(rk[p.value], k.at(x.t), ldk, w.back, x.first, w.Dk, b.thread);
+        B::VV::template fetch<MODE == ODD, kStatesIn>(rv[p.value], v.at(x.t), ldv, w.back, x.first, wide, b.thread);
     };
     auto step = [&](auto p) {
         b.next_chunk();
@@ -1071,9 +1072,9 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
     const float whole = (float)exp((double)ld * B::C);
     Chunk c(n, B::C);
     u32x4 rq[B::QK::count], rk[B::QK::count], rv[B::VV::count];
-    B::QK::template fetch<MODE == ODD>(rq, q.at(c.t), ldq, w.back, c.first, w.Dk, b.thread);
-    B::QK::template fetch<MODE == ODD>(rk, k.at(c.t), ldk, w.back, c.first, w.Dk, b.thread);
-    B::VV::template fetch<MODE == ODD>(rv, v.at(c.t), ldv, w.back, c.first, wide, b.thread);
+    B::QK::template fetch<MODE == ODD, kWalkIn>(rq, q.at(c.t), ldq, w.back, c.first, w.Dk, b.thread);
+    B::QK::template fetch<MODE == ODD, kWalkIn>(rk, k.at(c.t), ldk, w.back, c.first, w.Dk, b.thread);
+    B::VV::template fetch<MODE == ODD, kWalkIn>(rv, v.at(c.t), ldv, w.back, c.first, wide, b.thread);
     for (; c.any(); c = c.next()) {
         const Chunk next = c.next();
         b.next_chunk();
@@ -1081,9 +1082,9 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
         B::QK::keep(lk, rk, b.thread);
         B::VV::keep(lv, rv, b.thread);
         __syncthreads();
-        B::QK::template fetch<MODE == ODD>(rq, q.at(next.t), ldq, w.back, next.first, w.Dk, b.thread);
-        B::QK::template fetch<MODE == ODD>(rk, k.at(next.t), ldk, w.back, next.first, w.Dk, b.thread);
-        B::VV::template fetch<MODE == ODD>(rv, v.at(next.t), ldv, w.back, next.first, wide, b.thread);
+        B::QK::template fetch<MODE == ODD, kWalkIn>(rq, q.at(next.t), ldq, w.back, next.first, w.Dk, b.thread);
+        B::QK::template fetch<MODE == ODD, kWalkIn>(rk, k.at(next.t), ldk, w.back, next.first, w.Dk, b.thread);
+        B::VV::template fetch<MODE == ODD, kWalkIn>(rv, v.at(next.t), ldv, w.back, next.first, wide, b.thread);
         __builtin_amdgcn_sched_barrier(0);
         const float down = b.scores(lq, lk, lp, w.s0);
         if (B::is_f16 && b.lane == 0)

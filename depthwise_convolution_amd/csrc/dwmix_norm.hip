@@ -30,6 +30,7 @@ using namespace dwseq;
 // L vectors apart.  A workgroup takes `gw` adjacent groups of `slots` rows.
 struct RowsPlan {
     int L, V, K, gw, slots, windows, threads;
+    int R;                      // rows that a team of the forward holds at once
     long long blocks;           // of rows, for the gradient (which walks the rows)
 };
 
@@ -58,6 +59,12 @@ bool rows_plan(int size, long long N, long long P, int C, int groups, RowsPlan *
     p->gw = (int)cdiv(groups, p->windows);
     p->slots = 256 / (L * p->gw);
     p->threads = (int)cdiv(L * p->gw * p->slots, 64) * 64;
+    // Four vectors a lane in flight, which also share w and b, where that leaves two
+    // workgroups for every CU (16384 rows of 2048 bfloat16, 16 groups: FIGURE with 4
+    // rows a team, 36.5 us with 1).
+    p->R = std::max(1, 4 / p->K);
+    if (cdiv(N, (long long)p->slots * p->R) * p->windows < 512)
+        p->R = 1;
     // the gradient's workgroups walk 8 rows at least; 512 rows of partial sums at most
     p->blocks = std::max(1LL, std::min(512LL, cdiv(N, 8LL * p->slots)));
     return true;
@@ -111,61 +118,87 @@ struct RowsAt {
     }
 };
 
-template <typename T, int V, int K>
+template <typename T, int V, int K, int R>
 __global__ __launch_bounds__(256) void k_norm_rows(NormArgs a, RowsPlan p)
 {
     const RowsAt at(p, a.groups);
-    const long long n = (long long)(block_id() / p.windows) * p.slots + at.slot;
-    if (!at.team || n >= a.N)
+    const long long n0 = (long long)(block_id() / p.windows) * p.slots * R + at.slot;
+    if (!at.team || n0 >= a.N)
         return;         // whole teams; a team of 256 is the workgroup
     const int cg = a.C / a.groups, c0 = at.g * cg;
-    const T *x = static_cast<const T *>(a.x) + n * a.ldx + c0;
-    Raw<T, V> r[K];
-    float s[1] = {};
+    // row j; rows behind the last are read as the last one and not stored
+    auto row = [&](int j) { return min(n0 + (long long)j * p.slots, a.N - 1); };
+    Raw<T, V> r[R][K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (at.lane + k * p.L) * V;
-        r[k].clear();
-        if (c < cg) {
-            r[k].load(x + c);
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (at.lane + k * p.L) * V;
+            r[j][k].clear();
+            if (c < cg)
+                r[j][k].load(static_cast<const T *>(a.x) + row(j) * a.ldx + c0 + c);
+        }
+    constexpr bool kEarly = K <= 2;     // w and b wait in registers
+    float w[kEarly ? K : 1][V], b[kEarly ? K : 1][V];
+    auto params = [&](int k, int to) {
+        const int c = min((at.lane + k * p.L) * V, cg - V);
+        get_all<V>(a.w ? a.w + c0 + c : nullptr, w[to], 1.0f);
+        get_all<V>(a.b ? a.b + c0 + c : nullptr, b[to], 0.0f);
+    };
+    if constexpr (kEarly)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            params(k, k);
+    float mean[R] = {}, q[R] = {};
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                s[0] += r[k].get(v);
-        }
+                mean[j] += r[j][k].get(v);
+    team_sum(mean, p.L);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        mean[j] /= (float)cg;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if ((at.lane + k * p.L) * V < cg)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float d = r[j][k].get(v) - mean[j];
+                    q[j] += d * d;
+                }
     }
-    team_sum(s, p.L);
-    const float mean = s[0] / (float)cg;
-    float q[1] = {};
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        if ((at.lane + k * p.L) * V < cg)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float d = r[k].get(v) - mean;
-                q[0] += d * d;
-            }
     team_sum(q, p.L);
-    const float rstd = 1.0f / sqrtf(q[0] / (float)cg + a.eps);
-    T *y = static_cast<T *>(a.y) + n * a.ldy + c0;
+    float rstd[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        rstd[j] = 1.0f / sqrtf(q[j] / (float)cg + a.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (at.lane + k * p.L) * V;
-        if (c < cg) {
-            float w[V], b[V], z[V];
-            get_all<V>(a.w ? a.w + c0 + c : nullptr, w, 1.0f);
-            get_all<V>(a.b ? a.b + c0 + c : nullptr, b, 0.0f);
+        const int c = (at.lane + k * p.L) * V, of = kEarly ? k : 0;
+        if constexpr (!kEarly)
+            params(k, 0);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            float z[V];
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                z[v] = (r[k].get(v) - mean) * rstd * w[v] + b[v];
+                z[v] = (r[j][k].get(v) - mean[j]) * rstd[j] * w[of][v] + b[of][v];
             act_all(z, a.act);
-            store<T, V>(y + c, z);
+            if (c < cg && n0 + (long long)j * p.slots < a.N)
+                store<T, V>(static_cast<T *>(a.y) + row(j) * a.ldy + c0 + c, z);
         }
     }
-    if (a.stats && at.lane == 0) {
-        float *to = a.stats + (n * a.groups + at.g) * 2;
-        to[0] = mean;
-        to[1] = rstd;
-    }
+    if (a.stats && at.lane == 0)
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (n0 + (long long)j * p.slots < a.N) {
+                float *to = a.stats + (row(j) * a.groups + at.g) * 2;
+                to[0] = mean[j];
+                to[1] = rstd[j];
+            }
 }
 
 // dz of V elements and their xhat
@@ -352,8 +385,11 @@ struct RangePlan {
     long long total;                    // workgroups
 };
 
-constexpr int kJoin = 32;       // ranges that each workgroup of the second pass may join
+constexpr int kAtOnce = 8;      // rows that a thread loads at a time
+constexpr int kJoin = 64;       // ranges that each workgroup of the second pass may join
 
+// Ranges are whole batches of all threads (32 KB of x in 16-byte vectors), as many as
+// make 2048 workgroups at most.
 RangePlan range_plan(int size, bool grad, long long N, long long P, int C)
 {
     RangePlan p;
@@ -364,13 +400,13 @@ RangePlan range_plan(int size, bool grad, long long N, long long P, int C)
     p.tx = std::min(vectors, 256);
     p.ty = 256 / p.tx;
     p.cols = (int)cdiv(vectors, 256);
-    // 2048 workgroups, and 32 rows at least, where there are as many
-    const long long want = std::max(1LL, cdiv(2048, std::max(1LL, N * p.cols)));
-    long long chunks = std::max(1LL, std::min(want, P / 32));
-    p.joined = !grad && (chunks <= kJoin || N >= 8);
+    const long long unit = (long long)kAtOnce * p.ty;
+    long long chunks = std::max(1LL, cdiv(2048, std::max(1LL, N * p.cols)));
+    chunks = std::min(chunks, cdiv(P, unit));
+    p.joined = !grad && chunks <= 2 * kJoin;
     if (p.joined)
         chunks = std::min(chunks, (long long)kJoin);
-    p.chunk = (int)cdiv(P, chunks);
+    p.chunk = (int)std::min(cdiv(cdiv(P, chunks), unit) * unit, P);
     p.chunks = (int)cdiv(P, p.chunk);
     p.total = N * p.chunks * p.cols;
     return p;
@@ -411,9 +447,39 @@ __device__ __forceinline__ int join_lanes(int count)
     return l;
 }
 
+// A batch of a thread's rows, from row r of its range on and ty rows apart.  Rows
+// behind the range's last one are read as that one (so that all loads go out at once)
+// and weigh nothing.
+template <typename T, int V, int B> struct Rows {
+    Raw<T, V> v[B];
+    __device__ __forceinline__ void load(const T *x, long long ld, int r, const RangePlan &p,
+                                         int rows)
+    {
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            v[k].load(x + min(r + k * p.ty, rows - 1) * ld);
+    }
+};
+
+// Count, mean and sum of squares around it of some numbers.
+struct Moments {
+    float n, mean, m2;
+    __device__ __forceinline__ void add(float bn, float bmean, float bm2)
+    {
+        const float all = n + bn, part = all > 0.0f ? bn / all : 0.0f, d = bmean - mean;
+        mean += d * part;
+        m2 += bm2 + (d * n) * (d * part);      // 0 for n = 0, however large d
+        n = all;
+    }
+    __device__ __forceinline__ void add_lanes(int lanes)
+    {
+        for (int d = 1; d < lanes; d *= 2)
+            add(__shfl_xor(n, d), __shfl_xor(mean, d), __shfl_xor(m2, d));
+    }
+};
+
 // The mean and the sum of squares around it, per channel of a thread, of rows taken 8
 // at a time: those of the 8 are exact to rounding and are joined to the rest.
-constexpr int kRowsAtOnce = 8;
 
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_range_stats(NormArgs a, RangePlan p, float2 *part)
@@ -423,44 +489,31 @@ __global__ __launch_bounds__(256) void k_range_stats(NormArgs a, RangePlan p, fl
         return;
     const RangeAt at(p, a.P, a.C, false);
     float mean[V] = {}, m2[V] = {}, count = 0.0f;
-    const bool mine = at.c < a.C;
-    if (mine) {
+    if (at.c < a.C) {
         const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + at.c;
-        int r = at.y;
-        for (; r + (kRowsAtOnce - 1) * p.ty < at.rows; r += kRowsAtOnce * p.ty) {
-            Raw<T, V> v[kRowsAtOnce];
-#pragma unroll
-            for (int k = 0; k < kRowsAtOnce; ++k)
-                v[k].load(x + (long long)(r + k * p.ty) * a.ldx);
-            const float all = count + kRowsAtOnce, part_of = kRowsAtOnce / all;
+        for (int r = at.y; r < at.rows; r += kAtOnce * p.ty) {
+            Rows<T, V, kAtOnce> in;
+            in.load(x, a.ldx, r, p, at.rows);
+            const int left = (at.rows - 1 - r) / p.ty + 1;
+            const float n = (float)min(left, kAtOnce), one = 1.0f / n;
+            const float all = count + n, part_of = n / all;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float s = 0.0f, q = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kRowsAtOnce; ++k)
-                    s += v[k].get(e);
-                s *= 1.0f / kRowsAtOnce;
+                for (int k = 0; k < kAtOnce; ++k)
+                    s += k < left ? in.v[k].get(e) : 0.0f;
+                s *= one;
 #pragma unroll
-                for (int k = 0; k < kRowsAtOnce; ++k) {
-                    const float d = v[k].get(e) - s;
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const float d = k < left ? in.v[k].get(e) - s : 0.0f;
                     q += d * d;
                 }
                 const float d = s - mean[e];
                 mean[e] += d * part_of;
-                m2[e] += q + d * d * (count * part_of);
+                m2[e] += q + (d * count) * (d * part_of);
             }
             count = all;
-        }
-        for (; r < at.rows; r += p.ty) {
-            float v[V];
-            load<T, V>(x + (long long)r * a.ldx, v);
-            count += 1.0f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = v[e] - mean[e];
-                mean[e] += d / count;
-                m2[e] += d * (v[e] - mean[e]);
-            }
         }
     }
 #pragma unroll
@@ -493,47 +546,63 @@ __global__ __launch_bounds__(256) void k_range_stats(NormArgs a, RangePlan p, fl
         for (int d = 1; d < lanes; d *= 2)
             q += __shfl_xor(q, d);
         if (lane == 0)
-            part[(((long long)at.n * p.chunks + at.chunk) * p.cols + at.col) * a.groups + g] =
+            part[(((long long)at.n * a.groups + g) * p.chunks + at.chunk) * p.cols + at.col] =
                 make_float2(joint, q);
     }
 }
 
-// (mean, rstd) of group g of instance n from its ranges', in every lane of a team.
-__device__ __forceinline__ float2 join(const NormArgs &a, const RangePlan &p, const float2 *part,
-                                       int n, int g, int lane, int lanes)
+// A lane's share (of `lanes`) of the ranges of group g of instance n.
+__device__ __forceinline__ Moments join(const NormArgs &a, const RangePlan &p,
+                                        const float2 *part, int n, int g, int lane, int lanes)
 {
     const int cg = a.C / a.groups, block = 256 * p.V;
     const int col0 = g * cg / block, cols = ((g + 1) * cg - 1) / block - col0 + 1;
-    const float2 *from = part + (long long)n * p.chunks * p.cols * a.groups + g;
-    auto of = [&](int i, auto f) {
-        const int chunk = i / cols, col = col0 + i % cols;
-        const long long rows = min((long long)p.chunk, a.P - (long long)chunk * p.chunk);
-        const int wide = min((g + 1) * cg, (col + 1) * block) - max(g * cg, col * block);
-        f((float)rows * (float)wide, from[((long long)chunk * p.cols + col) * a.groups]);
-    };
-    float s = 0.0f, q = 0.0f;
-    for (int i = lane; i < p.chunks * cols; i += lanes)
-        of(i, [&](float c, float2 v) { s += c * v.x; });
-    for (int d = 1; d < lanes; d *= 2)
-        s += __shfl_xor(s, d);
-    const float all = (float)a.P * (float)cg, mean = s / all;
-    for (int i = lane; i < p.chunks * cols; i += lanes)
-        of(i, [&](float c, float2 v) { q += v.y + c * (v.x - mean) * (v.x - mean); });
-    for (int d = 1; d < lanes; d *= 2)
-        q += __shfl_xor(q, d);
-    return make_float2(mean, 1.0f / sqrtf(q / all + a.eps));
+    const float2 *from = part + ((long long)n * a.groups + g) * p.chunks * p.cols + col0;
+    const int items = p.chunks * cols;
+    Moments sum{};
+    for (int i = lane; i < items; i += 8 * lanes) {
+        float2 v[8];
+        float count[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int j = min(i + k * lanes, items - 1);
+            const int chunk = cols == 1 ? j : j / cols, c = j - chunk * cols, col = col0 + c;
+            const long long rows = min((long long)p.chunk, a.P - (long long)chunk * p.chunk);
+            const int wide = min((g + 1) * cg, (col + 1) * block) - max(g * cg, col * block);
+            count[k] = i + k * lanes < items ? (float)rows * (float)wide : 0.0f;
+            v[k] = from[(long long)chunk * p.cols + c];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sum.add(count[k], v[k].x, count[k] > 0.0f ? v[k].y : 0.0f);
+    }
+    return sum;
 }
 
+__device__ __forceinline__ float2 stats_of(const Moments &m, float eps)
+{
+    return make_float2(m.mean, 1.0f / sqrtf(m.m2 / m.n + eps));
+}
+
+// A workgroup for each group of each instance.
 __global__ __launch_bounds__(256) void k_norm_join(NormArgs a, RangePlan p, const float2 *part,
                                                    float2 *stats)
 {
-    const long long id = (long long)block_id() * 4 + (threadIdx.x >> 6);
+    __shared__ Moments of[4];
+    const long long id = block_id();
     if (id >= a.N * a.groups)
         return;
-    const float2 v = join(a, p, part, (int)(id / a.groups), (int)(id % a.groups),
-                          threadIdx.x & 63, 64);
+    Moments m = join(a, p, part, (int)(id / a.groups), (int)(id % a.groups), threadIdx.x, 256);
+    m.add_lanes(64);
     if ((threadIdx.x & 63) == 0)
-        stats[id] = v;
+        of[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+            m.add(of[k].n, of[k].mean, of[k].m2);
+        stats[id] = stats_of(m, a.eps);
+    }
 }
 
 // The second pass.  stats: all groups', or nullptr where they are joined here.
@@ -547,14 +616,20 @@ __global__ __launch_bounds__(256) void k_range_apply(NormArgs a, RangePlan p, co
     const RangeAt at(p, a.P, a.C, true);
     const int cg = a.C / a.groups, c_first = at.first(p), c_last = at.last(p, a.C);
     const int g0 = c_first / cg, touched = (c_last - 1) / cg - g0 + 1;
+    // the first rows are on their way while the ranges are joined
+    const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + min(at.c, a.C - V);
+    Rows<T, V, kAtOnce> in;
+    in.load(x, a.ldx, at.y, p, at.rows);
     if (stats) {
         for (int g = threadIdx.x; g < touched; g += 256)
             of[g] = stats[(long long)at.n * a.groups + g0 + g];
     } else {
         const int lanes = join_lanes(touched), lane = threadIdx.x % lanes;
         for (int g = (int)threadIdx.x / lanes; g < touched; g += 256 / lanes) {
-            const float2 v = join(a, p, part, at.n, g0 + g, lane, lanes);
+            Moments m = join(a, p, part, at.n, g0 + g, lane, lanes);
+            m.add_lanes(lanes);
             if (lane == 0) {
+                const float2 v = stats_of(m, a.eps);
                 of[g] = v;
                 // the block of the group's first channel keeps them
                 if (a.stats && at.chunk == 0 && (g0 + g) * cg >= c_first)
@@ -575,30 +650,22 @@ __global__ __launch_bounds__(256) void k_range_apply(NormArgs a, RangePlan p, co
         mean[e] = v.x;
         f[e] = v.y * w[e];
     }
-    const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + at.c;
     T *y = static_cast<T *>(a.y) + at.row0 * a.ldy + at.c;
-    auto one = [&](const Raw<T, V> &v, int r) {
-        float z[V];
+    for (int r = at.y;;) {
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            z[e] = (v.get(e) - mean[e]) * f[e] + b[e];
-        act_all(z, a.act);
-        store<T, V>(y + (long long)r * a.ldy, z);
-    };
-    int r = at.y;
-    for (; r + (kRowsAtOnce - 1) * p.ty < at.rows; r += kRowsAtOnce * p.ty) {
-        Raw<T, V> v[kRowsAtOnce];
+        for (int k = 0; k < kAtOnce; ++k) {
+            float z[V];
 #pragma unroll
-        for (int k = 0; k < kRowsAtOnce; ++k)
-            v[k].load(x + (long long)(r + k * p.ty) * a.ldx);
-#pragma unroll
-        for (int k = 0; k < kRowsAtOnce; ++k)
-            one(v[k], r + k * p.ty);
-    }
-    for (; r < at.rows; r += p.ty) {
-        Raw<T, V> v;
-        v.load(x + (long long)r * a.ldx);
-        one(v, r);
+            for (int e = 0; e < V; ++e)
+                z[e] = (in.v[k].get(e) - mean[e]) * f[e] + b[e];
+            act_all(z, a.act);
+            if (r + k * p.ty < at.rows)
+                store<T, V>(y + (r + k * p.ty) * a.ldy, z);
+        }
+        r += kAtOnce * p.ty;
+        if (r >= at.rows)
+            return;
+        in.load(x, a.ldx, r, p, at.rows);
     }
 }
 
@@ -624,39 +691,28 @@ __global__ __launch_bounds__(256) void k_range_sums(NormArgs a, RangePlan p, flo
         }
         const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + at.c;
         const T *dy = static_cast<const T *>(a.dy) + at.row0 * a.lddy + at.c;
-        auto one = [&](const Raw<T, V> &rx, const Raw<T, V> &rd) {
-            float z[V], xhat[V];
+        constexpr int B = kAtOnce / 2;
+        for (int r = at.y; r < at.rows; r += B * p.ty) {
+            Rows<T, V, B> rx, rd;
+            rx.load(x, a.ldx, r, p, at.rows);
+            rd.load(dy, a.lddy, r, p, at.rows);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                xhat[e] = (rx.get(e) - mean[e]) * rstd[e];
-                z[e] = xhat[e] * w[e] + b[e];
+            for (int k = 0; k < B; ++k) {
+                float z[V], xhat[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    xhat[e] = (rx.v[k].get(e) - mean[e]) * rstd[e];
+                    z[e] = xhat[e] * w[e] + b[e];
+                }
+                slope_all(z, a.act);
+                const bool counts = r + k * p.ty < at.rows;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float dz = counts ? rd.v[k].get(e) * z[e] : 0.0f;
+                    db[e] += dz;
+                    dw[e] += dz * xhat[e];
+                }
             }
-            slope_all(z, a.act);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float dz = rd.get(e) * z[e];
-                db[e] += dz;
-                dw[e] += dz * xhat[e];
-            }
-        };
-        constexpr int kAtOnce = 4;
-        int r = at.y;
-        for (; r + (kAtOnce - 1) * p.ty < at.rows; r += kAtOnce * p.ty) {
-            Raw<T, V> rx[kAtOnce], rd[kAtOnce];
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                rx[k].load(x + (long long)(r + k * p.ty) * a.ldx);
-                rd[k].load(dy + (long long)(r + k * p.ty) * a.lddy);
-            }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-                one(rx[k], rd[k]);
-        }
-        for (; r < at.rows; r += p.ty) {
-            Raw<T, V> rx, rd;
-            rx.load(x + (long long)r * a.ldx);
-            rd.load(dy + (long long)r * a.lddy);
-            one(rx, rd);
         }
     }
 #pragma unroll
@@ -704,16 +760,47 @@ __global__ __launch_bounds__(1024) void k_range_fold(const float *part, int chun
     }
 }
 
+// dw and db of 64 of the 2 C columns from the instances' sums.
+constexpr int kInstances = 64;
+
+__device__ __forceinline__ void add_instances(const NormArgs &a, const float *sums, int block,
+                                              float *lds)
+{
+    const long long col = block * 64LL + (threadIdx.x & 63);
+    const int wave = threadIdx.x >> 6;
+    float s = 0.0f;
+    if (col < 2 * a.C)
+#pragma unroll 4
+        for (int n = wave; n < a.N; n += 4)
+            s += sums[n * 2LL * a.C + col];
+    lds[threadIdx.x] = s;
+    __syncthreads();
+    float *to = col < a.C ? a.dw : a.db;
+    if (wave == 0 && col < 2 * a.C && to)
+        to[col < a.C ? col : col - a.C] =
+            ((lds[threadIdx.x] + lds[threadIdx.x + 64]) + lds[threadIdx.x + 128]) +
+            lds[threadIdx.x + 192];
+}
+
 // Gradient, second pass: dx, with the groups' means from their channels' sums.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_range_dx(NormArgs a, RangePlan p, const float *sums)
 {
     __shared__ float2 of[256 * V];
-    if (block_id() >= p.total)
+    if (block_id() >= p.total) {
+        // workgroups behind those of dx, if there are any, add up dw and db
+        add_instances(a, sums, (int)(block_id() - p.total), reinterpret_cast<float *>(of));
         return;
+    }
     const RangeAt at(p, a.P, a.C, true);
     const int cg = a.C / a.groups, c_first = at.first(p), c_last = at.last(p, a.C);
     const int g0 = c_first / cg, touched = (c_last - 1) / cg - g0 + 1;
+    constexpr int B = kAtOnce / 2;
+    const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + min(at.c, a.C - V);
+    const T *dy = static_cast<const T *>(a.dy) + at.row0 * a.lddy + min(at.c, a.C - V);
+    Rows<T, V, B> rx, rd;
+    rx.load(x, a.ldx, at.y, p, at.rows);
+    rd.load(dy, a.lddy, at.y, p, at.rows);
     {
         const int lanes = join_lanes(touched), lane = threadIdx.x % lanes;
         const float *dw = sums + (long long)at.n * 2 * a.C, *db = dw + a.C;
@@ -748,40 +835,28 @@ __global__ __launch_bounds__(256) void k_range_dx(NormArgs a, RangePlan p, const
         m1[e] = of[g - g0].x;
         m2[e] = of[g - g0].y;
     }
-    const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + at.c;
-    const T *dy = static_cast<const T *>(a.dy) + at.row0 * a.lddy + at.c;
     T *dx = static_cast<T *>(a.dx) + at.row0 * a.lddx + at.c;
-    auto one = [&](const Raw<T, V> &rx, const Raw<T, V> &rd, int r) {
-        float z[V], xhat[V];
+    for (int r = at.y;;) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            xhat[e] = (rx.get(e) - mean[e]) * rstd[e];
-            z[e] = xhat[e] * w[e] + b[e];
+        for (int k = 0; k < B; ++k) {
+            float z[V], xhat[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                xhat[e] = (rx.v[k].get(e) - mean[e]) * rstd[e];
+                z[e] = xhat[e] * w[e] + b[e];
+            }
+            slope_all(z, a.act);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                z[e] = rstd[e] * (rd.v[k].get(e) * z[e] * w[e] - m1[e] - xhat[e] * m2[e]);
+            if (r + k * p.ty < at.rows)
+                store<T, V>(dx + (r + k * p.ty) * a.lddx, z);
         }
-        slope_all(z, a.act);
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            z[e] = rstd[e] * (rd.get(e) * z[e] * w[e] - m1[e] - xhat[e] * m2[e]);
-        store<T, V>(dx + (long long)r * a.lddx, z);
-    };
-    constexpr int kAtOnce = 4;
-    int r = at.y;
-    for (; r + (kAtOnce - 1) * p.ty < at.rows; r += kAtOnce * p.ty) {
-        Raw<T, V> rx[kAtOnce], rd[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            rx[k].load(x + (long long)(r + k * p.ty) * a.ldx);
-            rd[k].load(dy + (long long)(r + k * p.ty) * a.lddy);
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-            one(rx[k], rd[k], r + k * p.ty);
-    }
-    for (; r < at.rows; r += p.ty) {
-        Raw<T, V> rx, rd;
-        rx.load(x + (long long)r * a.ldx);
-        rd.load(dy + (long long)r * a.lddy);
-        one(rx, rd, r);
+        r += B * p.ty;
+        if (r >= at.rows)
+            return;
+        rx.load(x, a.ldx, r, p, at.rows);
+        rd.load(dy, a.lddy, r, p, at.rows);
     }
 }
 
@@ -855,14 +930,16 @@ int launch_norm_fwd(const NormArgs &a, void *stream)
     const int size = elem_size(a.type);
     RowsPlan rows;
     if (rows_plan(size, a.N, a.P, a.C, a.groups, &rows)) {
-        const long long blocks = cdiv(a.N, rows.slots) * rows.windows;
+        const long long blocks = cdiv(a.N, (long long)rows.slots * rows.R) * rows.windows;
         if (blocks > kMostBlocks)
             return DWCONV_ERR_BAD_DIM;
         return with_type(a.type, [&](auto *t) {
             using T = std::remove_pointer_t<decltype(t)>;
             return with_width<T>(rows.V, [&](auto v) {
                 return with_keep(rows.K, [&](auto k) {
-                    return dwconv::launch_kernel(k_norm_rows<T, v.value, k.value>,
+                    constexpr int R = k.value < 4 ? 4 / k.value : 1;
+                    return dwconv::launch_kernel(rows.R == 1 ? k_norm_rows<T, v.value, k.value, 1>
+                                                             : k_norm_rows<T, v.value, k.value, R>,
                                                  grid_of(blocks), dim3(rows.threads), 0, st, a,
                                                  rows);
                 });
@@ -883,7 +960,7 @@ int launch_norm_fwd(const NormArgs &a, void *stream)
             int rc = dwconv::launch_kernel(k_range_stats<T, v.value>, grid_of(p.total), dim3(256),
                                            0, st, a, p, part);
             if (rc == DWCONV_OK && !p.joined)
-                rc = dwconv::launch_kernel(k_norm_join, grid_of(cdiv(a.N * a.groups, 4)),
+                rc = dwconv::launch_kernel(k_norm_join, grid_of(a.N * a.groups),
                                            dim3(256), 0, st, a, p, (const float2 *)part, joint);
             if (rc == DWCONV_OK)
                 rc = dwconv::launch_kernel(k_range_apply<T, v.value>, grid_of(p.total), dim3(256),
@@ -926,9 +1003,12 @@ int launch_norm_grad(const NormArgs &a, void *stream)
         return launch_columns(part, rows.blocks, a.C, strips, a.dw, a.db, st);
     }
     const RangePlan p = range_plan(size, true, a.N, a.P, a.C);
-    if (p.total > kMostBlocks)
+    if (p.total > kMostBlocks - a.C)
         return DWCONV_ERR_BAD_DIM;
     float *sums = p.chunks > 1 ? reinterpret_cast<float *>(space + s.part) : part;
+    // up to kInstances of them are added up beside dx, more by launches of their own
+    const bool beside = a.dx && (a.dw || a.db) && a.N <= kInstances;
+    const long long extra = beside ? cdiv(2LL * a.C, 64) : 0;
     int rc = with_type(a.type, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
         return with_width<T>(p.V, [&](auto v) {
@@ -939,12 +1019,12 @@ int launch_norm_grad(const NormArgs &a, void *stream)
                                            dim3(1024), 0, st, (const float *)part, p.chunks, a.C,
                                            a.N, sums);
             if (rc == DWCONV_OK && a.dx)
-                rc = dwconv::launch_kernel(k_range_dx<T, v.value>, grid_of(p.total), dim3(256), 0,
-                                           st, a, p, (const float *)sums);
+                rc = dwconv::launch_kernel(k_range_dx<T, v.value>, grid_of(p.total + extra),
+                                           dim3(256), 0, st, a, p, (const float *)sums);
             return rc;
         });
     });
-    if (rc != DWCONV_OK || (!a.dw && !a.db))
+    if (rc != DWCONV_OK || (!a.dw && !a.db) || beside)
         return rc;
     return launch_columns(sums, a.N, a.C, strips, a.dw, a.db, st);
 }

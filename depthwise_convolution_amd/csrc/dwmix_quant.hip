@@ -27,11 +27,24 @@ struct RowScale {
         if (!finite)
             scale = __builtin_nanf("");
     }
-    // x / scale to the nearest integer, halves to even: the quotient is estimated,
-    // and the sign of |x| - (n + 1/2) scale, which one multiply-add gives exactly,
-    // says whether it lies above the half.  (An estimate on the wrong side of an
-    // integer is put right the same way.)  0 in a row that is not finite.
-    __device__ __forceinline__ int number(float x) const
+    // x / scale to the nearest integer, halves to even, 0 in a row that is not finite.
+    // The estimate x * inv is off by a few units in its last place, so that its nearest
+    // integer n is the quotient's unless the quotient lies that near to a half: where
+    // |x - n scale|, which one multiply-add rounds once and so compares exactly with half
+    // the scale, is not below it.
+    //
+    // Adding 3 * 2^22 rounds to an integer, which then is in the sum's low bits.
+    __device__ __forceinline__ float shifted(float x) const
+    {
+        return __builtin_fmaf(x * up, inv, 0x1.8p23f);
+    }
+    __device__ __forceinline__ float rest(float x, float t) const
+    {
+        return fabsf(__builtin_fmaf(-(t - 0x1.8p23f), step, x * up));
+    }
+    __device__ __forceinline__ bool near_half(float rest) const { return !(rest < 0.5f * step); }
+    // ... and what it is there
+    __device__ int exact(float x) const
     {
         const float v = fabsf(x) * up;
         const float n = fminf(floorf(v * inv), 127.0f);
@@ -40,6 +53,26 @@ struct RowScale {
         i += above > 0.0f || (above == 0.0f && (i & 1));
         i = inv == 0.0f ? 0 : min(i, 127);
         return x < 0.0f ? -i : i;
+    }
+    // The numbers of V elements
+    template <int V, typename F>
+    __device__ __forceinline__ Pack<signed char, V> numbers(F get) const
+    {
+        float t[V], most = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            t[v] = shifted(get(v));
+            most = fmaxf(most, rest(get(v), t[v]));
+        }
+        Pack<signed char, V> n;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            n.v[v] = (signed char)__builtin_bit_cast(int, t[v]);
+        if (near_half(most) || inv == 0.0f)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                n.v[v] = (signed char)exact(get(v));
+        return n;
     }
 };
 
@@ -102,11 +135,8 @@ __global__ __launch_bounds__(256) void k_quantize(QuantizeArgs a)
         largest = max(largest, magnitude((float)x[tail]));
     const RowScale s(row_max<WAVES>(largest));
     auto put = [&](const Raw<T, V> &r, int c) {
-        Pack<signed char, V> n;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            n.v[v] = (signed char)s.number(r.get(v));
-        *reinterpret_cast<Pack<signed char, V> *>(q + (long long)c * V) = n;
+        *reinterpret_cast<Pack<signed char, V> *>(q + (long long)c * V) =
+            s.numbers<V>([&](int v) { return r.get(v); });
     };
 #pragma unroll
     for (int j = 0; j < kKeep; ++j)
@@ -118,7 +148,7 @@ __global__ __launch_bounds__(256) void k_quantize(QuantizeArgs a)
         put(r, c);
     }
     if (tail < a.K)
-        q[tail] = (signed char)s.number((float)x[tail]);
+        q[tail] = (signed char)s.exact((float)x[tail]);
     if (at == 0)
         a.scale[m] = s.scale;
 }
