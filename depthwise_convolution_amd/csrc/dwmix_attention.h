@@ -51,6 +51,7 @@ struct Walk {
     const float *log_decay, *state0;    // state0 nullptr: zero
     float *state1;                      // nullptr: not kept
     float *slots;                       // states that segments start from, [item][H][Dk][Dv]
+    bool ready;                         // slots are another walk's, and [item][H][Dv][Dk]
     long long ldq, ldk, ldv, ldo;
     int gq, gk, gv;                     // heads that share one of the tensor's
     int H, Dk, Dv;
@@ -62,7 +63,17 @@ struct Walk {
     int segment, per_seq, items;        // tokens; segments of a dense sequence; of all
 };
 
-template <typename T> int launch_walk(const Walk &w, hipStream_t st);
+// Up to kWalks walks of one batch that do not need each other's results, but that one
+// may take another's slots.
+constexpr int kWalks = 3;
+template <typename T> int launch_walks(const Walk *w, int count, hipStream_t st);
+
+// What one launch does of them: workgroups for each, a multiple of 8 (so that the
+// order on the XCDs is the same for all).
+struct Walks {
+    Walk w[kWalks];
+    int blocks[kWalks];
+};
 // columns of the state that a workgroup takes
 inline int walk_tile(int Dk, int Dv) { return Dk > 128 || Dv <= 64 ? 64 : 128; }
 
@@ -197,7 +208,6 @@ constexpr int kChunkBytes = 128;
 // Kernels of their own, so that none pays registers for what it does not do: widths of
 // whole chunks of 16 bytes with results of T, or (the parts of shared heads) of
 // float32; and other widths.
-constexpr int kStatesIn = 0, kWalkIn = 0, kWalkOut = 2;
 enum Mode { ROWS, PARTS, ODD };
 
 constexpr int kFar = 0x7ffffff0;        // beyond every descriptor's bounds
@@ -215,7 +225,7 @@ template <typename T, int C, int D, int kThr> struct Tile {
     // The chunk's rows from `from` on, columns up to `wide`; `lowest` is the row of lowest
     // address (which may lie before the array where `from` is not 0).
     // CUT: some width is no whole number of chunks.
-    template <bool CUT, int HINT>
+    template <bool CUT>
     static __device__ __forceinline__ void fetch(u32x4 (&regs)[count], const T *lowest, int ld,
                                                  bool back, int from, int wide, int thread)
     {
@@ -229,7 +239,7 @@ template <typename T, int C, int D, int kThr> struct Tile {
                 const bool in = row + k * apart >= from && col < wide;
                 regs[k] = __builtin_bit_cast(
                     u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                               rsrc, in ? first + k * step : kFar, 0, HINT));
+                               rsrc, in ? first + k * step : kFar, 0, 0));
             }
         } else {        // rows that end within a chunk: element by element
 #pragma unroll
@@ -240,9 +250,9 @@ template <typename T, int C, int D, int kThr> struct Tile {
                     const bool in = row + k * apart >= from && col + e < wide;
                     const int at = in ? first + k * step + e * size : kFar;
                     if constexpr (size == 2)
-                        v[e] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, HINT);
+                        v[e] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
                     else
-                        v[e] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, HINT);
+                        v[e] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
                 }
                 if constexpr (size == 2)
                     regs[k] = u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
@@ -828,7 +838,10 @@ template <typename T, int DK, int DVT, int MT> struct Body {
                     *(lds_u2)at = u32x2{w[c][m][0], w[c][m][1]};
             }
     }
-    // (A thread reads what it will write of the next V itself.)
+    // (A thread reads what it will write of the next V itself.)  The results are stored
+    // past the caches, which keep the inputs that other passes read: 8 x 4096 tokens, 16
+    // heads of 128 bfloat16 149 us for 160, gradients of 8 x 2048 78 for 84 a walk.
+    static constexpr int kPast = 2;     // the "nt" bit of a store
     __device__ __forceinline__ void store_rows(lds_ptr v, const Walk &w, long long row0, int t,
                                                int first, int h, int dv0) const
     {
@@ -844,7 +857,7 @@ template <typename T, int DK, int DVT, int MT> struct Body {
             const u4 x = *(__attribute__((address_space(3))) u4 *)(v + r * VV::pitch + col * size);
             const int at = (w.back ? C - 1 - r : r) * ldo + col * size;
             __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, r >= first && col < wide ? at : kFar,
-                                                   0, kWalkOut);
+                                                   0, kPast);
         }
     }
 
@@ -912,13 +925,27 @@ struct Chunk {
     __device__ __forceinline__ Chunk next() const { return Chunk(n, C, done + C); }
 };
 
+// A workgroup's walk, and its number there.
+struct Which {
+    int i, block;
+    __device__ __forceinline__ explicit Which(const Walks &all) : i(0), block((int)block_id())
+    {
+#pragma unroll
+        for (int k = 0; k + 1 < kWalks; ++k)
+            if (i == k && block >= all.blocks[k]) {
+                block -= all.blocks[k];
+                ++i;
+            }
+    }
+};
+
 // What a workgroup walks.
 struct Part {
     int item, h, dv0;
-    __device__ __forceinline__ Part(const Walk &w, int tile)
+    __device__ __forceinline__ Part(const Walk &w, int tile, int block)
     {
         const int tiles = (w.Dv + tile - 1) / tile;
-        const int b = dwconv::xcd_tile((int)block_id(), w.items * w.H * tiles);
+        const int b = dwconv::xcd_tile(block, w.items * w.H * tiles);
         dv0 = b % tiles * tile;
         h = b / tiles % w.H;
         item = b / tiles / w.H;
@@ -933,15 +960,17 @@ constexpr int waves_a_simd(int DK, int DVT, int MT)
 
 // The state that a segment adds by itself, to the slot of the next one.
 template <typename T, int DK, int DVT, int MT, Mode MODE>
-__global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_states(Walk w)
+__global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_states(Walks all)
 {
+    const Which which(all);
+    const Walk &w = all.w[which.i];
     using B = Body<T, DK, DVT, MT>;
     __shared__ alignas(16) char lds[B::QK::bytes + B::VV::bytes];
     __shared__ float powers[B::powers];
     const lds_ptr lk = (lds_ptr)lds, lv = lk + B::QK::bytes;
-    if ((int)block_id() >= w.items * w.H * (int)((w.Dv + DVT - 1) / DVT))
+    if (which.block >= w.items * w.H * (int)((w.Dv + DVT - 1) / DVT))
         return;
-    const Part part(w, DVT);
+    const Part part(w, DVT, which.block);
     const Item at(w, part.item);
     if (at.seg + 1 >= at.segments(w))
         return;
@@ -964,8 +993,8 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_sta
     Chunk c(n, B::C);
     u32x4 rk[2][B::QK::count], rv[2][B::VV::count];
     auto fetch = [&](auto p, const Chunk &x) {
-        B::QK::template fetch<MODE == ODD, kStatesIn>(rk[p.value], k.at(x.t), ldk, w.back, x.first, w.Dk, b.thread);
-        B::VV::template fetch<MODE == ODD, kStatesIn>(rv[p.value], v.at(x.t), ldv, w.back, x.first, wide, b.thread);
+        B::QK::template fetch<MODE == ODD>(rk[p.value], k.at(x.t), ldk, w.back, x.first, w.Dk, b.thread);
+        B::VV::template fetch<MODE == ODD>(rv[p.value], v.at(x.t), ldv, w.back, x.first, wide, b.thread);
     };
     auto step = [&](auto p) {
         b.next_chunk();
@@ -999,12 +1028,16 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_sta
 // thread takes 4 adjacent elements (or one, where a state is no whole number of 4); the
 // segments of a sequence one after the other.
 template <int V>
-__global__ __launch_bounds__(256) void k_link(Walk w, int blocks)
+__global__ __launch_bounds__(256) void k_link(Walks all, int blocks)
 {
-    const unsigned id = block_id();
-    const int at = ((int)(id % blocks) * 256 + (int)threadIdx.x) * V;
-    const int h = (int)(id / blocks % w.H), seq = (int)(id / blocks / w.H), size = w.Dk * w.Dv;
-    if (seq >= w.batch.seqs || at >= size)
+    const Which which(all);
+    const Walk &w = all.w[which.i];
+    const int id = which.block, size = w.Dk * w.Dv;
+    if (id >= w.batch.seqs * w.H * blocks)
+        return;
+    const int at = (id % blocks * 256 + (int)threadIdx.x) * V;
+    const int h = id / blocks % w.H, seq = id / blocks / w.H;
+    if (at >= size)
         return;
     // (from the sequence itself: offsets that break the rules might lead an item's
     // search to another one, with more slots than there are from here on)
@@ -1041,16 +1074,18 @@ __global__ __launch_bounds__(256) void k_link(Walk w, int blocks)
 }
 
 template <typename T, int DK, int DVT, int MT, Mode MODE>
-__global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_walk(Walk w)
+__global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_walk(Walks all)
 {
+    const Which which(all);
+    const Walk &w = all.w[which.i];
     using B = Body<T, DK, DVT, MT>;
     __shared__ alignas(16) char lds[2 * B::QK::bytes + B::VV::bytes + B::C * B::pitch];
     __shared__ float downs[B::waves], powers[B::powers];
     const lds_ptr lq = (lds_ptr)lds, lk = lq + B::QK::bytes, lv = lk + B::QK::bytes,
                   lp = lv + B::VV::bytes;
-    if ((int)block_id() >= w.items * w.H * (int)((w.Dv + DVT - 1) / DVT))
+    if (which.block >= w.items * w.H * (int)((w.Dv + DVT - 1) / DVT))
         return;
-    const Part part(w, DVT);
+    const Part part(w, DVT, which.block);
     const Item at(w, part.item);
     const int count = at.segments(w);
     if (at.seg >= count)
@@ -1062,7 +1097,7 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
     const long long own = ((long long)at.seq * w.H + part.h) * size;
     const float *from = at.seg ? w.slots + ((long long)part.item * w.H + part.h) * size
                                : w.state0 ? w.state0 + own : nullptr;
-    b.load_state(w, from, at.seg ? false : w.flip, part.dv0);
+    b.load_state(w, from, at.seg ? w.ready : w.flip, part.dv0);
     const int t0 = at.seg * w.segment, n = min(w.segment, at.length - t0);
     const long long row = w.back ? (long long)at.row0 + at.length - 1 - t0 : at.row0 + t0;
     const Rows<T, B::C> q(w.q, w.ldq, w.back, row, part.h / w.gq * w.Dk),
@@ -1072,9 +1107,9 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
     const float whole = (float)exp((double)ld * B::C);
     Chunk c(n, B::C);
     u32x4 rq[B::QK::count], rk[B::QK::count], rv[B::VV::count];
-    B::QK::template fetch<MODE == ODD, kWalkIn>(rq, q.at(c.t), ldq, w.back, c.first, w.Dk, b.thread);
-    B::QK::template fetch<MODE == ODD, kWalkIn>(rk, k.at(c.t), ldk, w.back, c.first, w.Dk, b.thread);
-    B::VV::template fetch<MODE == ODD, kWalkIn>(rv, v.at(c.t), ldv, w.back, c.first, wide, b.thread);
+    B::QK::template fetch<MODE == ODD>(rq, q.at(c.t), ldq, w.back, c.first, w.Dk, b.thread);
+    B::QK::template fetch<MODE == ODD>(rk, k.at(c.t), ldk, w.back, c.first, w.Dk, b.thread);
+    B::VV::template fetch<MODE == ODD>(rv, v.at(c.t), ldv, w.back, c.first, wide, b.thread);
     for (; c.any(); c = c.next()) {
         const Chunk next = c.next();
         b.next_chunk();
@@ -1082,9 +1117,9 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
         B::QK::keep(lk, rk, b.thread);
         B::VV::keep(lv, rv, b.thread);
         __syncthreads();
-        B::QK::template fetch<MODE == ODD, kWalkIn>(rq, q.at(next.t), ldq, w.back, next.first, w.Dk, b.thread);
-        B::QK::template fetch<MODE == ODD, kWalkIn>(rk, k.at(next.t), ldk, w.back, next.first, w.Dk, b.thread);
-        B::VV::template fetch<MODE == ODD, kWalkIn>(rv, v.at(next.t), ldv, w.back, next.first, wide, b.thread);
+        B::QK::template fetch<MODE == ODD>(rq, q.at(next.t), ldq, w.back, next.first, w.Dk, b.thread);
+        B::QK::template fetch<MODE == ODD>(rk, k.at(next.t), ldk, w.back, next.first, w.Dk, b.thread);
+        B::VV::template fetch<MODE == ODD>(rv, v.at(next.t), ldv, w.back, next.first, wide, b.thread);
         __builtin_amdgcn_sched_barrier(0);
         const float down = b.scores(lq, lk, lp, w.s0);
         if (B::is_f16 && b.lane == 0)
@@ -1125,49 +1160,135 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
 
 }  // namespace
 
-template <typename T> int launch_walk(const Walk &w, hipStream_t st)
+// The kernel that a walk takes.
+struct Kind {
+    int dk, dvt;
+    Mode mode;
+    bool operator==(const Kind &o) const
+    {
+        return dk == o.dk && dvt == o.dvt && mode == o.mode;
+    }
+};
+
+template <typename T> Kind kind_of(const Walk &w)
 {
-    const long long blocks = (long long)w.items * w.H * cdiv(w.Dv, walk_tile(w.Dk, w.Dv));
-    if (blocks > 0x7fffffffLL)
-        return DWCONV_ERR_BAD_DIM;
-    auto run_as = [&](auto dk, auto dvt, auto mode) {
-        constexpr int DK = decltype(dk)::value, DVT = decltype(dvt)::value, MT = 1;
-        constexpr Mode MODE = decltype(mode)::value;
-        int rc = DWCONV_OK;
-        if (w.slots) {
-            rc = dwconv::launch_kernel(k_states<T, DK, DVT, MT, MODE == ODD ? ODD : ROWS>, grid_of(blocks), dim3(DVT / MT * 4), 0, st, w);
-            const bool by4 = w.Dk * w.Dv % 4 == 0;
-            const int links = (int)cdiv(w.Dk * w.Dv, by4 ? 1024 : 256);
-            const long long all = (long long)w.batch.seqs * w.H * links;
-            if (all > 0x7fffffffLL)
-                return (int)DWCONV_ERR_BAD_DIM;
-            if (rc == DWCONV_OK)
-                rc = by4 ? dwconv::launch_kernel(k_link<4>, grid_of(all), dim3(256), 0, st, w,
-                                                 links)
-                         : dwconv::launch_kernel(k_link<1>, grid_of(all), dim3(256), 0, st, w,
-                                                 links);
-        }
-        if (rc == DWCONV_OK)
-            rc = dwconv::launch_kernel(k_walk<T, DK, DVT, MT, MODE>, grid_of(blocks), dim3(DVT / MT * 4), 0, st, w);
-        return rc;
-    };
     const int whole = 16 / (int)sizeof(T);
-    auto run = [&](auto dk, auto dvt) {
-        if (w.Dk % whole || w.Dv % whole)
-            return run_as(dk, dvt, std::integral_constant<Mode, ODD>());
-        if constexpr (sizeof(T) == 2)
-            if (w.out32)
-                return run_as(dk, dvt, std::integral_constant<Mode, PARTS>());
-        return run_as(dk, dvt, std::integral_constant<Mode, ROWS>());
-    };
+    const Mode mode = w.Dk % whole || w.Dv % whole ? ODD
+                      : sizeof(T) == 2 && w.out32  ? PARTS
+                                                   : ROWS;
+    return {w.Dk > 128 ? 256 : w.Dk > 64 ? 128 : 64, walk_tile(w.Dk, w.Dv), mode};
+}
+
+template <typename T, typename F> int with_kind(const Kind &k, F f)
+{
     using std::integral_constant;
-    if (w.Dk > 128)
-        return run(integral_constant<int, 256>(), integral_constant<int, 64>());
-    if (w.Dk > 64)
-        return w.Dv > 64 ? run(integral_constant<int, 128>(), integral_constant<int, 128>())
-                         : run(integral_constant<int, 128>(), integral_constant<int, 64>());
-    return w.Dv > 64 ? run(integral_constant<int, 64>(), integral_constant<int, 128>())
-                     : run(integral_constant<int, 64>(), integral_constant<int, 64>());
+    auto mode = [&](auto dk, auto dvt) {
+        if (k.mode == ODD)
+            return f(dk, dvt, integral_constant<Mode, ODD>());
+        if constexpr (sizeof(T) == 2)
+            if (k.mode == PARTS)
+                return f(dk, dvt, integral_constant<Mode, PARTS>());
+        return f(dk, dvt, integral_constant<Mode, ROWS>());
+    };
+    if (k.dk == 256)
+        return mode(integral_constant<int, 256>(), integral_constant<int, 64>());
+    if (k.dk == 128)
+        return k.dvt > 64 ? mode(integral_constant<int, 128>(), integral_constant<int, 128>())
+                          : mode(integral_constant<int, 128>(), integral_constant<int, 64>());
+    return k.dvt > 64 ? mode(integral_constant<int, 64>(), integral_constant<int, 128>())
+                      : mode(integral_constant<int, 64>(), integral_constant<int, 64>());
+}
+
+// Walks gathered for one launch.
+struct Gather {
+    Walks all{};
+    int count = 0;
+    long long total = 0;
+    void add(const Walk &w, long long blocks)
+    {
+        blocks = cdiv(blocks, 8) * 8;
+        total += blocks;
+        all.w[count] = w;
+        all.blocks[count++] = (int)std::min(blocks, 0x7fffffffLL);
+    }
+    // f(grid) launches; the last walk's number of workgroups is not looked at
+    template <typename F> int launch(F f) const
+    {
+        if (count == 0)
+            return DWCONV_OK;
+        return total > 0x7fffffffLL - kGridRow ? (int)DWCONV_ERR_BAD_DIM : f(grid_of(total));
+    }
+};
+
+// For each kind among the walks that `wanted` names, one launch.
+template <typename W, typename K, typename F>
+int for_kinds(const Walk *w, int count, W wanted, K kind, F launch)
+{
+    bool done[kWalks] = {};
+    int rc = DWCONV_OK;
+    for (int i = 0; i < count && rc == DWCONV_OK; ++i) {
+        if (done[i] || !wanted(w[i]))
+            continue;
+        const Kind k = kind(w[i]);
+        Gather g;
+        for (int j = i; j < count; ++j)
+            if (!done[j] && wanted(w[j]) && kind(w[j]) == k) {
+                g.add(w[j], (long long)w[j].items * w[j].H * cdiv(w[j].Dv, k.dvt));
+                done[j] = true;
+            }
+        rc = launch(k, g);
+    }
+    return rc;
+}
+
+template <typename T> int launch_walks(const Walk *w, int count, hipStream_t st)
+{
+    auto cut = [](const Walk &x) { return x.slots && !x.ready; };
+    int rc = for_kinds(
+        w, count, cut,
+        [](const Walk &x) {         // states have no results
+            Kind k = kind_of<T>(x);
+            k.mode = k.mode == ODD ? ODD : ROWS;
+            return k;
+        },
+        [&](const Kind &kind, const Gather &g) {
+            return with_kind<T>(kind, [&](auto dk, auto dvt, auto mode) {
+                constexpr int DK = decltype(dk)::value, DVT = decltype(dvt)::value;
+                constexpr Mode MODE = decltype(mode)::value == ODD ? ODD : ROWS;
+                return g.launch([&](dim3 grid) {
+                    return dwconv::launch_kernel(k_states<T, DK, DVT, 1, MODE>, grid,
+                                                 dim3(DVT * 4), 0, st, g.all);
+                });
+            });
+        });
+    if (rc != DWCONV_OK)
+        return rc;
+    Gather links;
+    bool by4 = true;        // the same for all: Dk * Dv is
+    int wide = 0;
+    for (int i = 0; i < count; ++i)
+        if (cut(w[i])) {
+            by4 = w[i].Dk * w[i].Dv % 4 == 0;
+            wide = (int)cdiv(w[i].Dk * w[i].Dv, by4 ? 1024 : 256);
+            links.add(w[i], (long long)w[i].batch.seqs * w[i].H * wide);
+        }
+    rc = links.launch([&](dim3 grid) {
+        return by4 ? dwconv::launch_kernel(k_link<4>, grid, dim3(256), 0, st, links.all, wide)
+                   : dwconv::launch_kernel(k_link<1>, grid, dim3(256), 0, st, links.all, wide);
+    });
+    if (rc != DWCONV_OK)
+        return rc;
+    return for_kinds(
+        w, count, [](const Walk &) { return true; }, [](const Walk &x) { return kind_of<T>(x); },
+        [&](const Kind &kind, const Gather &g) {
+            return with_kind<T>(kind, [&](auto dk, auto dvt, auto mode) {
+                constexpr int DK = decltype(dk)::value, DVT = decltype(dvt)::value;
+                return g.launch([&](dim3 grid) {
+                    return dwconv::launch_kernel(k_walk<T, DK, DVT, 1, decltype(mode)::value>,
+                                                 grid, dim3(DVT * 4), 0, st, g.all);
+                });
+            });
+        });
 }
 #endif  // DWMIX_ATTENTION_KERNELS
 

@@ -85,20 +85,32 @@ __global__ __launch_bounds__(256) void k_attention_step(AttentionArgs a, int tx,
 
 // ------------------------------------------------------- shared heads
 // The gradients of a key or value head: the sum of its query heads', in order.
+struct Shared {
+    const float *part;
+    void *out;
+    long long ldo;
+    int D, blocks;
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void k_shared(const float *part, T *out, long long ldo, int rows,
-                                                int H, int KV, int D)
+__global__ __launch_bounds__(256) void k_shared(Shared k, Shared v, int rows, int H, int KV)
 {
-    const long long wide = (long long)KV * D, id = (long long)block_id() * 256 + threadIdx.x;
+    const bool first = block_id() < (unsigned)k.blocks;
+    const Shared &s = first ? k : v;
+    if (!s.out)
+        return;     // what the grid's last row has too many
+    const long long wide = (long long)KV * s.D;
+    const long long id =
+        (long long)(block_id() - (first ? 0u : (unsigned)k.blocks)) * 256 + threadIdx.x;
     const long long row = id / wide;
     if (row >= rows)
         return;
     const int at = (int)(id % wide), group = H / KV;
-    const float *from = part + row * H * D + (long long)(at / D) * group * D + at % D;
-    float s = from[0];
+    const float *from = s.part + row * H * s.D + (long long)(at / s.D) * group * s.D + at % s.D;
+    float sum = from[0];
     for (int g = 1; g < group; ++g)
-        s += from[(long long)g * D];
-    out[row * ldo + at] = (T)s;
+        sum += from[(long long)g * s.D];
+    static_cast<T *>(s.out)[row * s.ldo + at] = (T)sum;
 }
 
 // -------------------------------------------------------------- planning
@@ -140,17 +152,16 @@ SegmentPlan segment_plan(const Batch &b, bool packed, int H, int Dk, int Dv)
 
 long long round16(long long bytes) { return cdiv(bytes, 16) * 16; }
 
-int walk(int type, const Walk &w, hipStream_t st)
+int walk(int type, const Walk *w, int count, hipStream_t st)
 {
     return with_type(type, [&](auto *t) {
-        return launch_walk<std::remove_pointer_t<decltype(t)>>(w, st);
+        return launch_walks<std::remove_pointer_t<decltype(t)>>(w, count, st);
     });
 }
 
 // The parts of the walk that a batch and its plan set.
-void place(Walk &w, const Batch &b, int H, int Dk, int Dv, void *slots)
+void place(Walk &w, const SegmentPlan &p, const Batch &b, int H, int Dk, int Dv, void *slots)
 {
-    const SegmentPlan p = segment_plan(b, b.off != nullptr, H, Dk, Dv);
     w.batch = b;
     w.H = H;
     w.Dk = Dk;
@@ -161,23 +172,38 @@ void place(Walk &w, const Batch &b, int H, int Dk, int Dv, void *slots)
     w.slots = p.cut ? static_cast<float *>(slots) : nullptr;
 }
 
+// The gradients' segments and the parts of their workspace: the slots of dq and those
+// of dk and dv, then shared heads' parts.
+struct GradPlan {
+    SegmentPlan q, k;
+    long long slots, dk, dv, total;
+};
+
+GradPlan grad_plan(const Batch &b, bool packed, int H, int KV, int Dk, int Dv)
+{
+    GradPlan p;
+    p.q = p.k = segment_plan(b, packed, H, Dv, Dk);
+    p.slots = round16(p.q.slots);
+    p.dk = KV == H ? 0 : round16(4LL * b.rows * H * Dk);
+    p.dv = KV == H ? 0 : round16(4LL * b.rows * H * Dv);
+    p.total = 2 * p.slots + p.dk + p.dv;
+    return p;
+}
+
 }  // namespace
 
 long long attention_workspace(bool grad, const Batch &b, bool packed, int H, int KV, int Dk,
                               int Dv)
 {
-    const long long fwd = segment_plan(b, packed, H, Dk, Dv).slots;
-    if (!grad)
-        return round16(fwd);
-    const long long turned = segment_plan(b, packed, H, Dv, Dk).slots;
-    const long long parts = KV == H ? 0 : 4LL * b.rows * H * std::max(Dk, Dv);
-    return round16(std::max(fwd, turned)) + round16(parts);
+    return grad ? grad_plan(b, packed, H, KV, Dk, Dv).total
+                : round16(segment_plan(b, packed, H, Dk, Dv).slots);
 }
 
 int launch_attention_fwd(const AttentionArgs &a, void *stream)
 {
     Walk w{};
-    place(w, a.batch, a.H, a.Dk, a.Dv, a.workspace);
+    place(w, segment_plan(a.batch, a.batch.off != nullptr, a.H, a.Dk, a.Dv), a.batch, a.H, a.Dk,
+          a.Dv, a.workspace);
     w.q = a.q; w.k = a.k; w.v = a.v; w.out = a.y;
     w.ldq = a.ldq; w.ldk = a.ldk; w.ldv = a.ldv; w.ldo = a.ldy;
     w.gq = 1;
@@ -185,34 +211,22 @@ int launch_attention_fwd(const AttentionArgs &a, void *stream)
     w.log_decay = a.log_decay; w.state0 = a.h0; w.state1 = a.hT;
     w.s0 = w.s1 = a.scale;
     w.s2 = 1.0f;
-    return walk(a.type, w, static_cast<hipStream_t>(stream));
+    return walk(a.type, &w, 1, static_cast<hipStream_t>(stream));
 }
 
+// The walks of dq, of dk (and dh0) and of dv in the same launches.  The states of the
+// last two, sums of q dy^T from the end, are each other's transposes: computed once.
 int launch_attention_grad(const AttentionArgs &a, void *stream)
 {
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int group = a.H / a.KV;
-    const long long slots = round16(
-        std::max(segment_plan(a.batch, a.batch.off != nullptr, a.H, a.Dk, a.Dv).slots,
-                 segment_plan(a.batch, a.batch.off != nullptr, a.H, a.Dv, a.Dk).slots));
-    float *part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + slots);
-    auto shared = [&](void *out, long long ldo, int D) {
-        return with_type(a.type, [&](auto *t) {
-            using T = std::remove_pointer_t<decltype(t)>;
-            const long long blocks = cdiv((long long)a.batch.rows * a.KV * D, 256);
-            if (blocks > 0x7fffffffLL)
-                return (int)DWCONV_ERR_BAD_DIM;
-            return blocks == 0 ? (int)DWCONV_OK
-                               : dwconv::launch_kernel(k_shared<T>, grid_of(blocks), dim3(256), 0,
-                                                       st, (const float *)part,
-                                                       static_cast<T *>(out), ldo, a.batch.rows,
-                                                       a.H, a.KV, D);
-        });
-    };
-    int rc = DWCONV_OK;
+    const GradPlan plan = grad_plan(a.batch, a.batch.off != nullptr, a.H, a.KV, a.Dk, a.Dv);
+    char *space = static_cast<char *>(a.workspace), *parts = space + 2 * plan.slots;
+    Walk walks[kWalks] = {};
+    int count = 0;
     if (a.dq) {
-        Walk w{};
-        place(w, a.batch, a.H, a.Dv, a.Dk, a.workspace);
+        Walk &w = walks[count++];
+        place(w, plan.q, a.batch, a.H, a.Dv, a.Dk, space);
         w.q = a.dy; w.k = a.v; w.v = a.k; w.out = a.dq;
         w.ldq = a.lddy; w.ldk = a.ldv; w.ldv = a.ldk; w.ldo = a.lddq;
         w.gq = 1;
@@ -220,52 +234,64 @@ int launch_attention_grad(const AttentionArgs &a, void *stream)
         w.log_decay = a.log_decay; w.state0 = a.h0; w.flip = true;
         w.s0 = w.s1 = a.scale;
         w.s2 = 1.0f;
-        rc = walk(a.type, w, st);
     }
-    // dk, and the state's gradient with it
-    if (rc == DWCONV_OK && (a.dk || a.dh0)) {
-        Walk w{};
-        place(w, a.batch, a.H, a.Dv, a.Dk, a.workspace);
+    const bool with_k = a.dk || a.dh0;
+    Shared dk{reinterpret_cast<float *>(parts), nullptr, a.lddk, a.Dk, 0};
+    Shared dv{reinterpret_cast<float *>(parts + plan.dk), nullptr, a.lddv, a.Dv, 0};
+    if (with_k) {
+        Walk &w = walks[count++];
+        place(w, plan.k, a.batch, a.H, a.Dv, a.Dk, space + plan.slots);
         w.q = a.v; w.k = a.dy; w.v = a.q;
         w.ldq = a.ldv; w.ldk = a.lddy; w.ldv = a.ldq;
         w.gq = group;
         w.gk = w.gv = 1;
         w.out = a.dk; w.ldo = a.lddk;
         if (group > 1 && a.dk) {
-            w.out = part;
+            w.out = parts;
             w.ldo = (long long)a.H * a.Dk;
             w.out32 = true;
+            dk.out = a.dk;
         }
         w.log_decay = a.log_decay; w.state0 = a.dhT; w.state1 = a.dh0; w.flip = true;
         w.s0 = w.s2 = a.scale;
         w.s1 = 1.0f;
         w.late = w.back = 1;
-        rc = walk(a.type, w, st);
-        if (rc == DWCONV_OK && w.out32)
-            rc = shared(a.dk, a.lddk, a.Dk);
     }
-    if (rc == DWCONV_OK && a.dv) {
-        Walk w{};
-        place(w, a.batch, a.H, a.Dk, a.Dv, a.workspace);
+    if (a.dv) {
+        Walk &w = walks[count++];
+        place(w, plan.k, a.batch, a.H, a.Dk, a.Dv, space + plan.slots);
+        w.ready = with_k;
         w.q = a.k; w.k = a.q; w.v = a.dy;
         w.ldq = a.ldk; w.ldk = a.ldq; w.ldv = a.lddy;
         w.gq = group;
         w.gk = w.gv = 1;
         w.out = a.dv; w.ldo = a.lddv;
         if (group > 1) {
-            w.out = part;
+            w.out = parts + plan.dk;
             w.ldo = (long long)a.H * a.Dv;
             w.out32 = true;
+            dv.out = a.dv;
         }
         w.log_decay = a.log_decay; w.state0 = a.dhT;
         w.s0 = w.s2 = a.scale;
         w.s1 = 1.0f;
         w.late = w.back = 1;
-        rc = walk(a.type, w, st);
-        if (rc == DWCONV_OK && w.out32)
-            rc = shared(a.dv, a.lddv, a.Dv);
     }
-    return rc;
+    const int rc = walk(a.type, walks, count, st);
+    if (rc != DWCONV_OK || (!dk.out && !dv.out) || a.batch.rows == 0)
+        return rc;
+    auto blocks_of = [&](const Shared &s) {
+        return s.out ? cdiv((long long)a.batch.rows * a.KV * s.D, 256) : 0;
+    };
+    const long long total = blocks_of(dk) + blocks_of(dv);
+    if (total > 0x7fffffffLL)
+        return DWCONV_ERR_BAD_DIM;
+    dk.blocks = (int)blocks_of(dk);
+    dv.blocks = (int)blocks_of(dv);
+    return with_type(a.type, [&](auto *t) {
+        return dwconv::launch_kernel(k_shared<std::remove_pointer_t<decltype(t)>>, grid_of(total),
+                                     dim3(256), 0, st, dk, dv, a.batch.rows, a.H, a.KV);
+    });
 }
 
 int launch_attention_step(const AttentionArgs &a, void *stream)

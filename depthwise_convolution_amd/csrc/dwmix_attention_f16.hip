@@ -3,5 +3,5 @@
 #include "dwmix_attention.h"
 
 namespace dwmix {
-template int launch_walk<dwseq::f16>(const Walk &w, hipStream_t st);
+template int launch_walks<dwseq::f16>(const Walk *w, int count, hipStream_t st);
 }  // namespace dwmix

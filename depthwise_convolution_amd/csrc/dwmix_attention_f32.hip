@@ -3,5 +3,5 @@
 #include "dwmix_attention.h"
 
 namespace dwmix {
-template int launch_walk<float>(const Walk &w, hipStream_t st);
+template int launch_walks<float>(const Walk *w, int count, hipStream_t st);
 }  // namespace dwmix
