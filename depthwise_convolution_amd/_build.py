@@ -15,7 +15,8 @@ HIP_SOURCES = ["dwconv_direct.hip", "dwconv_tiled_nhwc.hip", "dwconv_tiled_nchw.
                "dwconv_wgrad.hip", "dwconv_launch.hip", "dwconv_stream.hip",
                "dwseq_conv.hip", "dwseq_scan.hip", "dwseq_linear.hip",
                "dwseq_gemm_f32.hip", "dwseq_gemm_f16.hip", "dwseq_gemm_bf16.hip",
-               "dwseq_gemm_i8.hip", "dwmix_quant.hip", "dwmix_norm.hip", "dwmix_attention.hip",
+               "dwseq_gemm_i8.hip", "dwmix_quant.hip", "dwmix_few.hip",
+               "dwmix_norm.hip", "dwmix_attention.hip",
                "dwmix_attention_f32.hip", "dwmix_attention_f16.hip", "dwmix_attention_bf16.hip"]
 ARCH = "gfx950"
 

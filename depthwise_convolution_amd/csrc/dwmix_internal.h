@@ -62,6 +62,9 @@ struct LinearI8Args {
 long long linear_i8_workspace(bool quantized, int M, int N, int K);
 void linear_i8_describe(bool quantized, bool aligned, int M, int N, int K, const char **name,
                         int *splits);
+// Few rows that are quantised by the product's own launch: 64 elements a thread of 512.
+inline bool few_rows_fit(int M, int K) { return M <= 16 && (long long)M * K <= 32768; }
+int launch_linear_few(const LinearI8Args &a, void *stream);
 int launch_linear_i8(const LinearI8Args &a, void *stream);
 
 }  // namespace dwmix

@@ -2,79 +2,13 @@
 // integers with a scale for each row and column (include/dwconv_mix.h).  The
 // product's kernels are those of dwseq_gemm.h.
 #include "dwmix_internal.h"
+#include "dwmix_quantize.h"
 #include "dwseq_gemm.h"
 
 namespace dwmix {
 namespace {
 
 using namespace dwseq;
-
-// What a row's largest absolute value, as bits, gives: its scale, and the factors
-// that its numbers are made with.  Rows of very small scales are computed 2^60
-// times larger, so that a remainder next to a half never falls below the smallest
-// float32.
-struct RowScale {
-    float scale, up, step, inv;
-
-    __device__ __forceinline__ explicit RowScale(unsigned largest)
-    {
-        const bool finite = largest < 0x7f800000u;
-        scale = fmaxf(__builtin_bit_cast(float, finite ? largest : 0u) * (1.0f / 127.0f),
-                      0x1p-126f);
-        up = scale < 0x1p-60f ? 0x1p60f : 1.0f;
-        step = scale * up;
-        inv = finite ? __builtin_amdgcn_rcpf(step) : 0.0f;
-        if (!finite)
-            scale = __builtin_nanf("");
-    }
-    // x / scale to the nearest integer, halves to even, 0 in a row that is not finite.
-    // The estimate x * inv is off by a few units in its last place, so that its nearest
-    // integer n is the quotient's unless the quotient lies that near to a half: where
-    // |x - n scale|, which one multiply-add rounds once and so compares exactly with half
-    // the scale, is not below it.
-    //
-    // Adding 3 * 2^22 rounds to an integer, which then is in the sum's low bits.
-    __device__ __forceinline__ float shifted(float x) const
-    {
-        return __builtin_fmaf(x * up, inv, 0x1.8p23f);
-    }
-    __device__ __forceinline__ float rest(float x, float t) const
-    {
-        return fabsf(__builtin_fmaf(-(t - 0x1.8p23f), step, x * up));
-    }
-    __device__ __forceinline__ bool near_half(float rest) const { return !(rest < 0.5f * step); }
-    // ... and what it is there
-    __device__ int exact(float x) const
-    {
-        const float v = fabsf(x) * up;
-        const float n = fminf(floorf(v * inv), 127.0f);
-        const float above = __builtin_fmaf(-(n + 0.5f), step, v);
-        int i = (int)n;
-        i += above > 0.0f || (above == 0.0f && (i & 1));
-        i = inv == 0.0f ? 0 : min(i, 127);
-        return x < 0.0f ? -i : i;
-    }
-    // The numbers of V elements
-    template <int V, typename F>
-    __device__ __forceinline__ Pack<signed char, V> numbers(F get) const
-    {
-        float t[V], most = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            t[v] = shifted(get(v));
-            most = fmaxf(most, rest(get(v), t[v]));
-        }
-        Pack<signed char, V> n;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            n.v[v] = (signed char)__builtin_bit_cast(int, t[v]);
-        if (near_half(most) || inv == 0.0f)
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                n.v[v] = (signed char)exact(get(v));
-        return n;
-    }
-};
 
 template <int WAVES> __device__ __forceinline__ unsigned row_max(unsigned m)
 {
@@ -92,14 +26,7 @@ template <int WAVES> __device__ __forceinline__ unsigned row_max(unsigned m)
     return m;
 }
 
-template <typename T> __device__ __forceinline__ unsigned magnitude(T v)
-{
-    return __builtin_bit_cast(unsigned, (float)v) & 0x7fffffffu;
-}
-
-// A row for each WAVES waves (a workgroup has 256 threads).  The largest magnitude
-// is found on bit patterns, which order NaN above infinity above the rest.  A row
-// of up to kKeep vectors a thread is read once and waits in registers; a longer
+// A row for each WAVES waves (a workgroup has 256 threads).  A row of up to kKeep vectors a thread is read once and waits in registers; a longer
 // one is read again, from the caches.
 constexpr int kKeep = 4;
 
@@ -114,25 +41,25 @@ __global__ __launch_bounds__(256) void k_quantize(QuantizeArgs a)
     signed char *q = a.q + (long long)m * a.ldq;
     const int whole = a.K / V;      // vectors
     Raw<T, V> kept[kKeep];
-    unsigned largest = 0;
+    Largest<T> all;
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        kept[j].clear();
+        if (at + j * lanes < whole)
+            kept[j].load(x + (at + j * lanes) * V);
+    }
 #pragma unroll
     for (int j = 0; j < kKeep; ++j)
-        if (at + j * lanes < whole) {
-            kept[j].load(x + (at + j * lanes) * V);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                largest = max(largest, magnitude(kept[j].get(v)));
-        }
+        all.look(kept[j]);
     for (int c = at + kKeep * lanes; c < whole; c += lanes) {
         Raw<T, V> r;
         r.load(x + (long long)c * V);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            largest = max(largest, magnitude(r.get(v)));
+        all.look(r);
     }
+    unsigned largest = all.get();
     const int tail = whole * V + at;        // fewer than V elements
     if (tail < a.K)
-        largest = max(largest, magnitude((float)x[tail]));
+        largest = max(largest, magnitude(x[tail]));
     const RowScale s(row_max<WAVES>(largest));
     auto put = [&](const Raw<T, V> &r, int c) {
         *reinterpret_cast<Pack<signed char, V> *>(q + (long long)c * V) =
@@ -191,7 +118,7 @@ int launch_quantize(const QuantizeArgs &a, void *stream)
 
 long long linear_i8_workspace(bool quantized, int M, int N, int K)
 {
-    if (M == 0)
+    if (M == 0 || (!quantized && few_rows_fit(M, K)))
         return 0;
     const Space s = space_of(quantized, M, N, K);
     return s.numbers + s.scales + s.sums;
@@ -200,7 +127,11 @@ long long linear_i8_workspace(bool quantized, int M, int N, int K)
 void linear_i8_describe(bool quantized, bool aligned, int M, int N, int K, const char **name,
                         int *splits)
 {
-    (void)quantized;
+    if (!quantized && few_rows_fit(M, K)) {
+        *splits = 1;
+        *name = "few_rows_quantized";
+        return;
+    }
     const GemmPlan plan = gemm_plan(1, 0, M, N, K);
     const bool direct = aligned && direct_ok(nullptr, 0, false, K, 1);
     *splits = split_count(K, plan.splits, 1);
@@ -212,6 +143,8 @@ int launch_linear_i8(const LinearI8Args &a, void *stream)
     if (a.M == 0)
         return DWCONV_OK;
     const bool quantized = a.x_scale != nullptr;
+    if (!quantized && few_rows_fit(a.M, a.K))
+        return launch_linear_few(a, stream);
     const Space s = space_of(quantized, a.M, a.N, a.K);
     char *space = static_cast<char *>(a.workspace);
     const void *x = a.x;

@@ -73,23 +73,25 @@ template <typename T, int V> struct Raw {
             __builtin_memcpy(w, &t, sizeof(t));
         }
     }
-    // through a buffer descriptor, `lane` plus `row` bytes from its start
+    // through a buffer descriptor, `lane` plus `row` bytes from its start; HINT: the
+    // instruction's cache bits
+    template <int HINT = 0>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, int lane, int row)
     {
         if constexpr (V * sizeof(T) == 2) {
-            w[0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, lane, row, 0);
+            w[0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, lane, row, HINT);
         } else if constexpr (words == 1) {
-            w[0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, lane, row, 0);
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, lane, row, HINT);
         } else if constexpr (words == 2) {
             *this = __builtin_bit_cast(Raw,
-                                       __builtin_amdgcn_raw_buffer_load_b64(rsrc, lane, row, 0));
+                                       __builtin_amdgcn_raw_buffer_load_b64(rsrc, lane, row, HINT));
         } else if constexpr (words == 4) {
             *this = __builtin_bit_cast(Raw,
-                                       __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, 0));
+                                       __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, HINT));
         } else {
             static_assert(words == 8);
-            const auto lo = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, 0);
-            const auto hi = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane + 16, row, 0);
+            const auto lo = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, row, HINT);
+            const auto hi = __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane + 16, row, HINT);
             __builtin_memcpy(w, &lo, 16);
             __builtin_memcpy(w + 4, &hi, 16);
         }
@@ -98,26 +100,27 @@ template <typename T, int V> struct Raw {
     // have read its registers at once and overwrites them in the next
     // instruction, which has been seen to change the last word of some lanes.
     // Without one it waits.
+    template <int HINT = 0>
     __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t rsrc, int lane, int row) const
     {
         typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
         typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
         if constexpr (V * sizeof(T) == 2) {
-            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)w[0], rsrc, lane, row, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)w[0], rsrc, lane, row, HINT);
         } else if constexpr (words == 1) {
-            __builtin_amdgcn_raw_buffer_store_b32(w[0], rsrc, lane, row, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(w[0], rsrc, lane, row, HINT);
         } else if constexpr (words == 2) {
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, *this), rsrc, lane, row,
-                                                  0);
+                                                  HINT);
         } else if constexpr (words == 4) {
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, *this), rsrc,
-                                                   lane + row, 0, 0);
+                                                   lane + row, 0, HINT);
         } else {
             static_assert(words == 8);
             __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, rsrc, lane + row,
-                                                   0, 0);
+                                                   0, HINT);
             __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[4], w[5], w[6], w[7]}, rsrc,
-                                                   lane + row + 16, 0, 0);
+                                                   lane + row + 16, 0, HINT);
         }
     }
     __device__ __forceinline__ float get(int v) const

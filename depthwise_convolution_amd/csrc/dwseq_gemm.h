@@ -477,7 +477,7 @@ template <int V, typename F> __device__ __forceinline__ void with_cut(int left, 
 // same in the wave).  The descriptor ends with the tile's last row, so that
 // rows beyond M are neither read (as zero) nor written; lanes beyond N are sent out
 // of bounds.  CUT: a vector that N cuts moves by element.
-template <typename E, int V, bool CUT> struct Block {
+template <typename E, int V, bool CUT, int HINT = 0> struct Block {
     static constexpr int size = (int)sizeof(E);
     const char *base;
     int ld, bytes, left;        // bytes of a row's stride and in all; columns to N
@@ -500,32 +500,32 @@ template <typename E, int V, bool CUT> struct Block {
     __device__ __forceinline__ void load(Raw<E, V> &v, int line, int row, int col) const
     {
         const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(base, bytes);
-        v.load(rsrc, at(line, col), row * ld);
+        v.template load<HINT>(rsrc, at(line, col), row * ld);
         if constexpr (CUT)
 #pragma unroll
             for (int e = 0; e < V - 1; ++e) {
                 Raw<E, 1> one;
-                one.load(rsrc, at(line, col, e), row * ld);
+                one.template load<HINT>(rsrc, at(line, col, e), row * ld);
                 v.w[e * size / 4] |= one.w[0] << (e * size % 4 * 8);
             }
     }
     __device__ __forceinline__ void store(const float (&s)[V], int line, int row, int col) const
     {
         const __amdgpu_buffer_rsrc_t rsrc = dwconv::make_rsrc(base, bytes);
-        Raw<E, V>(s).store(rsrc, at(line, col), row * ld);
+        Raw<E, V>(s).template store<HINT>(rsrc, at(line, col), row * ld);
         if constexpr (CUT)
 #pragma unroll
             for (int e = 0; e < V - 1; ++e) {
                 const float one[1] = {s[e]};
-                Raw<E, 1>(one).store(rsrc, at(line, col, e), row * ld);
+                Raw<E, 1>(one).template store<HINT>(rsrc, at(line, col, e), row * ld);
             }
     }
 };
 
 // V adjacent sums of a tile on their way to memory; b: their biases, r: residuals
-template <int ACT, typename T, int V, bool CUT>
-__device__ __forceinline__ void finish(const Finish &f, const Block<T, V, CUT> &z,
-                                       const Block<T, V, CUT> &y, const float (&b)[V],
+template <int ACT, typename T, int V, bool CUT, int HINT>
+__device__ __forceinline__ void finish(const Finish &f, const Block<T, V, CUT, HINT> &z,
+                                       const Block<T, V, CUT, HINT> &y, const float (&b)[V],
                                        const Raw<T, V> &r, float (&s)[V], int line, int row,
                                        int col)
 {
@@ -977,7 +977,9 @@ __global__ __launch_bounds__(512) void k_gemm_256(Product a, int tiles_m, int ti
     with_cut<8>(a.N - n0, 256, [&](auto c) {
         constexpr bool CUT = decltype(c)::value;
         using O = result_t<T>;
-        const Block<O, 8, CUT> from(a.f.res, a.f.ldres, m0, n0, 256, a.M, a.N),
+        // past the caches, for 8-bit integers: FIGURE
+        constexpr int kHint = sizeof(T) == 1 ? 2 : 0;
+        const Block<O, 8, CUT, kHint> from(a.f.res, a.f.ldres, m0, n0, 256, a.M, a.N),
             z(a.f.z, a.f.ldz, m0, n0, 256, a.M, a.N), y(a.f.y, a.f.ldy, m0, n0, 256, a.M, a.N);
         Raw<O, 8> res[kRows];
         auto fetch = [&](int hp) {
@@ -1096,6 +1098,26 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few_rows(Product a, int k_pe
 #pragma unroll
             for (int m = 0; m < MF; ++m)
                 mma<T>(fq[u], fp[u][m], acc[m]);
+    }
+    if constexpr (sizeof(T) == 1) {     // half as many bytes: ranges are often shorter than that
+        constexpr int kRest = 4;
+        for (; k < k1; k += kRest * step) {
+            u32x4 fq[kRest], fp[kRest][MF];
+#pragma unroll
+            for (int u = 0; u < kRest; ++u) {
+                const bool in = k + u * step < k1;
+                fq[u] = in ? chunk_of(q, k + u * step + g * elems, a.K) : u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+                    fp[u][m] = in ? chunk_of(p[m], k + u * step + g * elems, a.K)
+                                  : u32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int u = 0; u < kRest; ++u)
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+                    mma<T>(fq[u], fp[u][m], acc[m]);
+        }
     }
     for (; k < k1; k += step) {
         const u32x4 fq = chunk_of(q, k + g * elems, a.K);
