@@ -10,7 +10,9 @@
 //   each range of rows, the mean and the sum of squares around it; the ranges' are
 //   joined (counts, means, squares: no difference of large sums), and a second pass
 //   normalises, over the ranges in the opposite order, so that it begins with what
-//   the caches (256 MB before HBM) still hold.
+//   the caches (256 MB before HBM) still hold.  It reads and writes past them: results
+//   that wait there to be written would drive x out, and slow down who reads next (1 x
+//   512 x 512 x 256 float32: first pass 51 us for 77, second 81 for 84).
 //
 // Gradients need two sums over a group, sum(g) and sum(g * xhat), and per channel
 // sum(dz) and sum(dz * xhat), whose w-weighted sums over a group's channels are the
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs a, RowsPlan p)
             const int c = (at.lane + k * p.L) * V;
             r[j][k].clear();
             if (c < cg)
-                r[j][k].load(static_cast<const T *>(a.x) + row(j) * a.ldx + c0 + c);
+                r[j][k].load_past(static_cast<const T *>(a.x) + row(j) * a.ldx + c0 + c);
         }
     constexpr bool kEarly = K <= 2;     // w and b wait in registers
     float w[kEarly ? K : 1][V], b[kEarly ? K : 1][V];
@@ -188,7 +190,7 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs a, RowsPlan p)
                 z[v] = (r[j][k].get(v) - mean[j]) * rstd[j] * w[of][v] + b[of][v];
             act_all(z, a.act);
             if (c < cg && n0 + (long long)j * p.slots < a.N)
-                store<T, V>(static_cast<T *>(a.y) + row(j) * a.ldy + c0 + c, z);
+                Raw<T, V>(z).store_past(static_cast<T *>(a.y) + row(j) * a.ldy + c0 + c);
         }
     }
     if (a.stats && at.lane == 0)
@@ -452,12 +454,19 @@ __device__ __forceinline__ int join_lanes(int count)
 // and weigh nothing.
 template <typename T, int V, int B> struct Rows {
     Raw<T, V> v[B];
+    // LAST: for the last time
+    template <bool LAST>
     __device__ __forceinline__ void load(const T *x, long long ld, int r, const RangePlan &p,
                                          int rows)
     {
 #pragma unroll
-        for (int k = 0; k < B; ++k)
-            v[k].load(x + min(r + k * p.ty, rows - 1) * ld);
+        for (int k = 0; k < B; ++k) {
+            const T *from = x + min(r + k * p.ty, rows - 1) * ld;
+            if constexpr (LAST)
+                v[k].load_past(from);
+            else
+                v[k].load(from);
+        }
     }
 };
 
@@ -493,7 +502,7 @@ __global__ __launch_bounds__(256) void k_range_stats(NormArgs a, RangePlan p, fl
         const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + at.c;
         for (int r = at.y; r < at.rows; r += kAtOnce * p.ty) {
             Rows<T, V, kAtOnce> in;
-            in.load(x, a.ldx, r, p, at.rows);
+            in.template load<false>(x, a.ldx, r, p, at.rows);
             const int left = (at.rows - 1 - r) / p.ty + 1;
             const float n = (float)min(left, kAtOnce), one = 1.0f / n;
             const float all = count + n, part_of = n / all;
@@ -619,7 +628,7 @@ __global__ __launch_bounds__(256) void k_range_apply(NormArgs a, RangePlan p, co
     // the first rows are on their way while the ranges are joined
     const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + min(at.c, a.C - V);
     Rows<T, V, kAtOnce> in;
-    in.load(x, a.ldx, at.y, p, at.rows);
+    in.template load<true>(x, a.ldx, at.y, p, at.rows);
     if (stats) {
         for (int g = threadIdx.x; g < touched; g += 256)
             of[g] = stats[(long long)at.n * a.groups + g0 + g];
@@ -660,12 +669,12 @@ __global__ __launch_bounds__(256) void k_range_apply(NormArgs a, RangePlan p, co
                 z[e] = (in.v[k].get(e) - mean[e]) * f[e] + b[e];
             act_all(z, a.act);
             if (r + k * p.ty < at.rows)
-                store<T, V>(y + (r + k * p.ty) * a.ldy, z);
+                Raw<T, V>(z).store_past(y + (r + k * p.ty) * a.ldy);
         }
         r += kAtOnce * p.ty;
         if (r >= at.rows)
             return;
-        in.load(x, a.ldx, r, p, at.rows);
+        in.template load<true>(x, a.ldx, r, p, at.rows);
     }
 }
 
@@ -694,8 +703,8 @@ __global__ __launch_bounds__(256) void k_range_sums(NormArgs a, RangePlan p, flo
         constexpr int B = kAtOnce / 2;
         for (int r = at.y; r < at.rows; r += B * p.ty) {
             Rows<T, V, B> rx, rd;
-            rx.load(x, a.ldx, r, p, at.rows);
-            rd.load(dy, a.lddy, r, p, at.rows);
+            rx.template load<false>(x, a.ldx, r, p, at.rows);
+            rd.template load<false>(dy, a.lddy, r, p, at.rows);
 #pragma unroll
             for (int k = 0; k < B; ++k) {
                 float z[V], xhat[V];
@@ -799,8 +808,8 @@ __global__ __launch_bounds__(256) void k_range_dx(NormArgs a, RangePlan p, const
     const T *x = static_cast<const T *>(a.x) + at.row0 * a.ldx + min(at.c, a.C - V);
     const T *dy = static_cast<const T *>(a.dy) + at.row0 * a.lddy + min(at.c, a.C - V);
     Rows<T, V, B> rx, rd;
-    rx.load(x, a.ldx, at.y, p, at.rows);
-    rd.load(dy, a.lddy, at.y, p, at.rows);
+    rx.template load<true>(x, a.ldx, at.y, p, at.rows);
+    rd.template load<true>(dy, a.lddy, at.y, p, at.rows);
     {
         const int lanes = join_lanes(touched), lane = threadIdx.x % lanes;
         const float *dw = sums + (long long)at.n * 2 * a.C, *db = dw + a.C;
@@ -850,13 +859,13 @@ __global__ __launch_bounds__(256) void k_range_dx(NormArgs a, RangePlan p, const
             for (int e = 0; e < V; ++e)
                 z[e] = rstd[e] * (rd.v[k].get(e) * z[e] * w[e] - m1[e] - xhat[e] * m2[e]);
             if (r + k * p.ty < at.rows)
-                store<T, V>(dx + (r + k * p.ty) * a.lddx, z);
+                Raw<T, V>(z).store_past(dx + (r + k * p.ty) * a.lddx);
         }
         r += B * p.ty;
         if (r >= at.rows)
             return;
-        rx.load(x, a.ldx, r, p, at.rows);
-        rd.load(dy, a.lddy, r, p, at.rows);
+        rx.template load<true>(x, a.ldx, r, p, at.rows);
+        rd.template load<true>(dy, a.lddy, r, p, at.rows);
     }
 }
 

@@ -73,6 +73,31 @@ template <typename T, int V> struct Raw {
             __builtin_memcpy(w, &t, sizeof(t));
         }
     }
+    // past the caches: what is not read again, or written and not read soon
+    __device__ __forceinline__ void load_past(const T *p)
+    {
+        if constexpr (V * sizeof(T) == 2) {
+            w[0] = __builtin_nontemporal_load(reinterpret_cast<const unsigned short *>(p));
+        } else {
+            typedef unsigned words_t
+                __attribute__((ext_vector_type(words), aligned(sizeof(T))));
+            const words_t t = __builtin_nontemporal_load(reinterpret_cast<const words_t *>(p));
+            __builtin_memcpy(w, &t, sizeof(w));
+        }
+    }
+    __device__ __forceinline__ void store_past(T *p) const
+    {
+        if constexpr (V * sizeof(T) == 2) {
+            __builtin_nontemporal_store((unsigned short)w[0],
+                                        reinterpret_cast<unsigned short *>(p));
+        } else {
+            typedef unsigned words_t
+                __attribute__((ext_vector_type(words), aligned(sizeof(T))));
+            words_t t;
+            __builtin_memcpy(&t, w, sizeof(w));
+            __builtin_nontemporal_store(t, reinterpret_cast<words_t *>(p));
+        }
+    }
     // through a buffer descriptor, `lane` plus `row` bytes from its start; HINT: the
     // instruction's cache bits
     template <int HINT = 0>
