@@ -380,6 +380,12 @@ __device__ __forceinline__ float range_scale(float most, float lo, float hi, F f
     return __builtin_bit_cast(float, (unsigned)(127 - min(max(e, -120), 120)) << 23);
 }
 
+// 1 / v of such a power of two
+__device__ __forceinline__ float inverse(float v)
+{
+    return __builtin_bit_cast(float, 0x7f000000u - __builtin_bit_cast(unsigned, v));
+}
+
 __device__ __forceinline__ float finite_size(float v)
 {
     return fabsf(v) <= 3.4e38f ? fabsf(v) : 0.0f;
@@ -629,7 +635,7 @@ template <typename T, int DK, int DVT, int MT> struct Body {
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    S[t][m] *= 1.0f / up;
+                    S[t][m] *= inverse(up);
         if (any)
             for (int j = 0; j < C; ++j)
 #pragma unroll
@@ -783,7 +789,7 @@ template <typename T, int DK, int DVT, int MT> struct Body {
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
             const int n = max(t * 16 + i + 1 - late - first, 0);
-            const float f = s1 * pw[C - n] / down;
+            const float f = s1 * pw[C - n] * inverse(down);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 o[t][m] *= f;
@@ -819,7 +825,7 @@ template <typename T, int DK, int DVT, int MT> struct Body {
                             for (int q = 0; q < score_parts; ++q)
                                 mma<T>(f[ks][m], pf[q], o[t][m]);
                             if constexpr (scaled.value)
-                                o[t][m] *= 1.0f / down_of(t, ks);
+                                o[t][m] *= inverse(down_of(t, ks));
                         }
                     }
         };
@@ -841,7 +847,7 @@ template <typename T, int DK, int DVT, int MT> struct Body {
                 for (int t = 0; t < CT; ++t) {
                     const float s =
                         (float)*(__attribute__((address_space(3))) const T *)(
-                            p + (t * 16 + i) * pitch + slot * size) / down_of(t, j / span);
+                            p + (t * 16 + i) * pitch + slot * size) * inverse(down_of(t, j / span));
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
