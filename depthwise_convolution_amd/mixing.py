@@ -33,7 +33,8 @@ MIX_EXPORTS = ("dwconv_attention_workspace_size", "dwconv_attention_fwd", "dwcon
                "dwconv_linear_i8_describe", "dwconv_linear_i8")
 
 __all__ = ["linear_attention", "linear_attention_step", "linear_attention_grad",
-           "ATTENTION_MAX_DIM", "group_norm", "group_norm_grad", "quantize_rows", "linear_i8", "T_I8", "I8_MAX_K", "MIX_EXPORTS", *MIX_EXPORTS]
+           "ATTENTION_MAX_DIM", "group_norm", "group_norm_grad", "quantize_rows", "linear_i8",
+           "T_I8", "I8_MAX_K", "MIX_EXPORTS", *MIX_EXPORTS]
 
 
 def declare(L):

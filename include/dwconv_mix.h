@@ -31,10 +31,10 @@ extern "C" {
  * DWCONV_ATTENTION_MAX_DIM; row strides are below 2^21 elements.
  *
  * Tokens are taken in chunks.  For 16-bit types the scores q[i] . k[j] of a
- * chunk, times their decay, and the state that a chunk starts from are rounded
- * to `type` where they enter a product (the state itself is kept and passed on
- * in float32); float32 tensors are multiplied to float32 accuracy.  A token's
- * infinities and NaN reach the tokens after it, never those before it.
+ * chunk, times their decay, and the state that a chunk starts from enter a
+ * product as the sum of two numbers of `type` (the state itself is kept and
+ * passed on in float32); float32 tensors are multiplied to float32 accuracy.  A
+ * token's infinities and NaN reach the tokens after it, never those before it.
  * workspace: at least dwconv_attention_workspace_size(grad = 0) bytes, 16-byte
  * aligned (NULL where that is 0). */
 #define DWCONV_ATTENTION_MAX_DIM 256
@@ -111,12 +111,12 @@ int dwconv_norm_grad(const void *dy, long long lddy, const void *x, long long ld
 
 /* ---- matrix product in 8-bit integers ----------------------------------------
  *
- * Quantised rows: scale[m] = max_k |x[m,k]| * (1 / 127), the factor and the product
- * rounded to float32, and at least 2^-126; q[m,k] = x[m,k] / scale[m] rounded to the nearest integer, halves to
- * even, within -127 .. 127.  A row that holds an infinity or a NaN has the
- * scale NaN and numbers of 0, so that its products are NaN.  x is M rows of K
- * of a float `type`, q M rows of K int8 (ldq elements apart), scale [M]
- * float32.  M = 0 is allowed. */
+ * Quantised rows: scale[m] = max_k |x[m,k]| * (1 / 127), the factor and the
+ * product rounded to float32, and at least 2^-126; q[m,k] = x[m,k] / scale[m]
+ * rounded to the nearest integer, halves to even, within -127 .. 127.  A row
+ * that holds an infinity or a NaN has the scale NaN and numbers of 0, so that
+ * its products are NaN.  x is M rows of K of a float `type`, q M rows of K int8
+ * (ldq elements apart), scale [M] float32.  M = 0 is allowed. */
 #define DWCONV_T_I8 3
 
 int dwconv_quantize_rows(const void *x, long long ldx, int type, void *q, long long ldq,
@@ -143,7 +143,8 @@ int dwconv_linear_i8(const void *x, long long ldx, int xtype, const float *x_sca
 
 /* The kernel of such a product, as dwconv_linear_describe does: `quantized` is
  * whether x is given in int8, `aligned` whether the addresses and row strides of
- * w (and of x, if given in int8) are multiples of 16. */
+ * w (and of x, if given in int8) are multiples of 16.  A kernel that quantises x
+ * itself has "quantized" in its name. */
 int dwconv_linear_i8_describe(int quantized, int type, int aligned, long long M, int N, int K,
                               char *name, int name_len, int *splits);
 
