@@ -1076,7 +1076,9 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_sta
 
 // The segments' own states, each to be added to what it gets from those before it.  A
 // thread takes 4 adjacent elements (or one, where a state is no whole number of 4); the
-// segments of a sequence one after the other.
+// segments of a sequence one after the other.  (Workgroups of one wave: 1 x 65537 tokens,
+// 8 heads of 128, 18.3 us for 19.8, but gradients of 23 short sequences 15.9 for 13.8; 16
+// slots on their way instead of 4: 13.2 for 11.0 with 4 segments.)
 template <int V>
 __global__ __launch_bounds__(256) void k_link(Walks all, int blocks)
 {

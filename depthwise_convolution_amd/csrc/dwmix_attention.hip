@@ -92,25 +92,30 @@ struct Shared {
     int D, blocks;
 };
 
-template <typename T>
+template <typename T, int V>
 __global__ __launch_bounds__(256) void k_shared(Shared k, Shared v, int rows, int H, int KV)
 {
     const bool first = block_id() < (unsigned)k.blocks;
     const Shared &s = first ? k : v;
     if (!s.out)
         return;     // what the grid's last row has too many
-    const long long wide = (long long)KV * s.D;
+    const unsigned wide = (unsigned)(KV * s.D / V);
     const long long id =
         (long long)(block_id() - (first ? 0u : (unsigned)k.blocks)) * 256 + threadIdx.x;
     const long long row = id / wide;
     if (row >= rows)
         return;
-    const int at = (int)(id % wide), group = H / KV;
+    const int at = (int)(id - row * wide) * V, group = H / KV;
     const float *from = s.part + row * H * s.D + (long long)(at / s.D) * group * s.D + at % s.D;
-    float sum = from[0];
-    for (int g = 1; g < group; ++g)
-        sum += from[(long long)g * s.D];
-    static_cast<T *>(s.out)[row * s.ldo + at] = (T)sum;
+    float sum[V], more[V];
+    load<float, V>(from, sum);
+    for (int g = 1; g < group; ++g) {
+        load<float, V>(from + (long long)g * s.D, more);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            sum[e] += more[e];
+    }
+    store<T, V>(static_cast<T *>(s.out) + row * s.ldo + at, sum);
 }
 
 // -------------------------------------------------------------- planning
@@ -280,8 +285,9 @@ int launch_attention_grad(const AttentionArgs &a, void *stream)
     const int rc = walk(a.type, walks, count, st);
     if (rc != DWCONV_OK || (!dk.out && !dv.out) || a.batch.rows == 0)
         return rc;
+    const int vec = a.Dk % 4 == 0 && a.Dv % 4 == 0 ? 4 : 1;
     auto blocks_of = [&](const Shared &s) {
-        return s.out ? cdiv((long long)a.batch.rows * a.KV * s.D, 256) : 0;
+        return s.out ? cdiv((long long)a.batch.rows * a.KV * (s.D / vec), 256) : 0;
     };
     const long long total = blocks_of(dk) + blocks_of(dv);
     if (total > 0x7fffffffLL)
@@ -289,7 +295,8 @@ int launch_attention_grad(const AttentionArgs &a, void *stream)
     dk.blocks = (int)blocks_of(dk);
     dv.blocks = (int)blocks_of(dv);
     return with_type(a.type, [&](auto *t) {
-        return dwconv::launch_kernel(k_shared<std::remove_pointer_t<decltype(t)>>, grid_of(total),
+        using T = std::remove_pointer_t<decltype(t)>;
+        return dwconv::launch_kernel(vec == 4 ? k_shared<T, 4> : k_shared<T, 1>, grid_of(total),
                                      dim3(256), 0, st, dk, dv, a.batch.rows, a.H, a.KV);
     });
 }

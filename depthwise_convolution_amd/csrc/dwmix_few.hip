@@ -14,7 +14,7 @@ using namespace dwseq;
 // takes 16 NF columns; its 8 waves each take a range of k, as in the product of few rows
 // that are numbers already.  Every workgroup quantises all of x for itself, into LDS,
 // while its first rows of w are on their way: up to 64 elements a thread, about 2 us,
-// where a launch of its own took 4 us and a pause (8 x 8192 x 2048, in all: FIGURE).
+// where a launch of its own took 4 us and a pause (8 x 8192 x 2048: a call takes 12.5 us for 17).
 template <typename O, int NF> __global__ __launch_bounds__(512) void k_linear_few(LinearI8Args a)
 {
     typedef I8<O> T;

@@ -62,7 +62,7 @@ bool rows_plan(int size, long long N, long long P, int C, int groups, RowsPlan *
     p->slots = 256 / (L * p->gw);
     p->threads = (int)cdiv(L * p->gw * p->slots, 64) * 64;
     // Four vectors a lane in flight, which also share w and b, where that leaves two
-    // workgroups for every CU (16384 rows of 2048 bfloat16, 16 groups: FIGURE with 4
+    // workgroups for every CU (16384 rows of 2048 bfloat16, 16 groups: 31 us with 4
     // rows a team, 36.5 us with 1).
     p->R = std::max(1, 4 / p->K);
     if (cdiv(N, (long long)p->slots * p->R) * p->windows < 512)
