@@ -25,15 +25,21 @@
 //            then P V on top
 //   state    S = a^n S + K^T (V with its decays), the same columns
 //
-// so that LDS holds q, k, v and P (60 KB for widths of 128), a state never
+// so that LDS holds q, k, v and P (71 KB for widths of 128), a state never
 // leaves its registers, and two workgroups share a CU.
 //
-// Roundings of 16-bit types.  P and the chunk's S are rounded once where they become
-// operands, each by half a step of the type, as the output is afterwards: with
-// independent roundings the output's error grows from one rounding's to sqrt(2) of
-// it.  A second part would double the products.  V with its decays, which the
-// state is built from, is split into parts (three bfloat16, two float16) that hold
-// 22 bits and more: what is lost there would add up in the float32 state.
+// Roundings of 16-bit types.  P and the chunk's S become two numbers of the type each
+// where they are operands, 16 bits and more of them, so that the output's own rounding
+// is all that shows.  V with its decays, which the state is built from, is split into
+// parts (three bfloat16, two float16) that hold 22 bits and more: what is lost
+// there would add up in the float32 state.
+//
+// What bounds it (8 x 4096 tokens, 16 heads of 128 bfloat16: states 66 us, links 11,
+// walk 157): nothing alone.  In the walk the vector units are active 0.43 of the time,
+// LDS 0.39, the matrix cores 0.29, and its 268 MB would take 42 us; the three barriers of a
+// chunk keep these from overlapping more, at two workgroups a CU.  The states' pass reads
+// 3 of 4 segments, so that half of the CUs have two workgroups and half have one.
+//
 // float16 has too few exponents for scores and states: the values are scaled by a power
 // of two, one for each wave, where their largest would be too large or too small.
 #pragma once
@@ -1159,9 +1165,12 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
     const float whole = (float)exp((double)ld * B::C);
     Chunk c(n, B::C);
     u32x4 rq[B::QK::count], rk[B::QK::count], rv[B::VV::count];
-    B::QK::template fetch<MODE == ODD>(rq, q.at(c.t), ldq, w.back, c.first, w.Dk, b.thread);
-    B::QK::template fetch<MODE == ODD>(rk, k.at(c.t), ldk, w.back, c.first, w.Dk, b.thread);
-    B::VV::template fetch<MODE == ODD>(rv, v.at(c.t), ldv, w.back, c.first, wide, b.thread);
+    auto fetch = [&](const Chunk &x) {
+        B::QK::template fetch<MODE == ODD>(rq, q.at(x.t), ldq, w.back, x.first, w.Dk, b.thread);
+        B::QK::template fetch<MODE == ODD>(rk, k.at(x.t), ldk, w.back, x.first, w.Dk, b.thread);
+        B::VV::template fetch<MODE == ODD>(rv, v.at(x.t), ldv, w.back, x.first, wide, b.thread);
+    };
+    fetch(c);
     for (; c.any(); c = c.next()) {
         const Chunk next = c.next();
         b.next_chunk();
@@ -1169,9 +1178,12 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
         B::QK::keep(lk, rk, b.thread);
         B::VV::keep(lv, rv, b.thread);
         __syncthreads();
-        B::QK::template fetch<MODE == ODD>(rq, q.at(next.t), ldq, w.back, next.first, w.Dk, b.thread);
-        B::QK::template fetch<MODE == ODD>(rk, k.at(next.t), ldk, w.back, next.first, w.Dk, b.thread);
-        B::VV::template fetch<MODE == ODD>(rv, v.at(next.t), ldv, w.back, next.first, wide, b.thread);
+        // The next chunk's rows.  16-bit types send for them once scores and results are
+        // done: next to the parts of S there are no registers for them, and spilled, they
+        // are waited for at once (20011 tokens in 37 sequences, 12 heads of 96 and 80
+        // float16 138 us, so 106; bfloat16 takes either as long).
+        if constexpr (sizeof(T) == 4)
+            fetch(next);
         __builtin_amdgcn_sched_barrier(0);
         const float down = b.scores(lq, lk, lp, w.s0);
         if (B::is_f16 && b.lane == 0)
@@ -1197,6 +1209,8 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
                                               part.h, part.dv0);
         }
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (sizeof(T) == 2)
+            fetch(next);
         b.update(w, lk, lv, vf, any,
                  c.first == 0 ? whole : expf(ld * (float)(B::C - c.first)));
         if constexpr (MODE == ROWS)
