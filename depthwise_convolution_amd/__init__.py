@@ -20,8 +20,8 @@ allocated here; given ``pads`` or ``mult`` they use the general forms.
 
 The sequence operators (causal depthwise convolution over tokens, gated
 linear recurrence, matrix product with epilogue) are in ``sequence``, the
-mixing operators (matrix product in 8-bit integers) in ``mixing``; both are
-exported here.
+mixing operators (linear attention, group normalisation, matrix product in
+8-bit integers) in ``mixing``; both are exported here.
 
 Tensor shapes: NHWC tensors are ``(N, H, W, C)``, NCHW tensors
 ``(N, C, H, W)``; weights ``(mult*C, kH, kW)`` float32 or float16; bias

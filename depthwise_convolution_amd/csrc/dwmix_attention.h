@@ -35,8 +35,8 @@
 // there would add up in the float32 state.
 //
 // What bounds it (8 x 4096 tokens, 16 heads of 128 bfloat16: states 66 us, links 11,
-// walk 157): nothing alone.  In the walk the vector units are active 0.43 of the time,
-// LDS 0.39, the matrix cores 0.29, and its 268 MB would take 42 us; the three barriers of a
+// walk 155): nothing alone.  In the walk the vector units are active 0.54 of the time,
+// LDS 0.45, the matrix cores 0.31, and its 268 MB would take 42 us; the three barriers of a
 // chunk keep these from overlapping more, at two workgroups a CU.  The states' pass reads
 // 3 of 4 segments, so that half of the CUs have two workgroups and half have one.
 //
