@@ -48,6 +48,8 @@
 #include "dwseq_device.h"
 #include "../../include/dwconv_mix.h"
 
+#include <algorithm>
+
 namespace dwmix {
 
 // One walk.
@@ -1280,9 +1282,7 @@ struct Gather {
     // f(grid) launches; the last walk's number of workgroups is not looked at
     template <typename F> int launch(F f) const
     {
-        if (count == 0)
-            return DWCONV_OK;
-        return total > 0x7fffffffLL - kGridRow ? (int)DWCONV_ERR_BAD_DIM : f(grid_of(total));
+        return count == 0 ? (int)DWCONV_OK : f(grid_of(total));
     }
 };
 
@@ -1310,6 +1310,14 @@ int for_kinds(const Walk *w, int count, W wanted, K kind, F launch)
 template <typename T> int launch_walks(const Walk *w, int count, hipStream_t st)
 {
     auto cut = [](const Walk &x) { return x.slots && !x.ready; };
+    long long most = 0;     // no launch before all are known to fit
+    for (int i = 0; i < count; ++i) {
+        const long long walk = (long long)w[i].items * w[i].H * cdiv(w[i].Dv, 64);
+        const long long link = (long long)w[i].batch.seqs * w[i].H * cdiv(w[i].Dk * w[i].Dv, 256);
+        most += std::max(walk, cut(w[i]) ? link : 0) + 8;
+    }
+    if (most > 0x7fffffffLL - kGridRow)
+        return DWCONV_ERR_BAD_DIM;
     int rc = for_kinds(
         w, count, cut,
         [](const Walk &x) {         // states have no results

@@ -232,3 +232,11 @@ def test_stream_of_another_device():
                  lambda: dw.linear_i8(x, w, x, stream=other)):
         with pytest.raises(ValueError, match="stream is on cuda:1"):
             call()
+
+
+def test_attention_refuses_more_workgroups_than_a_grid_holds(L):
+    """Before anything is enqueued: 2^29 sequences of one token, 4 heads."""
+    d = dict(q=1 << 44, ldq=4, k=2 << 44, ldk=2, v=3 << 44, ldv=2, type=0, g=B, scale=1.0,
+             h0=None, y=4 << 44, ldy=4, hT=None, ws=None, wsb=0, seqs=1 << 29, tokens=1,
+             offsets=None, H=4, KV=2, Dk=1, Dv=1, stream=None)
+    _refuses(L, "dwconv_attention_fwd", d, [({}, "BAD_DIM")])
