@@ -1051,8 +1051,10 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_sta
     Chunk c(n, B::C);
     u32x4 rk[2][B::QK::count], rv[2][B::VV::count];
     auto fetch = [&](auto p, const Chunk &x) {
-        B::QK::template fetch<MODE == ODD>(rk[p.value], k.at(x.t), ldk, w.back, x.first, w.Dk, b.thread);
-        B::VV::template fetch<MODE == ODD>(rv[p.value], v.at(x.t), ldv, w.back, x.first, wide, b.thread);
+        B::QK::template fetch<MODE == ODD>(rk[p.value], k.at(x.t), ldk, w.back, x.first, w.Dk,
+                                           b.thread);
+        B::VV::template fetch<MODE == ODD>(rv[p.value], v.at(x.t), ldv, w.back, x.first, wide,
+                                           b.thread);
     };
     auto step = [&](auto p) {
         b.next_chunk();

@@ -14,12 +14,14 @@ using namespace dwseq;
 // takes 16 NF columns; its 8 waves each take a range of k, as in the product of few rows
 // that are numbers already.  Every workgroup quantises all of x for itself, into LDS,
 // while its first rows of w are on their way: up to 64 elements a thread, about 2 us,
-// where a launch of its own took 4 us and a pause (8 x 8192 x 2048: a call takes 12.5 us for 17).
+// where a launch of its own took 4 us and a pause (8 x 8192 x 2048: a call takes 12.5
+// us for 17).
 template <typename O, int NF> __global__ __launch_bounds__(512) void k_linear_few(LinearI8Args a)
 {
     typedef I8<O> T;
     constexpr int V = 16 / (int)sizeof(O), kWaves = 8, step = 64, kAhead = 8 / NF;
-    extern __shared__ __attribute__((aligned(16))) signed char numbers[];   // [M][pitch]
+    // [M][pitch]
+    extern __shared__ __attribute__((aligned(16))) signed char numbers[];
     __shared__ f32x4 sums[kWaves][NF][64];
     __shared__ float scales[16];
     __shared__ unsigned tops[kWaves];

