@@ -59,9 +59,10 @@ __global__ __launch_bounds__(256) void k_quantize(QuantizeArgs a)
         all.look(r);
     }
     unsigned largest = all.get();
-    const int tail = whole * V + at;        // fewer than V elements
-    if (tail < a.K)
-        largest = max(largest, magnitude(x[tail]));
+    const int tail = whole * V;     // fewer than V elements from there on
+    const bool ends = at < a.K - tail;
+    if (ends)
+        largest = max(largest, magnitude(x[tail + at]));
     const RowScale s(row_max<WAVES>(largest));
     auto put = [&](const Raw<T, V> &r, int c) {
         *reinterpret_cast<Pack<signed char, V> *>(q + (long long)c * V) =
@@ -76,8 +77,8 @@ __global__ __launch_bounds__(256) void k_quantize(QuantizeArgs a)
         r.load(x + (long long)c * V);
         put(r, c);
     }
-    if (tail < a.K)
-        q[tail] = (signed char)s.exact((float)x[tail]);
+    if (ends)
+        q[tail + at] = (signed char)s.exact((float)x[tail + at]);
     if (at == 0)
         a.scale[m] = s.scale;
 }
