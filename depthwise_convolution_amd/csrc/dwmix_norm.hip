@@ -383,6 +383,7 @@ int launch_columns(const float *part, long long rows, int C, float *space, float
 // channels (whatever the groups): tx vectors, ty rows at a time.
 struct RangePlan {
     int V, tx, ty, cols, chunk, chunks; // column blocks; rows of a range, ranges
+    int span;                           // column blocks that a group lies in, at most
     bool joined;                        // the second pass joins the ranges by itself
     long long total;                    // workgroups
 };
@@ -392,7 +393,7 @@ constexpr int kJoin = 64;       // ranges that each workgroup of the second pass
 
 // Ranges are whole batches of all threads (32 KB of x in 16-byte vectors), as many as
 // make 2048 workgroups at most.
-RangePlan range_plan(int size, bool grad, long long N, long long P, int C)
+RangePlan range_plan(int size, bool grad, long long N, long long P, int C, int groups)
 {
     RangePlan p;
     p.V = 16 / size;
@@ -402,6 +403,8 @@ RangePlan range_plan(int size, bool grad, long long N, long long P, int C)
     p.tx = std::min(vectors, 256);
     p.ty = 256 / p.tx;
     p.cols = (int)cdiv(vectors, 256);
+    const int cg = C / groups, block = 256 * p.V;
+    p.span = block % cg == 0 ? 1 : std::min(p.cols, (cg - 1) / block + 2);
     const long long unit = (long long)kAtOnce * p.ty;
     long long chunks = std::max(1LL, cdiv(2048, std::max(1LL, N * p.cols)));
     chunks = std::min(chunks, cdiv(P, unit));
@@ -555,8 +558,8 @@ __global__ __launch_bounds__(256) void k_range_stats(NormArgs a, RangePlan p, fl
         for (int d = 1; d < lanes; d *= 2)
             q += __shfl_xor(q, d);
         if (lane == 0)
-            part[(((long long)at.n * a.groups + g) * p.chunks + at.chunk) * p.cols + at.col] =
-                make_float2(joint, q);
+            part[(((long long)at.n * a.groups + g) * p.chunks + at.chunk) * p.span + at.col -
+                 g * cg / (256 * p.V)] = make_float2(joint, q);
     }
 }
 
@@ -566,7 +569,7 @@ __device__ __forceinline__ Moments join(const NormArgs &a, const RangePlan &p,
 {
     const int cg = a.C / a.groups, block = 256 * p.V;
     const int col0 = g * cg / block, cols = ((g + 1) * cg - 1) / block - col0 + 1;
-    const float2 *from = part + ((long long)n * a.groups + g) * p.chunks * p.cols + col0;
+    const float2 *from = part + ((long long)n * a.groups + g) * p.chunks * p.span;
     const int items = p.chunks * cols;
     Moments sum{};
     for (int i = lane; i < items; i += 8 * lanes) {
@@ -579,7 +582,7 @@ __device__ __forceinline__ Moments join(const NormArgs &a, const RangePlan &p,
             const long long rows = min((long long)p.chunk, a.P - (long long)chunk * p.chunk);
             const int wide = min((g + 1) * cg, (col + 1) * block) - max(g * cg, col * block);
             count[k] = i + k * lanes < items ? (float)rows * (float)wide : 0.0f;
-            v[k] = from[(long long)chunk * p.cols + c];
+            v[k] = from[(long long)chunk * p.span + c];
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -886,9 +889,9 @@ Space space_of(bool grad, int size, long long N, long long P, int C, int groups)
         if (grad)
             s.part = round16(8LL * rows.blocks * C);
     } else {
-        const RangePlan p = range_plan(size, grad, N, P, C);
+        const RangePlan p = range_plan(size, grad, N, P, C, groups);
         if (!grad) {
-            s.part = round16(8LL * N * p.chunks * p.cols * groups);
+            s.part = round16(8LL * N * p.chunks * p.span * groups);
             s.sums = p.joined ? 0 : round16(8LL * N * groups);
         } else {
             s.part = round16(8LL * N * p.chunks * C);
@@ -956,7 +959,7 @@ int launch_norm_fwd(const NormArgs &a, void *stream)
             });
         });
     }
-    const RangePlan p = range_plan(size, false, a.N, a.P, a.C);
+    const RangePlan p = range_plan(size, false, a.N, a.P, a.C, a.groups);
     if (p.total > kMostBlocks)
         return DWCONV_ERR_BAD_DIM;
     const Space s = space_of(false, size, a.N, a.P, a.C, a.groups);
@@ -1012,7 +1015,7 @@ int launch_norm_grad(const NormArgs &a, void *stream)
             return rc;
         return launch_columns(part, rows.blocks, a.C, strips, a.dw, a.db, st);
     }
-    const RangePlan p = range_plan(size, true, a.N, a.P, a.C);
+    const RangePlan p = range_plan(size, true, a.N, a.P, a.C, a.groups);
     if (p.total > kMostBlocks - a.C)
         return DWCONV_ERR_BAD_DIM;
     float *sums = p.chunks > 1 ? reinterpret_cast<float *>(space + s.part) : part;
