@@ -752,24 +752,25 @@ __global__ __launch_bounds__(1024) void k_range_fold(const float *part, int chun
                                                      long long N, float *sums)
 {
     __shared__ float lds[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wide = (2 * C + 63) / 64;
-    const long long n = block_id() / wide;
-    const int col = (int)(block_id() % wide) * 64 + lane;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long long wide = 2LL * C;
+    const unsigned blocks = (unsigned)((wide + 63) / 64);
+    const long long n = block_id() / blocks, col = (long long)(block_id() % blocks) * 64 + lane;
     if (n >= N)
         return;
-    const float *from = part + n * chunks * 2 * C + col;
+    const float *from = part + n * chunks * wide + col;
     float s = 0.0f;
-    if (col < 2 * C)
+    if (col < wide)
 #pragma unroll 4
         for (int k = wave; k < chunks; k += 16)
-            s += from[(long long)k * 2 * C];
+            s += from[k * wide];
     lds[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && col < 2 * C) {
+    if (wave == 0 && col < wide) {
 #pragma unroll
         for (int k = 1; k < 16; ++k)
             s += lds[k][lane];
-        sums[n * 2 * C + col] = s;
+        sums[n * wide + col] = s;
     }
 }
 
@@ -779,17 +780,17 @@ constexpr int kInstances = 64;
 __device__ __forceinline__ void add_instances(const NormArgs &a, const float *sums, int block,
                                               float *lds)
 {
-    const long long col = block * 64LL + (threadIdx.x & 63);
+    const long long col = block * 64LL + (threadIdx.x & 63), wide = 2LL * a.C;
     const int wave = threadIdx.x >> 6;
     float s = 0.0f;
-    if (col < 2 * a.C)
+    if (col < wide)
 #pragma unroll 4
         for (int n = wave; n < a.N; n += 4)
-            s += sums[n * 2LL * a.C + col];
+            s += sums[n * wide + col];
     lds[threadIdx.x] = s;
     __syncthreads();
     float *to = col < a.C ? a.dw : a.db;
-    if (wave == 0 && col < 2 * a.C && to)
+    if (wave == 0 && col < wide && to)
         to[col < a.C ? col : col - a.C] =
             ((lds[threadIdx.x] + lds[threadIdx.x + 64]) + lds[threadIdx.x + 128]) +
             lds[threadIdx.x + 192];
