@@ -1017,12 +1017,12 @@ int launch_norm_grad(const NormArgs &a, void *stream)
         return launch_columns(part, rows.blocks, a.C, strips, a.dw, a.db, st);
     }
     const RangePlan p = range_plan(size, true, a.N, a.P, a.C, a.groups);
-    if (p.total > kMostBlocks - a.C)
-        return DWCONV_ERR_BAD_DIM;
     float *sums = p.chunks > 1 ? reinterpret_cast<float *>(space + s.part) : part;
     // up to kInstances of them are added up beside dx, more by launches of their own
     const bool beside = a.dx && (a.dw || a.db) && a.N <= kInstances;
     const long long extra = beside ? cdiv(2LL * a.C, 64) : 0;
+    if (p.total + extra > kMostBlocks)
+        return DWCONV_ERR_BAD_DIM;
     int rc = with_type(a.type, [&](auto *t) {
         using T = std::remove_pointer_t<decltype(t)>;
         return with_width<T>(p.V, [&](auto v) {

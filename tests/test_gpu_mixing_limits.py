@@ -70,3 +70,9 @@ def _norm_of_wide_rows(torch, P, C):
 def test_norm_of_more_than_2_30_channels(torch, P):
     """The 2 C sums of a gradient are more than 2^31."""
     _norm_of_wide_rows(torch, P, (1 << 30) + 128)
+
+
+@pytest.mark.parametrize("P", [1, 2])
+def test_norm_of_the_most_channels(torch, P):
+    """A gradient takes as many workgroups as it needs, and not one for each channel."""
+    _norm_of_wide_rows(torch, P, dw.SEQ_MAX_ROWS)
