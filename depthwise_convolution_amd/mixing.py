@@ -18,7 +18,7 @@ gives; the header states the formulas; calls are asynchronous on ``stream``
 import ctypes
 
 from . import sequence as _seq
-from .sequence import (_act, _dense, _gpu, _needed, _rows, _size, _space, _start, _status,
+from .sequence import (_act, _dense, _fits, _gpu, _needed, _rows, _size, _space, _start, _status,
                        _workspace)
 
 T_I8 = 3                     # DWCONV_T_I8
@@ -118,7 +118,10 @@ def _heads(q, k, v, lead):
         raise ValueError("v must be (..., KV heads, Dv) with k's tokens and heads")
     if KV < 1 or H % KV:
         raise ValueError(f"{KV} heads of k and v do not divide the {H} heads of q")
-    return H, KV, Dk, v.shape[-1]
+    Dv = v.shape[-1]
+    if Dv > _seq._INT_MAX:
+        _fits(v, "v")
+    return H, KV, Dk, Dv
 
 
 def _sequences(q, offsets):
@@ -267,6 +270,8 @@ def _instances(x, groups):
     C = x.shape[-1]
     if isinstance(groups, bool) or not isinstance(groups, int):
         raise TypeError("groups must be an int")
+    if abs(groups) > _seq._INT_MAX:
+        raise ValueError(f"{groups} groups of {C} channels")
     P = 1
     for size in x.shape[1:-1]:
         P *= size
@@ -428,7 +433,10 @@ def _map(x, w):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() < 1 or w.dim() != 2 or w.shape[1] != x.shape[-1]:
         raise ValueError("w must be (N, K) with K the last axis of x")
-    return w.shape
+    N, K = w.shape
+    if N > _seq._INT_MAX:
+        _fits(w, "w")
+    return N, K
 
 
 def linear_i8(x, w, w_scale, b=None, act="none", res=None, x_scale=None, dtype=None, stream=None):

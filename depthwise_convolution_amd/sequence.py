@@ -33,6 +33,7 @@ T_F32, T_F16, T_BF16 = 0, 1, 2
 CAUSAL_MAX_TAPS = 8          # DWCONV_CAUSAL_MAX_TAPS
 SEQ_MAX_ROWS = (1 << 31) - (1 << 16)         # DWCONV_SEQ_MAX_ROWS
 SCAN_RUN = 8                # DWCONV_SCAN_RUN
+_INT_MAX = (1 << 31) - 1     # ctypes passes a larger number on as its low 32 bits
 LINEAR_Y, LINEAR_DX, LINEAR_DW = 0, 1, 2     # DWCONV_LINEAR_*
 
 SEQ_EXPORTS = ("dwconv_causal_fwd", "dwconv_causal_step", "dwconv_causal_grad_workspace_size",
@@ -126,6 +127,9 @@ def _start(x, stream, name="x"):
         raise TypeError(f"{name} has dtype {x.dtype}, expected float32, float16 or bfloat16")
     if type(stream) is _Handle:
         return code, stream, None
+    size = x.numel()
+    if size > _INT_MAX or size == 0:
+        _fits(x, name)
     index = x.get_device()
     if stream is None:
         handle = _Handle(_raw_stream(index))
@@ -136,6 +140,11 @@ def _start(x, stream, name="x"):
     elif getattr(stream, "device", x.device) != x.device:
         raise ValueError(f"stream is on {stream.device}, {name} on {x.device}")
     return code, _Handle(stream.cuda_stream), torch.cuda.stream(stream)
+
+
+def _fits(t, name):
+    if any(n > _INT_MAX for n in t.shape):
+        raise ValueError(f"{name} has an axis of 2^31 or more elements")
 
 
 def _gpu(t, name, x):
@@ -208,7 +217,10 @@ def _batch(x, offsets):
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 \
             or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 tensor of sequences + 1 numbers")
-    return offsets.numel() - 1, x.shape[0], offsets.data_ptr()
+    seqs = offsets.numel() - 1
+    if seqs > _INT_MAX:
+        _fits(offsets, "offsets")
+    return seqs, x.shape[0], offsets.data_ptr()
 
 
 def _tokens(x):
@@ -225,7 +237,10 @@ def _filter(w, x):
         raise TypeError(f"w has dtype {w.dtype}, expected float32, float16 or bfloat16")
     if w.dim() != 2 or w.shape[0] != x.shape[-1] or not w.is_contiguous():
         raise ValueError("w must be a contiguous (C, taps) tensor")
-    return w.data_ptr(), code, w.shape[1]
+    taps = w.shape[1]
+    if taps > _INT_MAX:
+        _fits(w, "w")
+    return w.data_ptr(), code, taps
 
 
 def _weights(w, x):
@@ -233,7 +248,10 @@ def _weights(w, x):
     pw, ldw = _rows(w, "w", x)
     if w.dim() != 2 or w.shape[1] != x.shape[-1]:
         raise ValueError("w must be (N, K) with K the last axis of x")
-    return pw, ldw, w.shape[0], w.shape[1]
+    N, K = w.shape
+    if N > _INT_MAX:
+        _fits(w, "w")
+    return pw, ldw, N, K
 
 
 def _status(st, what):
