@@ -1,0 +1,68 @@
+"""Linear attention where nothing but the store of a result rounds (tests/mixing_exact.py):
+every result equal to the exact one, rounded once."""
+import numpy as np
+import pytest
+
+import depthwise_convolution_amd as dw
+
+from . import mixing_exact as exact
+from . import mixing_reference as ref
+from .sequence_reference import bounds_of
+from .test_gpu_mixing import DTYPES, _back, _gpu, _near, _offsets, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _same(got, want, dtype, what):
+    got, want = _back(got).reshape(want.shape), exact.rounded(want, dtype)
+    bad = got != want
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} differ, first at "
+                           f"{np.argwhere(bad)[0].tolist()}: {got[bad][0]} for {want[bad][0]}")
+
+
+CASES = [
+    # (lengths, H, KV, Dk, Dv): chunks that are whole and cut, segments, shared heads, odd widths
+    ([64], 1, 1, 64, 64), ([1, 0, 63, 200], 2, 1, 64, 64), ([300], 2, 2, 40, 24),
+    ([130, 67], 2, 2, 33, 17), ([150], 1, 1, 128, 128), ([90, 40], 1, 1, 160, 72),
+    ([300], 4, 2, 16, 80),
+]
+
+
+def _inputs(torch, case, dtype):     # noqa: F811
+    lengths, H, KV, Dk, Dv = case
+    rng = np.random.default_rng(len(lengths) * 1000 + Dk)
+    rows, S = sum(lengths), len(lengths)
+    r = dict(q=exact.whole(rng, (rows, H, Dk), 15), k=exact.whole(rng, (rows, KV, Dk), 15),
+             v=exact.whole(rng, (rows, KV, Dv), 7), dy=exact.whole(rng, (rows, H, Dv), 15),
+             h0=exact.whole(rng, (S, H, Dk, Dv), 4000),
+             dhT=exact.whole(rng, (S, H, Dk, Dv), 4000, 2.0 ** -6))
+    g = {n: _gpu(torch, t, "float32" if n in ("h0", "dhT") else dtype) for n, t in r.items()}
+    for n in r:
+        assert np.array_equal(_back(g[n]), r[n])
+    logs = np.array([0.0, -np.inf, 0.0, 0.0][:H])
+    g["log_decay"], g["off"] = _gpu(torch, logs), _gpu(torch, _offsets(lengths), "int32")
+    return g, r, logs, bounds_of(_offsets(lengths))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_nothing_is_lost(torch, case, dtype):    # noqa: F811
+    """The forward and every gradient, heads that forget nothing and all."""
+    print(f"\n[case] exact attention {CASES[case]} {dtype}", flush=True)
+    g, r, logs, bounds = _inputs(torch, CASES[case], dtype)
+    scale = 2.0 ** -6
+    args = r["q"], r["k"], r["v"]
+    top = exact.majorants(*args, r["dy"], logs, scale, bounds, r["h0"], r["dhT"])
+    for name, t in top.items():         # all sums are whole numbers of 2^-6 (hT: of 1)
+        assert t.max(initial=0.0) < 2.0 ** (24 if name == "hT" else 18), name
+    y, hT = dw.linear_attention(g["q"], g["k"], g["v"], g["log_decay"], h0=g["h0"],
+                                offsets=g["off"], scale=scale)
+    grads = dw.linear_attention_grad(g["dy"], g["q"], g["k"], g["v"], g["log_decay"], h0=g["h0"],
+                                     dhT=g["dhT"], offsets=g["off"], scale=scale)
+    torch.cuda.synchronize()
+    want, state = ref.attention(*args, logs, scale, bounds, r["h0"])
+    _same(y, want, dtype, "y")
+    _same(hT, state, "float32", "hT")
+    want = ref.attention_grad(r["dy"], *args, logs, scale, bounds, r["h0"], r["dhT"])
+    for name, t in zip(("dq", "dk", "dv", "dh0"), grads):
+        _same(t, want[name], "float32" if name == "dh0" else dtype, name)
