@@ -372,10 +372,10 @@ __device__ __forceinline__ float wave_max(float m)
     return m;
 }
 
-// The power of two that brings the largest finite size of a wave's numbers to [1, 2),
-// or 1 while it lies between lo and hi (float16: where its numbers are normal and far
-// from their end), which takes two votes.  `most`: a lane's largest size; finite():
-// its largest finite one.
+// The power of two that brings the largest finite size of a wave's numbers to [1, 2)
+// where it is below lo, and to [2^13, 2^14) where it is above hi = 2^14 (which leaves the
+// small ones beside it as many bits as float16 has); 1 between the two, which takes two
+// votes.  `most`: a lane's largest size; finite(): its largest finite one.
 template <typename F>
 __device__ __forceinline__ float range_scale(float most, float lo, float hi, F finite)
 {
@@ -385,7 +385,7 @@ __device__ __forceinline__ float range_scale(float most, float lo, float hi, F f
     if (!(m > 0.0f) || (m >= lo && m <= hi))
         return 1.0f;
     const int e = (int)((__builtin_bit_cast(unsigned, m) >> 23) & 255) - 127;
-    return __builtin_bit_cast(float, (unsigned)(127 - min(max(e, -120), 120)) << 23);
+    return __builtin_bit_cast(float, (unsigned)(127 + min((m > hi ? 13 : 0) - e, 120)) << 23);
 }
 
 // 1 / v of such a power of two

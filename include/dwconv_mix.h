@@ -33,8 +33,12 @@ extern "C" {
  * Tokens are taken in chunks.  For 16-bit types the scores q[i] . k[j] of a
  * chunk, times their decay, and the state that a chunk starts from enter a
  * product as the sum of two numbers of `type` (the state itself is kept and
- * passed on in float32); float32 tensors are multiplied to float32 accuracy.  A
- * token's infinities and NaN reach the tokens after it, never those before it.
+ * passed on in float32); float32 tensors are multiplied to float32 accuracy.
+ * What float16 has too few exponents for is scaled by a power of two, 16 columns of
+ * the values or of the state and 16 rows of scores by one: besides the two numbers'
+ * 2^-22 of itself, a number then loses at most 2^-25 while the largest of those beside
+ * it is below 2^14, and 2^-38 of that one where it is above.
+ * A token's infinities and NaN reach the tokens after it, never those before it.
  * workspace: at least dwconv_attention_workspace_size(grad = 0) bytes, 16-byte
  * aligned (NULL where that is 0). */
 #define DWCONV_ATTENTION_MAX_DIM 256

@@ -66,3 +66,35 @@ def test_nothing_is_lost(torch, case, dtype):    # noqa: F811
     want = ref.attention_grad(r["dy"], *args, logs, scale, bounds, r["h0"], r["dhT"])
     for name, t in zip(("dq", "dk", "dv", "dh0"), grads):
         _same(t, want[name], "float32" if name == "dh0" else dtype, name)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("large", [20000.0, 60000.0])
+def test_large_float16_values_leave_their_neighbours_exact(torch, large, D):    # noqa: F811
+    """One value above 2^14 among columns around 2^-7: their states, and what later tokens
+    read of them, keep every bit; and scores above 2^14 among small ones."""
+    rng = np.random.default_rng(5)
+    n = 200
+    q, k = (exact.whole(rng, (n, 1, D), 15) for _ in range(2))
+    v = exact.whole(rng, (n, 1, D), 7, 2.0 ** -10)
+    v[5, 0, 3] = v[100, 0, D - 1] = large
+    g, off, scale = np.zeros(1), [(0, n)], 2.0 ** -10
+    want, state = ref.attention(q, k, v, g, scale, off, None)
+    small = [c for c in range(D) if c not in (3, D - 1)]
+    big, bs = ref.attention(*(np.abs(t) for t in (q, k, v)), g, scale, off, None)
+    # whole numbers of 2^-20 and of 2^-10
+    assert big[:, :, small].max() < 2.0 ** 4 and bs[:, :, :, small].max() < 2.0 ** 14
+    args = [_gpu(torch, t[None], "float16") for t in (q, k, v)]
+    y, hT = dw.linear_attention(*args, _gpu(torch, g), scale=scale)
+    _same(hT[..., small], state[..., small], "float32", "hT")
+    # the large ones themselves pass 2^18, with steps of 2^-10: 28 bits, of which float32
+    # holds 24, so that each sum may round
+    _near(hT, state, ref.attention_tol(bs, 0, n, "float32", 0.0, True), "all of hT")
+    _same(y[..., small], want[..., small], "float16", "y")
+    # scores: one query of 2^13 times the others
+    q[70] *= 2.0 ** 10
+    v[5, 0, 3] = v[100, 0, D - 1] = 0.0
+    want, _ = ref.attention(q, k, v, g, scale * 2.0 ** 6, off, None)
+    args = [_gpu(torch, t[None], "float16") for t in (q, k, v)]
+    y, _ = dw.linear_attention(*args, _gpu(torch, g), scale=scale * 2.0 ** 6)
+    _same(y, want, "float16", "y of large scores")
