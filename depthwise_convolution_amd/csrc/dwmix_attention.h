@@ -375,9 +375,11 @@ __device__ __forceinline__ float wave_max(float m)
 // The power of two that brings the largest finite size of a wave's numbers to [1, 2)
 // where it is below lo, and to [2^13, 2^14) where it is above hi = 2^14 (which leaves the
 // small ones beside it as many bits as float16 has); 1 between the two, which takes two
-// votes.  `most`: a lane's largest size; finite(): its largest finite one.
+// votes.  `most`: a lane's largest size; finite(): its largest finite one; `up`: 2^up is
+// the largest such power.
 template <typename F>
-__device__ __forceinline__ float range_scale(float most, float lo, float hi, F finite)
+__device__ __forceinline__ float range_scale(float most, float lo, float hi, F finite,
+                                             int up = 120)
 {
     if (!__any(most > hi) && __any(most >= lo))
         return 1.0f;
@@ -385,7 +387,15 @@ __device__ __forceinline__ float range_scale(float most, float lo, float hi, F f
     if (!(m > 0.0f) || (m >= lo && m <= hi))
         return 1.0f;
     const int e = (int)((__builtin_bit_cast(unsigned, m) >> 23) & 255) - 127;
-    return __builtin_bit_cast(float, (unsigned)(127 + min((m > hi ? 13 : 0) - e, 120)) << 23);
+    return __builtin_bit_cast(float, (unsigned)(127 + min((m > hi ? 13 : 0) - e, up)) << 23);
+}
+
+// The largest power of two, 1 at least, that leaves a wave's numbers below 2^100 in size
+// (`most`: a lane's largest finite one).
+__device__ __forceinline__ float room_above(float most)
+{
+    const int e = (int)(__builtin_bit_cast(unsigned, wave_max(most)) >> 23) - 127;
+    return __builtin_bit_cast(float, (unsigned)(127 + min(max(99 - e, 0), 120)) << 23);
 }
 
 // 1 / v of such a power of two
@@ -416,6 +426,9 @@ template <typename T, int DK, int DVT, int MT> struct Body {
     // to it, 1.4 times as much and, where few numbers are summed, up to twice as much;
     // 8 x 4096 tokens, 16 heads of 128 bfloat16 136 us instead of 157.)
     static constexpr int score_parts = size == 4 ? 1 : 2, state_parts = score_parts;
+    // Scores are scaled up by 2^48 at most, and the results that they are added to with
+    // them: smaller scores, times values below 2^16, are nothing in a float16 result.
+    static constexpr int kScoreUp = 48;
     using QK = Tile<T, C, DK, threads>;
     using VV = Tile<T, C, DVT, threads>;
     static constexpr int pitch = kChunkBytes + 16;      // of the scores' rows in LDS
@@ -605,6 +618,17 @@ template <typename T, int DK, int DVT, int MT> struct Body {
                 return most * fabsf(w.s2);
             };
             up = range_scale(largest(), 0x1p-3f, 0x1p14f, largest);
+            if (up > 1.0f) {    // the state is scaled with them
+                float most = 0.0f;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            most = fmaxf(most, finite_size(S[t][m][r]));
+                up = fminf(up, room_above(most));
+            }
         }
         const float keep = a_n * up, s2 = w.s2 * up;
         const table late_pw = pw + (1 - w.late);        // a^(C - 1 - j + late) for row j
@@ -705,7 +729,7 @@ template <typename T, int DK, int DVT, int MT> struct Body {
                     for (int r = 0; r < 4; ++r)
                         m = fmaxf(m, finite_size(v[t][r]));
                 return m;
-            });
+            }, kScoreUp);
 #pragma unroll
         for (int t = 0; t < JT; ++t) {
             if constexpr (is_f16)

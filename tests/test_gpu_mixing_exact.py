@@ -98,3 +98,27 @@ def test_large_float16_values_leave_their_neighbours_exact(torch, large, D):    
     args = [_gpu(torch, t[None], "float16") for t in (q, k, v)]
     y, _ = dw.linear_attention(*args, _gpu(torch, g), scale=scale * 2.0 ** 6)
     _same(y, want, "float16", "y of large scores")
+
+
+def test_float16_beside_a_large_state(torch):   # noqa: F811
+    """Values and scores far below the state that they are added to: scaling them up does
+    not take the state beyond float32."""
+    D, n = 64, 130
+    rng = np.random.default_rng(6)
+    g, one = _gpu(torch, np.zeros(1)), np.ones((1, n, 1, D))
+    # a state of 2^116 or 0, to which each token's product adds 2^-20
+    h0 = exact.whole(rng, (1, 1, D, D), 100, 2.0 ** 110)
+    q, k, v = (_gpu(torch, one * x, "float16") for x in (1.0, 1.0, 2.0 ** -20))
+    _, hT = dw.linear_attention(q, k, v, g, h0=_gpu(torch, h0), scale=2.0 ** -120)
+    _same(hT, (h0 + n * 2.0 ** -20).astype(np.float32).astype(np.float64), "float32", "hT")
+    # and its cotangent, where the scale makes what is added 2^-130: the state, 2^27 at
+    # most, has room for a factor of 2^72, so that 2^-25 of that is lost of a token
+    dhT = exact.whole(rng, (1, 1, D, D), 100, 2.0 ** 20)
+    dh0 = dw.linear_attention_grad(v, q, k, v, g, h0=_gpu(torch, h0), dhT=_gpu(torch, dhT),
+                                   scale=2.0 ** -110)[3]
+    _near(dh0, dhT + n * 2.0 ** -130, 2.0 ** -24 * np.abs(dhT) + n * 2.0 ** (-25 - 72), "dh0")
+    # results of a large state beside scores of 2^-122: 7 * 64 * 2^6 in each
+    q, k, v = (_gpu(torch, one * x, "float16") for x in (7.0, 2.0 ** -11, 1.0))
+    h0 = np.full((1, 1, D, D), 2.0 ** 126)
+    y, _ = dw.linear_attention(q, k, v, g, h0=_gpu(torch, h0), scale=2.0 ** -120)
+    _same(y, np.full((1, n, 1, D), 28672.0), "float16", "y")
