@@ -58,8 +58,8 @@ struct Walk {
     void *out;                          // nullptr: only the state is wanted
     const float *log_decay, *state0;    // state0 nullptr: zero
     float *state1;                      // nullptr: not kept
-    float *slots;                       // states that segments start from, [item][H][Dk][Dv]
-    bool ready;                         // slots are another walk's, and [item][H][Dv][Dk]
+    float *slots;                       // states that segments start from, [slot][H][Dk][Dv]
+    bool ready;                         // slots are another walk's, and [slot][H][Dv][Dk]
     long long ldq, ldk, ldv, ldo;
     int gq, gk, gv;                     // heads that share one of the tensor's
     int H, Dk, Dv;
@@ -203,6 +203,14 @@ __device__ __forceinline__ float log_decay_of(const float *p, int h)
 {
     const float g = p[h];
     return g != g ? g : fmaxf(fminf(g, 0.0f), -1e4f);
+}
+
+// The slot of segment `seg` of a sequence that begins with row0; segment 0 has none.  A
+// sequence's last one is at most (row after it - 1) / segment - 1, before the next one's
+// first: rows alone say how many there are.
+__device__ __forceinline__ int slot_of(const Walk &w, int row0, int seg)
+{
+    return row0 / w.segment + seg - 1;
 }
 
 // Element [dk][dv] of a state array that is [Dk][Dv], or flipped.
@@ -1104,8 +1112,8 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_sta
             step(odd);
     }
     b.next_chunk();
-    b.store_state(w, w.slots + ((long long)(part.item + 1) * w.H + part.h) * w.Dk * w.Dv, false,
-                  part.dv0);
+    const int slot = slot_of(w, at.row0, at.seg + 1);
+    b.store_state(w, w.slots + ((long long)slot * w.H + part.h) * w.Dk * w.Dv, false, part.dv0);
 }
 
 // The segments' own states, each to be added to what it gets from those before it.  A
@@ -1125,10 +1133,9 @@ __global__ __launch_bounds__(256) void k_link(Walks all, int blocks)
     const int h = id / blocks % w.H, seq = id / blocks / w.H;
     if (at >= size)
         return;
-    // (from the sequence itself: offsets that break the rules might lead an item's
-    // search to another one, with more slots than there are from here on)
+    // (from the sequence itself, which offsets that break the rules leave within the rows
+    // and so within the slots)
     const int row0 = seq_start(w.batch, seq), end = seq_start(w.batch, seq + 1);
-    const int first = w.batch.off ? row0 / w.segment + seq : seq * w.per_seq;
     const int count = Item::count(w, max(end - row0, 0));
     if (count == 1)
         return;
@@ -1140,17 +1147,17 @@ __global__ __launch_bounds__(256) void k_link(Walks all, int blocks)
         for (int e = 0; e < V; ++e)
             run[e] = w.state0[((long long)seq * w.H + h) * size +
                               state_at(w, w.flip, (at + e) / w.Dv, (at + e) % w.Dv)];
-    float *slot = w.slots + ((long long)first * w.H + h) * size + at;
+    float *slot = w.slots + ((long long)slot_of(w, row0, 1) * w.H + h) * size + at;
     const long long next = (long long)w.H * size;
     constexpr int kAhead = 4;
-    for (int j = 1; j < count; j += kAhead) {
+    for (int j = 0; j < count - 1; j += kAhead) {
         float v[kAhead][V];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            load<float, V>(slot + min(j + u, count - 1) * next, v[u]);
+            load<float, V>(slot + min(j + u, count - 2) * next, v[u]);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (j + u < count) {
+            if (j + u < count - 1) {
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     run[e] = a * run[e] + v[u][e];
@@ -1181,7 +1188,8 @@ __global__ __launch_bounds__(DVT / MT * 4, waves_a_simd(DK, DVT, MT)) void k_wal
     B b((typename B::table)powers, ld);
     const long long size = (long long)w.Dk * w.Dv;
     const long long own = ((long long)at.seq * w.H + part.h) * size;
-    const float *from = at.seg ? w.slots + ((long long)part.item * w.H + part.h) * size
+    const long long slot = slot_of(w, at.row0, at.seg);
+    const float *from = at.seg ? w.slots + (slot * w.H + part.h) * size
                                : w.state0 ? w.state0 + own : nullptr;
     b.load_state(w, from, at.seg ? w.ready : w.flip, part.dv0);
     const int t0 = at.seg * w.segment, n = min(w.segment, at.length - t0);

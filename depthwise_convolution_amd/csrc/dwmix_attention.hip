@@ -151,7 +151,8 @@ SegmentPlan segment_plan(const Batch &b, bool packed, int H, int Dk, int Dv)
                                    : (long long)b.seqs * p.per_seq;
     p.items = (int)std::min(items, 0x7fffffffLL);
     p.cut = tokens > p.segment;
-    p.slots = p.cut ? 4LL * p.items * H * Dk * Dv : 0;
+    // one for each segment but the first that all rows would be cut into as one sequence
+    p.slots = p.cut ? 4LL * (cdiv(b.rows, p.segment) - 1) * H * Dk * Dv : 0;
     return p;
 }
 

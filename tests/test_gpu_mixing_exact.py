@@ -25,6 +25,8 @@ CASES = [
     ([64], 1, 1, 64, 64), ([1, 0, 63, 200], 2, 1, 64, 64), ([300], 2, 2, 40, 24),
     ([130, 67], 2, 2, 33, 17), ([150], 1, 1, 128, 128), ([90, 40], 1, 1, 160, 72),
     ([300], 4, 2, 16, 80),
+    # many sequences that begin and end next to where the rows are cut
+    ([63, 129, 1, 64, 65, 128, 1, 190, 0, 2, 66, 64, 64, 130, 62], 2, 1, 32, 24),
 ]
 
 

@@ -65,3 +65,20 @@ def test_axes_that_32_bits_do_not_hold_are_refused(monkeypatch):
     for groups in (BIG, -BIG):
         with pytest.raises(ValueError, match="groups"):
             dw.group_norm(x, groups)
+
+
+def test_attention_workspace_counts_rows_and_not_sequences():
+    """Packed: a state for each segment that the rows are cut into, however many sequences
+    they belong to, most of which are shorter than a segment."""
+    heads, state = (16, 16, 128, 128), 4 * 16 * 128 * 128
+    for seqs, rows in ((512, 32768), (1000, 64000), (16384, 65536), (65536, 65536)):
+        for grad in (False, True):
+            n = [dw.dwconv_attention_workspace_size(grad, torch.bfloat16, s, rows, True, *heads)
+                 for s in (1, seqs)]
+            assert n[0] == n[1]
+            # a segment is at least 64 rows of 32 KB, beside which a state has 1 MB; the
+            # gradient keeps two sets
+            assert 0 < n[1] <= (2 if grad else 1) * state * (rows // 256), (seqs, rows, grad)
+    # dense ones alike
+    n = dw.dwconv_attention_workspace_size(False, torch.bfloat16, 3, 1000, False, 1, 1, 64, 64)
+    assert n == 4 * 64 * 64 * (-(-3000 // 64) - 1)
