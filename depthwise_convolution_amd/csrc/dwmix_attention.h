@@ -930,7 +930,9 @@ template <typename T, int DK, int DVT, int MT> struct Body {
     }
     // (A thread reads what it will write of the next V itself.)  The results are stored
     // past the caches, which keep the inputs that other passes read: 8 x 4096 tokens, 16
-    // heads of 128 bfloat16 149 us for 160, gradients of 8 x 2048 78 for 84 a walk.
+    // heads of 128 bfloat16 149 us for 160, gradients of 8 x 2048 78 for 84 a walk.  With a
+    // kernel behind it that reads the results 275 us for 280, 2 x 4096 tokens 100 for 102, 1 x
+    // 512 25.9 for 25.6 (it then waits for HBM by itself).
     static constexpr int kPast = 2;     // the "nt" bit of a store
     __device__ __forceinline__ void store_rows(lds_ptr v, const Walk &w, long long row0, int t,
                                                int first, int h, int dv0) const

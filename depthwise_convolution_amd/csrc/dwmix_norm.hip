@@ -10,9 +10,10 @@
 //   each range of rows, the mean and the sum of squares around it; the ranges' are
 //   joined (counts, means, squares: no difference of large sums), and a second pass
 //   normalises, over the ranges in the opposite order, so that it begins with what
-//   the caches (256 MB before HBM) still hold.  It reads and writes past them: results
-//   that wait there to be written would drive x out, and slow down who reads next (1 x
-//   512 x 512 x 256 float32: first pass 51 us for 77, second 81 for 84).
+//   the caches (256 MB before HBM) still hold.  It writes past them: results that
+//   wait there to be written would drive x out, and slow down who reads next (1 x 512 x
+//   512 x 256 float32: first pass 51 us for 77, second 81 for 84; with a kernel behind
+//   it that reads the results, 280 us for 293, 8 x 56 x 56 x 128 24.5 for 24.9).
 //
 // Gradients need two sums over a group, sum(g) and sum(g * xhat), and per channel
 // sum(dz) and sum(dz * xhat), whose w-weighted sums over a group's channels are the
@@ -63,7 +64,7 @@ bool rows_plan(int size, long long N, long long P, int C, int groups, RowsPlan *
     p->threads = (int)cdiv(L * p->gw * p->slots, 64) * 64;
     // Four vectors a lane in flight, which also share w and b, where that leaves two
     // workgroups for every CU (16384 rows of 2048 bfloat16, 16 groups: 31 us with 4
-    // rows a team, 36.5 us with 1).
+    // rows a team, 36.5 us with 1; 27.5 with x read through the caches).
     p->R = std::max(1, 4 / p->K);
     if (cdiv(N, (long long)p->slots * p->R) * p->windows < 512)
         p->R = 1;
@@ -138,7 +139,9 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs a, RowsPlan p)
             const int c = (at.lane + k * p.L) * V;
             r[j][k].clear();
             if (c < cg)
-                r[j][k].load_past(static_cast<const T *>(a.x) + row(j) * a.ldx + c0 + c);
+                r[j][k].load(static_cast<const T *>(a.x) + row(j) * a.ldx + c0 + c);
+            // (through the caches, where a residual finds x again: 16384 rows of 2048
+            // bfloat16 27.5 us for 29.0, with a sum of x and y behind it 60.6 for 66.3)
         }
     constexpr bool kEarly = K <= 2;     // w and b wait in registers
     float w[kEarly ? K : 1][V], b[kEarly ? K : 1][V];
@@ -385,6 +388,7 @@ struct RangePlan {
     int V, tx, ty, cols, chunk, chunks; // column blocks; rows of a range, ranges
     int span;                           // column blocks that a group lies in, at most
     bool joined;                        // the second pass joins the ranges by itself
+    bool past;                          // it reads past the caches
     long long total;                    // workgroups
 };
 
@@ -414,6 +418,11 @@ RangePlan range_plan(int size, bool grad, long long N, long long P, int C, int g
     p.chunk = (int)std::min(cdiv(cdiv(P, chunks), unit) * unit, P);
     p.chunks = (int)cdiv(P, p.chunk);
     p.total = N * p.chunks * p.cols;
+    // An x that fills the caches by itself is read for the last time past them (268 MB:
+    // 137 us for 141, 280 for 282 with a sum of x and y behind it); a smaller one is left
+    // there for who reads it next, a residual or the gradient (op and sum: 201 MB 204 us for
+    // 212, 67 MB 72 for 79, 13 MB 24.3 for 25.6; the op alone within 5 % either way).
+    p.past = (long long)size * N * P >= (256LL << 20) / C;
     return p;
 }
 
@@ -462,13 +471,18 @@ template <typename T, int V, int B> struct Rows {
     __device__ __forceinline__ void load(const T *x, long long ld, int r, const RangePlan &p,
                                          int rows)
     {
+        const auto from = [&](int k) { return x + min(r + k * p.ty, rows - 1) * ld; };
+        if (LAST && p.past) {
+            // (the compiler would make one load of the two, without the hint)
+            asm volatile("" ::: "memory");
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const T *from = x + min(r + k * p.ty, rows - 1) * ld;
-            if constexpr (LAST)
-                v[k].load_past(from);
-            else
-                v[k].load(from);
+            for (int k = 0; k < B; ++k)
+                v[k].load_past(from(k));
+            asm volatile("" ::: "memory");
+        } else {
+#pragma unroll
+            for (int k = 0; k < B; ++k)
+                v[k].load(from(k));
         }
     }
 };
