@@ -14,6 +14,14 @@ def torch():
     return t
 
 
+@pytest.fixture(autouse=True)
+def _free():
+    yield
+    import torch as t
+    if t.cuda.is_available():
+        t.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_quantize_the_longest_row(torch, dtype):
     """A row of 2^31 - 1 elements: its last ones, which fill no vector, lie less than a
@@ -76,3 +84,92 @@ def test_norm_of_more_than_2_30_channels(torch, P):
 def test_norm_of_the_most_channels(torch, P):
     """A gradient takes as many workgroups as it needs, and not one for each channel."""
     _norm_of_wide_rows(torch, P, dw.SEQ_MAX_ROWS)
+
+
+TOP = dw.SEQ_MAX_ROWS
+PIECE = 1 << 27
+
+
+def _pieces():
+    return ((lo, min(lo + PIECE, TOP)) for lo in range(0, TOP, PIECE))
+
+
+def _whole(torch, *shape):
+    """Whole numbers from -3 to 3 in float16."""
+    return torch.randint(-3, 4, shape, device="cuda", dtype=torch.int8).half()
+
+
+def test_attention_of_the_most_rows(torch):
+    """One sequence, and as many as rows: a head that forgets everything at once, so that
+    each token stands for itself."""
+    print(f"\n[case] linear_attention, one sequence of {TOP} tokens", flush=True)
+    torch.manual_seed(1)
+    q, k, v, dy = (_whole(torch, 1, TOP, 1, 1) for _ in range(4))
+    g = torch.tensor([float("-inf")], device="cuda")
+    y, hT = dw.linear_attention(q, k, v, g, scale=1.0)
+    torch.cuda.synchronize()
+    for lo, hi in _pieces():
+        assert torch.equal(y[0, lo:hi], q[0, lo:hi] * k[0, lo:hi] * v[0, lo:hi]), lo
+    assert hT.item() == (k[0, -1] * v[0, -1]).item()
+    del y
+    print("[case] its gradient", flush=True)
+    dq, dk, dv, _ = dw.linear_attention_grad(dy, q, k, v, g, scale=1.0)
+    torch.cuda.synchronize()
+    for lo, hi in _pieces():
+        a, b, c, d = (t[0, lo:hi] for t in (q, k, v, dy))
+        assert torch.equal(dq[0, lo:hi], b * c * d), lo
+        assert torch.equal(dk[0, lo:hi], c * d * a), lo
+        assert torch.equal(dv[0, lo:hi], b * a * d), lo
+    del dq, dk, dv
+    print("[case] a token for each sequence", flush=True)
+    h = torch.ones(TOP, 1, 1, 1, device="cuda")
+    g = torch.zeros(1, device="cuda")
+    y = dw.linear_attention_step(q[0], k[0], v[0], g, h, scale=1.0)
+    torch.cuda.synchronize()
+    for lo, hi in _pieces():
+        state = 1 + k[0, lo:hi] * v[0, lo:hi]
+        assert torch.equal(y[lo:hi], q[0, lo:hi] * state), lo
+        assert torch.equal(h[lo:hi, 0], state.float()), lo
+
+
+def test_norm_of_the_most_rows(torch):
+    print(f"\n[case] group_norm of {TOP} tokens", flush=True)
+    torch.manual_seed(2)
+    x, dy = _whole(torch, TOP, 2), _whole(torch, TOP, 2)
+    y, stats = dw.group_norm(x, 1, save_stats=True)
+    dx, gw, gb = dw.group_norm_grad(dy, x, stats, 1)
+    torch.cuda.synchronize()
+    total = torch.zeros(2, dtype=torch.float64, device="cuda")
+    for lo, hi in _pieces():
+        a, d = x[lo:hi].double(), dy[lo:hi].double()
+        half = (a[:, :1] - a[:, 1:]) / 2        # from the mean
+        rstd = 1 / (half * half + 1e-5).sqrt()
+        xh = torch.cat([half * rstd, -half * rstd], 1)
+        want = rstd * (d - d.mean(1, True) - xh * (d * xh).mean(1, True))
+        assert ((y[lo:hi].double() - xh).abs() <= 2.0 ** -10).all(), lo
+        # where the two are equal rstd is 316 and half the difference of dy is its factor
+        assert ((dx[lo:hi].double() - want).abs() <= 2.0 ** -10 * (want.abs() + 0.1)).all(), lo
+        total += d.sum(0)
+    # whole numbers of either sign: partial sums stay below 2^24, where float32 is exact
+    assert torch.equal(gb.double(), total)
+
+
+def test_products_of_the_most_rows(torch):
+    print(f"\n[case] quantize_rows and linear_i8 of {TOP} rows", flush=True)
+    torch.manual_seed(3)
+    x = _whole(torch, TOP, 2)
+    x[:, 0] = 127.0
+    q, s = dw.quantize_rows(x)
+    torch.cuda.synchronize()
+    w = torch.tensor([[1, 2]], dtype=torch.int8, device="cuda")
+    one = torch.ones(1, device="cuda")
+    y = dw.linear_i8(q, w, one, x_scale=s, dtype=torch.float16)
+    torch.cuda.synchronize()
+    for lo, hi in _pieces():
+        assert torch.equal(q[lo:hi], x[lo:hi].to(torch.int8)) and (s[lo:hi] == 1.0).all(), lo
+        assert torch.equal(y[lo:hi, 0], x[lo:hi, 0] + 2 * x[lo:hi, 1]), lo
+    del y
+    y = dw.linear_i8(x, w, one)
+    torch.cuda.synchronize()
+    for lo, hi in _pieces():
+        assert torch.equal(y[lo:hi, 0], x[lo:hi, 0] + 2 * x[lo:hi, 1]), lo
