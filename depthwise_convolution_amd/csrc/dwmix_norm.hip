@@ -388,12 +388,15 @@ struct RangePlan {
     int V, tx, ty, cols, chunk, chunks; // column blocks; rows of a range, ranges
     int span;                           // column blocks that a group lies in, at most
     bool joined;                        // the second pass joins the ranges by itself
+    bool means;                         // ... or (gradient) adds up a group's channels
     bool past;                          // it reads past the caches
     long long total;                    // workgroups
 };
 
 constexpr int kAtOnce = 8;      // rows that a thread loads at a time
 constexpr int kJoin = 64;       // ranges that each workgroup of the second pass may join
+constexpr int kJoinMost = 512;  // and parts of a group in all
+constexpr int kMeansMost = 512; // channels of a group that it may add up
 
 // Ranges are whole batches of all threads (32 KB of x in 16-byte vectors), as many as
 // make 2048 workgroups at most.
@@ -415,6 +418,13 @@ RangePlan range_plan(int size, bool grad, long long N, long long P, int C, int g
     p.joined = !grad && chunks <= 2 * kJoin;
     if (p.joined)
         chunks = std::min(chunks, (long long)kJoin);
+    // Each of a group's workgroups reads all of its parts, or sums, again: as many reads as the
+    // square of the group's width.  More parts than a wave has under way at once are left to
+    // a launch of their own, and so are a gradient's sums of more than 512 channels, where
+    // that costs nothing (4 x 64 x 64 bfloat16, gradient: 512 channels 27.4 us for 27.4, 1024
+    // 39.6 for 43.1; 512 x 32768 151 for 1346).
+    p.joined = p.joined && chunks * p.span <= kJoinMost;
+    p.means = !grad || cg <= kMeansMost;
     p.chunk = (int)std::min(cdiv(cdiv(P, chunks), unit) * unit, P);
     p.chunks = (int)cdiv(P, p.chunk);
     p.total = N * p.chunks * p.cols;
@@ -788,6 +798,38 @@ __global__ __launch_bounds__(1024) void k_range_fold(const float *part, int chun
     }
 }
 
+// The means of a gradient of each group of each instance, a workgroup each.  (In 64 bits, as
+// a thread may add up a great many.)
+__global__ __launch_bounds__(256) void k_range_means(NormArgs a, const float *sums, float2 *means)
+{
+    __shared__ double2 of[4];
+    const long long id = block_id();
+    if (id >= a.N * a.groups)
+        return;
+    const int cg = a.C / a.groups, g = (int)(id % a.groups);
+    const float *dw = sums + id / a.groups * 2 * a.C + (long long)g * cg, *db = dw + a.C;
+    const float *w = a.w ? a.w + (long long)g * cg : nullptr;
+    double s1 = 0.0, s2 = 0.0;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < cg; c += 256) {
+        const double f = w ? w[c] : 1.0f;
+        s1 += f * db[c];
+        s2 += f * dw[c];
+    }
+    for (int d = 1; d < 64; d *= 2) {
+        s1 += __shfl_xor(s1, d);
+        s2 += __shfl_xor(s2, d);
+    }
+    if ((threadIdx.x & 63) == 0)
+        of[threadIdx.x >> 6] = make_double2(s1, s2);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const double all = (double)a.P * cg;
+        means[id] = make_float2((float)(((of[0].x + of[1].x) + (of[2].x + of[3].x)) / all),
+                                (float)(((of[0].y + of[1].y) + (of[2].y + of[3].y)) / all));
+    }
+}
+
 // dw and db of 64 of the 2 C columns from the instances' sums.
 constexpr int kInstances = 64;
 
@@ -810,9 +852,11 @@ __device__ __forceinline__ void add_instances(const NormArgs &a, const float *su
             lds[threadIdx.x + 192];
 }
 
-// Gradient, second pass: dx, with the groups' means from their channels' sums.
+// Gradient, second pass: dx, with the groups' means from their channels' sums (means:
+// all groups', or nullptr where they are added up here).
 template <typename T, int V>
-__global__ __launch_bounds__(256) void k_range_dx(NormArgs a, RangePlan p, const float *sums)
+__global__ __launch_bounds__(256) void k_range_dx(NormArgs a, RangePlan p, const float *sums,
+                                                  const float2 *means)
 {
     __shared__ float2 of[256 * V];
     if (block_id() >= p.total) {
@@ -829,7 +873,10 @@ __global__ __launch_bounds__(256) void k_range_dx(NormArgs a, RangePlan p, const
     Rows<T, V, B> rx, rd;
     rx.template load<true>(x, a.ldx, at.y, p, at.rows);
     rd.template load<true>(dy, a.lddy, at.y, p, at.rows);
-    {
+    if (means) {
+        for (int g = threadIdx.x; g < touched; g += 256)
+            of[g] = means[(long long)at.n * a.groups + g0 + g];
+    } else {
         const int lanes = join_lanes(touched), lane = threadIdx.x % lanes;
         const float *dw = sums + (long long)at.n * 2 * a.C, *db = dw + a.C;
         const float all = (float)a.P * (float)cg;
@@ -893,7 +940,7 @@ long long round16(long long bytes) { return cdiv(bytes, 16) * 16; }
 
 // The parts of a workspace.
 struct Space {
-    long long part, sums, strips, total;
+    long long part, sums, strips, means, total;
 };
 
 Space space_of(bool grad, int size, long long N, long long P, int C, int groups)
@@ -912,9 +959,10 @@ Space space_of(bool grad, int size, long long N, long long P, int C, int groups)
             s.part = round16(8LL * N * p.chunks * C);
             s.sums = p.chunks > 1 ? round16(8LL * N * C) : 0;
             s.strips = N > strip_of(N) ? round16(8LL * kStrips * C) : 0;
+            s.means = p.means ? 0 : round16(8LL * N * groups);
         }
     }
-    s.total = s.part + s.sums + s.strips;
+    s.total = s.part + s.sums + s.strips + s.means;
     return s;
 }
 
@@ -1032,6 +1080,7 @@ int launch_norm_grad(const NormArgs &a, void *stream)
     }
     const RangePlan p = range_plan(size, true, a.N, a.P, a.C, a.groups);
     float *sums = p.chunks > 1 ? reinterpret_cast<float *>(space + s.part) : part;
+    float2 *means = reinterpret_cast<float2 *>(space + s.part + s.sums + s.strips);
     // up to kInstances of them are added up beside dx, more by launches of their own
     const bool beside = a.dx && (a.dw || a.db) && a.N <= kInstances;
     const long long extra = beside ? cdiv(2LL * a.C, 64) : 0;
@@ -1046,9 +1095,13 @@ int launch_norm_grad(const NormArgs &a, void *stream)
                 rc = dwconv::launch_kernel(k_range_fold, grid_of(a.N * cdiv(2LL * a.C, 64)),
                                            dim3(1024), 0, st, (const float *)part, p.chunks, a.C,
                                            a.N, sums);
+            if (rc == DWCONV_OK && a.dx && !p.means)
+                rc = dwconv::launch_kernel(k_range_means, grid_of(a.N * a.groups), dim3(256), 0,
+                                           st, a, (const float *)sums, means);
             if (rc == DWCONV_OK && a.dx)
                 rc = dwconv::launch_kernel(k_range_dx<T, v.value>, grid_of(p.total + extra),
-                                           dim3(256), 0, st, a, p, (const float *)sums);
+                                           dim3(256), 0, st, a, p, (const float *)sums,
+                                           p.means ? nullptr : (const float2 *)means);
             return rc;
         });
     });

@@ -173,3 +173,31 @@ def test_products_of_the_most_rows(torch):
     torch.cuda.synchronize()
     for lo, hi in _pieces():
         assert torch.equal(y[lo:hi, 0], x[lo:hi, 0] + 2 * x[lo:hi, 1]), lo
+
+
+def test_norm_of_one_wide_group(torch):
+    """A group of 2^27 channels: its workgroups do not each read all of its sums again, some
+    2^43 bytes.  Every channel of half of them is 2, of the others -2."""
+    C = 1 << 27
+    x = torch.full((2, 2, C), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[..., C // 2:] = -2.0
+    dy = torch.zeros_like(x)
+    dy[0, :, :C // 4] = 8.0
+    y, stats = dw.group_norm(x, 1, eps=0.0, save_stats=True)
+    dx, gw, gb = dw.group_norm_grad(dy, x, stats, 1)
+    torch.cuda.synchronize()
+    # 2^16 workgroups' parts are joined by 256 threads and their tree: some 270 in a row, each
+    # with two roundings of at most 2 and one of the mean, 270 * 3 * 2^-23 = 1e-4; the
+    # variance alike, so that mean, rstd, and what follows from them by factors of up to 8
+    # are within 1e-3, far below half a step of bfloat16's 1 and 2
+    def near(t, want):
+        return ((t.float() - want).abs() <= 1e-3).all()
+
+    assert torch.equal(y, x / 2)
+    assert near(stats[..., 0], 0.0) and near(stats[..., 1], 0.5)
+    # instance 0: the means of dy and of dy * xhat are 8 / 4; dx = (dy - 2 - 2 xhat) / 2
+    assert near(dx[1], 0.0)
+    for lo, hi, want in ((0, C // 4, 2.0), (C // 4, C // 2, -2.0), (C // 2, C, 0.0)):
+        assert near(dx[0, :, lo:hi], want)
+    assert near(gw[:C // 4] / 16, 1.0) and (gb[:C // 4] == 16).all()
+    assert not gw[C // 4:].any() and not gb[C // 4:].any()

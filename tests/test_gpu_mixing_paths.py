@@ -12,7 +12,9 @@ pytestmark = pytest.mark.gpu
 
 # (shape, groups, act): groups that lie across the columns of two workgroups and more
 WIDE_NORMS = [((2, 5, 20000), 8, "silu"), ((3, 70, 6144), 12, "none"), ((1, 40, 2304), 1, "relu"),
-              ((2, 3, 4098), 6, "silu"), ((1, 9, 8192), 2048, "silu")]
+              ((2, 3, 4098), 6, "silu"), ((1, 9, 8192), 2048, "silu"),
+              # and of more than 512 workgroups
+              ((2, 3, 600000), 1, "silu"), ((2, 1200000), 2, "none"), ((3, 5, 2000), 2, "relu6")]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
