@@ -58,6 +58,23 @@ def build(verbose: bool = False, extra_hipcc=()) -> str:
     return LIB
 
 
+def _kernel_name(demangled):
+    """A kernel's name and template arguments, without namespaces and parameters."""
+    name = demangled
+    for space in ("dwconv::", "dwseq::", "dwmix::"):
+        name = name.replace(space, "")
+    name = name.replace("(anonymous namespace)::", "")
+    for k, mode in enumerate(("ROWS", "PARTS", "ODD")):     # of the attention's walk
+        name = name.replace(f"(Mode){k}", mode)
+    depth = 0
+    for at, c in enumerate(name):
+        depth += (c == "<") - (c == ">")
+        if c == "(" and depth == 0:
+            name = name[:at]
+            break
+    return name.replace("half", "_Float16").replace("__int128", "__bf16")
+
+
 def resource_usage():
     """Per-kernel resources of the gfx950 code as the compiler reports them
     (its kernel-resource-usage remarks): {demangled name: {"VGPRs", "SGPRs",
@@ -89,10 +106,7 @@ def resource_usage():
     names = [n.replace("DF16_", "Dh").replace("DF16b", "n") for n in out]
     dem = subprocess.run(["c++filt"], input="\n".join(names), capture_output=True, text=True,
                          check=True).stdout.split("\n")
-    return {d.replace("dwconv::(anonymous namespace)::", "")
-            .replace("dwseq::(anonymous namespace)::", "").replace("half", "_Float16")
-            .replace("__int128", "__bf16"): v
-            for d, v in zip(dem, out.values())}
+    return {_kernel_name(d): v for d, v in zip(dem, out.values())}
 
 
 if __name__ == "__main__":
@@ -103,7 +117,7 @@ if __name__ == "__main__":
               "waves / SIMD |\n|---|---|---|---|---|---|")
         for k in sorted(res):
             v = res[k]
-            print(f"| `{k.split('(')[0]}` | {v.get('VGPRs')} | {v.get('SGPRs')} | {v.get('LDS')} | "
+            print(f"| `{k}` | {v.get('VGPRs')} | {v.get('SGPRs')} | {v.get('LDS')} | "
                   f"{v.get('scratch')} | {v.get('occupancy')} |")
     else:
         print(build(verbose=True))
