@@ -124,6 +124,11 @@ __global__ __launch_bounds__(256) void k_shared(Shared k, Shared v, int rows, in
 // whose lengths are not known here, into half as long parts, which are shared out more
 // evenly (20011 tokens in 37 sequences, 12 heads of 96 and 80 float16: 163 us in all
 // against 173; equal lengths lose by it: 8 x 4096, 16 heads of 128, 257 against 218).
+// Two workgroups a CU is what the walk has room for with 128 x 128 tiles of 16-bit types, 71
+// KB of LDS each.  Widths above 128 take 80 to 96 KB, one a CU (8 x 4096, 16 heads of 256
+// bfloat16 867 us, 5.1 times the floor, where 128 has 2.7), tiles of 64 x 64 31 to 47 KB, three to
+// five, and a gradient's walks share a launch: other numbers of segments have not been
+// measured for these.
 struct SegmentPlan {
     int segment, per_seq, items;
     bool cut;

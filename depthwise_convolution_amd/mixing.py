@@ -301,8 +301,8 @@ def dwconv_norm_fwd(x, groups, w, b, y, eps=1e-5, act="none", stats=None, worksp
 
 def group_norm(x, groups, w=None, b=None, eps=1e-5, act="none", save_stats=False, stream=None):
     """y = act((x - mean) * rstd * w + b), or (y, stats) with save_stats: x (N, ...,
-    C) normalised over the positions and the C / groups adjacent channels of each
-    group of each of the N instances.  A tensor of tokens, (tokens, C), is
+    C) normalised over the positions (one at least) and the C / groups adjacent channels of
+    each group of each of the N instances.  A tensor of tokens, (tokens, C), is
     normalised token by token.  w and b are (C,) float32; stats (N, groups, 2)
     float32, mean and rstd, is what group_norm_grad needs."""
     _, st, ctx = _start(x, stream)
@@ -371,7 +371,8 @@ def dwconv_quantize_rows(x, q, scale, stream=None):
 
 def quantize_rows(x, stream=None):
     """(q, scale): the rows of x (..., K) as int8 numbers (..., K) and float32
-    scales (...), scale = max |x| / 127 and q = x / scale, rounded to the nearest
+    scales (...), scale = max |x| * (1 / 127), factor and product rounded to float32 (up to
+    one unit in the last place from max |x| / 127), and q = x / scale, rounded to the nearest
     integer.  A row that is not finite has the scale NaN and numbers of 0."""
     _, st, ctx = _start(x, stream)
     if ctx is not None:

@@ -38,7 +38,8 @@ extern "C" {
  * the values or of the state and 16 rows of scores by one: besides the two numbers'
  * 2^-22 of itself, a number then loses at most 2^-25 while the largest of those beside
  * it is below 2^14, and 2^-38 of that one where it is above.
- * A token's infinities and NaN reach the tokens after it, never those before it.
+ * A token's infinities and NaN reach the tokens after it, never those before it; an
+ * infinity of q or k may reach results of a 16-bit type as NaN.
  * workspace: at least dwconv_attention_workspace_size(grad = 0) bytes, 16-byte
  * aligned (NULL where that is 0). */
 #define DWCONV_ATTENTION_MAX_DIM 256
@@ -80,8 +81,8 @@ int dwconv_attention_grad(const void *dy, long long lddy, const void *q, long lo
 
 /* ---- group normalisation with an activation, channels last ------------------
  *
- * x is N instances of P positions of C channels: row n * P + p holds position p of
- * instance n.  A group is C / groups adjacent channels of one instance;
+ * x is N instances of P positions (at least one) of C channels: row n * P + p holds
+ * position p of instance n.  A group is C / groups adjacent channels of one instance;
  *
  *   y = act((x - mean) * rstd * w[c] + b[c]),    rstd = 1 / sqrt(var + eps)
  *
