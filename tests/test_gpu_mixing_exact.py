@@ -124,3 +124,28 @@ def test_float16_beside_a_large_state(torch):   # noqa: F811
     h0 = np.full((1, 1, D, D), 2.0 ** 126)
     y, _ = dw.linear_attention(q, k, v, g, h0=_gpu(torch, h0), scale=2.0 ** -120)
     _same(y, np.full((1, n, 1, D), 28672.0), "float16", "y")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", [3, 6, 7])
+def test_gradients_that_are_left_out(torch, case, dtype):   # noqa: F811
+    """Every choice among dq, dk, dv and dh0, in sequences that are cut: the states of one
+    walk serve another only where both are wanted."""
+    print(f"\n[case] some gradients {CASES[case]} {dtype}", flush=True)
+    g, r, logs, bounds = _inputs(torch, CASES[case], dtype)
+    scale = 2.0 ** -6
+    want = ref.attention_grad(r["dy"], r["q"], r["k"], r["v"], logs, scale, bounds, r["h0"],
+                              r["dhT"])
+    lengths, H, KV, Dk, Dv = CASES[case]
+    n = dw.dwconv_attention_workspace_size(True, g["q"].dtype, len(lengths), sum(lengths), True, H,
+                                           KV, Dk, Dv)
+    for chosen in range(16):
+        space = torch.full((n,), 255, dtype=torch.uint8, device="cuda") if n else None
+        out = [torch.full_like(g[x], float("nan")) if chosen >> b & 1 else None
+               for b, x in enumerate(("q", "k", "v", "h0"))]
+        dw.dwconv_attention_grad(g["dy"], g["q"], g["k"], g["v"], g["log_decay"], *out,
+                                 workspace=space, scale=scale, h0=g["h0"], dhT=g["dhT"],
+                                 offsets=g["off"])
+        for name, t in zip(("dq", "dk", "dv", "dh0"), out):
+            if t is not None:
+                _same(t, want[name], "float32" if name == "dh0" else dtype, (name, chosen))

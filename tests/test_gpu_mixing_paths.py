@@ -118,3 +118,37 @@ def test_group_norm_of_many_ranges(torch, monkeypatch, case, dtype):      # noqa
     space = torch.empty(n, dtype=torch.uint8, device="cuda")
     dw.dwconv_norm_fwd(x, groups, w, b, x, act=act, workspace=space)
     assert torch.equal(x, want)
+
+
+def _filled(torch, n, value):        # noqa: F811
+    return torch.full((n,), value, dtype=torch.uint8, device="cuda") if n else None
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_what_a_workspace_held_before_does_not_matter(torch, dtype):     # noqa: F811
+    kind = getattr(torch, dtype)
+    for shape, groups in ((s[0], s[1]) for s in WIDE_NORMS + JOINED_NORMS):
+        N, C = shape[0], shape[-1]
+        x, dy = (torch.randn(shape, device="cuda").to(kind) for _ in range(2))
+        P = x.numel() // N // C
+        sizes = [dw.dwconv_norm_workspace_size(g, kind, N, P, C, groups) for g in (False, True)]
+        got = []
+        for value in (0, 255):
+            y, dx = torch.empty_like(x), torch.empty_like(x)
+            stats = torch.empty(N, groups, 2, device="cuda")
+            gw, gb = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+            dw.dwconv_norm_fwd(x, groups, None, None, y, act="silu", stats=stats,
+                               workspace=_filled(torch, sizes[0], value))
+            dw.dwconv_norm_grad(dy, x, stats, groups, None, None, dx, gw, gb, act="silu",
+                                workspace=_filled(torch, sizes[1], value))
+            got.append((y, stats, dx, gw, gb))
+        assert all(torch.equal(a, b) for a, b in zip(*got)), (shape, groups)
+    for M, N, K, *_ in I8_LARGE[:3] + I8_LARGE[10:] + [(8, 256, 512), (40, 100, 8192)]:
+        x = torch.randn(M, K, device="cuda").to(kind)
+        w, s = dw.quantize_rows(torch.randn(N, K, device="cuda"))
+        n = dw.dwconv_linear_i8_workspace_size(kind, kind, M, N, K)
+        got = []
+        for value in (0, 255):
+            y = torch.empty(M, N, dtype=kind, device="cuda")
+            got.append(dw.dwconv_linear_i8(x, w, s, None, y, workspace=_filled(torch, n, value)))
+        assert torch.equal(*got), (M, N, K)
