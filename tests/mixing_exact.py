@@ -64,3 +64,64 @@ def majorants(q, k, v, dy, log_decay, scale, bounds, h0=None, dhT=None):
     y, hT = ref.attention(*a, log_decay, scale, bounds, h0)
     return dict(y=y, hT=hT, **ref.attention_grad(np.abs(dy), *a, log_decay, scale, bounds, h0,
                                                  dhT))
+
+
+# ------------------------------------------------------ float16 with any decay
+UNIT = 2.0 ** -25       # half a step of float16's smallest numbers
+
+
+def _floor_of_walk(q, k, v, a, s1, bounds, back):
+    """What a walk over (q, k, v) loses of numbers that are small for float16, per result
+    (rows, H, Dv): the scores that a result is made of (those of a chunk's 64 tokens at
+    most), each UNIT, times |v|; the elements of the state where it meets q, each UNIT, times
+    s1 |q|; and what the state has lost of v, UNIT a token times |k|, which the decay reaches
+    once the token's chunk has ended.  The numbers that are scaled together stay below 2^14."""
+    out = np.zeros((*q.shape[:2], v.shape[2]))
+    for lo, hi in bounds:
+        rows = range(hi - 1, lo - 1, -1) if back else range(lo, hi)
+        near_v, near_k, far = [], [], np.zeros(k.shape[1:])
+        for t in rows:
+            if len(near_k) == 64:
+                near_v.pop(0)
+                far = a[:, None] * (far + near_k.pop(0))
+            else:
+                far = a[:, None] * far
+            near_v.append(np.abs(v[t]))
+            near_k.append(np.abs(k[t]))
+            lost = 1.0 + far + np.sum(near_k, 0)
+            out[t] = UNIT * (np.sum(near_v, 0) +
+                             s1 * np.einsum("hd,hd->h", np.abs(q[t]), lost)[:, None])
+    return out
+
+
+def float16_floors(r, scale):
+    """dict of y, dq, dk, dv: what float16 loses of each."""
+    group = r["q"].shape[1] // r["k"].shape[1]
+    k, v = (np.repeat(r[n], group, 1) for n in ("k", "v"))
+    q, dy, a, b = r["q"], r["dy"], ref.decay(r["log_decay"]), r["bounds"]
+
+    def shared(x):
+        return x.reshape(len(x), -1, group, x.shape[2]).sum(2)
+
+    return dict(y=_floor_of_walk(q, k, v, a, scale, b, False),
+                dq=_floor_of_walk(dy, v, k, a, scale, b, False),
+                dk=shared(_floor_of_walk(v, dy, q, a, 1.0, b, True)),
+                dv=shared(_floor_of_walk(k, q, dy, a, 1.0, b, True)))
+
+
+def float16_tol(big, sums, tokens, floor):
+    """Error of a float16 result before its store: the float32 arithmetic's, two numbers of
+    22 bits for scores, states and values, and the floor."""
+    return ref.attention_tol(big, sums, tokens, "float32") + 2 * 2.0 ** -22 * big + floor
+
+
+def float16_bounds(r, scale):
+    """{y, dq, dk, dv: (result, error before its store)}."""
+    args = r["q"], r["k"], r["v"], r["log_decay"], scale, r["bounds"], r["h0"]
+    want = dict(ref.attention_grad(r["dy"], *args, r["dhT"]), y=ref.attention(*args)[0])
+    big = majorants(*args[:3], r["dy"], *args[3:], r["dhT"])
+    assert max(np.max(big[n]) for n in ("y", "hT", "dq", "dk", "dv", "dh0")) < 2.0 ** 14
+    floors, tokens = float16_floors(r, scale), max(hi - lo for lo, hi in r["bounds"])
+    width = max(r["k"].shape[2], r["v"].shape[2]) + r["q"].shape[1] // r["k"].shape[1]
+    return {n: (want[n], float16_tol(big[n], width, tokens, floors[n]))
+            for n in ("y", "dq", "dk", "dv")}

@@ -149,3 +149,47 @@ def test_gradients_that_are_left_out(torch, case, dtype):   # noqa: F811
         for name, t in zip(("dq", "dk", "dv", "dh0"), out):
             if t is not None:
                 _same(t, want[name], "float32" if name == "dh0" else dtype, (name, chosen))
+
+
+# ------------------------------------------------------ float16 with any decay
+DECAYS = [
+    # (lengths, H, KV, Dk, Dv)
+    ([200], 4, 4, 8, 8), ([64, 1, 0, 129], 4, 2, 16, 24), ([70, 300], 4, 1, 33, 17),
+    ([150], 4, 4, 64, 64), ([130], 4, 2, 96, 80), ([100], 4, 4, 160, 40),
+]
+
+
+def decay_inputs(case):
+    """float64 arrays of numbers that float16 holds."""
+    lengths, H, KV, Dk, Dv = DECAYS[case]
+    rng = np.random.default_rng(70 + case)
+
+    def some(*shape):
+        return rng.standard_normal(shape).astype(np.float16).astype(np.float64)
+
+    rows, S = sum(lengths), len(lengths)
+    r = dict(q=some(rows, H, Dk), k=some(rows, KV, Dk), v=some(rows, KV, Dv),
+             dy=some(rows, H, Dv), h0=some(S, H, Dk, Dv), dhT=some(S, H, Dk, Dv))
+    r["log_decay"] = np.array([-0.02, -1.0, -8.0, 0.0]).astype(np.float32).astype(np.float64)
+    r["bounds"] = bounds_of(_offsets(lengths))
+    return r, _offsets(lengths), Dk ** -0.5
+
+
+@pytest.mark.parametrize("case", range(len(DECAYS)))
+def test_float16_element_by_element(torch, case):     # noqa: F811
+    """The forward and the gradients within what each element's own terms allow."""
+    lengths, H, KV, Dk, Dv = DECAYS[case]
+    print(f"\n[case] float16 attention {DECAYS[case]}", flush=True)
+    r, offsets, scale = decay_inputs(case)
+    g = {n: _gpu(torch, r[n], "float16") for n in ("q", "k", "v", "dy")}
+    for n in ("h0", "dhT", "log_decay"):
+        g[n] = _gpu(torch, r[n])
+    off = _gpu(torch, offsets, "int32")
+    y, _ = dw.linear_attention(g["q"], g["k"], g["v"], g["log_decay"], h0=g["h0"], offsets=off,
+                               scale=scale)
+    grads = dw.linear_attention_grad(g["dy"], g["q"], g["k"], g["v"], g["log_decay"], h0=g["h0"],
+                                     dhT=g["dhT"], offsets=off, scale=scale)
+    torch.cuda.synchronize()
+    got = dict(zip(("dq", "dk", "dv"), grads), y=y)
+    for name, (want, tol) in exact.float16_bounds(r, scale).items():
+        _near(got[name], want, ref.store_tol(want, tol, "float16"), name)

@@ -5,6 +5,7 @@ import pytest
 
 from . import mixing_exact as exact
 from . import mixing_reference as ref
+from .test_gpu_mixing_exact import DECAYS, decay_inputs
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
@@ -43,3 +44,37 @@ def test_a_dropped_term_shows():
     lost = ref.attention_grad(dy, q, k, one, *args)
     assert (exact.rounded(want["dq"], "float16")[3:] !=
             exact.rounded(lost["dq"], "float16")[3:]).mean() > 0.5
+
+
+def _outside(got, want, tol):
+    return np.abs(exact.rounded(got, "float16") - want) > ref.store_tol(want, tol, "float16")
+
+
+@pytest.mark.parametrize("case", range(len(DECAYS)))
+def test_the_float16_bounds_tell_mistakes_apart(case):
+    """They hold for the exact results, rounded once, and not without one token's term."""
+    r, _, scale = decay_inputs(case)
+    bounds = exact.float16_bounds(r, scale)
+    for name, (want, tol) in bounds.items():
+        assert not _outside(want, want, tol).any(), name
+        # what float16's range costs is small beside the rounding of a typical result
+        floor = exact.float16_floors(r, scale)[name]
+        assert np.median(floor) < 2.0 ** -13 * np.median(np.abs(want)), name
+    t = r["bounds"][0][1] // 2
+    for lost in ("k", "v", "q", "dy"):
+        one = dict(r, **{lost: r[lost].copy()})
+        one[lost][t, 0, 0] = 0.0
+        got = exact.float16_bounds(one, scale)
+        for name, (want, tol) in bounds.items():
+            own = {"q": "dq", "k": "dk", "v": "dv"}.get(lost)
+            if name != own and not (name == "y" and lost == "dy"):
+                assert _outside(got[name][0], want, tol).any(), (lost, name)
+
+
+def test_the_float16_bounds_tell_one_number_apart():
+    r, _, scale = decay_inputs(0)
+    want, tol = exact.float16_bounds(r, scale)["y"]
+    head = 3            # the one that forgets nothing, whose scores are not decayed
+    got = exact.one_number(r["q"][:, head:], r["k"][:, head:], r["v"][:, head:],
+                           r["h0"][0, head:], scale, "float16")
+    assert _outside(got, want[:, head:], tol[:, head:]).mean() > 0.01
