@@ -127,8 +127,7 @@ def _start(x, stream, name="x"):
         raise TypeError(f"{name} has dtype {x.dtype}, expected float32, float16 or bfloat16")
     if type(stream) is _Handle:
         return code, stream, None
-    size = x.numel()
-    if size > _INT_MAX or size == 0:
+    if not 0 < x.numel() <= _INT_MAX:
         _fits(x, name)
     index = x.get_device()
     if stream is None:
